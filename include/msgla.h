@@ -384,6 +384,104 @@ msgla_status msgla_backward_saved(const msgla_config* cfg, const void* packed, c
                                   void* dx, const msgla_grads* grads, void* workspace,
                                   size_t workspace_bytes, void* stream);
 
+/* ==== Sequence operators beside the layer =====================================
+ *
+ * A model of MS-GLA layers needs other mixers of the sequence next to them.
+ * Those below keep the layer's conventions (device pointers, caller-owned
+ * memory, work enqueued on `stream`, argument errors returned synchronously)
+ * and its two storage types; they take no packed weights.
+ */
+
+/* Rows of a tensor [B][L][width] whose elements are contiguous within a row:
+ * row (b, t) starts at data + b * stride_b + t * stride_t elements.  A slice of
+ * a wider tensor (one projection's columns) is such a view.  Strides are not
+ * negative; rows of an output may not overlap one another or an input.  data is
+ * aligned to the element; rows whose starts are all multiples of four elements
+ * take the vector path. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_t;
+} msgla_rows;
+
+/*
+ * Gated linear recurrence: the layer's gate and state with one scalar state per
+ * channel in place of a d_k x d_v matrix per head.  For every sequence and
+ * channel,
+ *     log alpha_t = logsigmoid(z_t + bias) / gate_normalizer
+ *     h_t = alpha_t h_{t-1} + beta_t x_t,      y_t = h_t
+ * with the input's scale beta by `input`: 1 (PLAIN), 1 - alpha (CONVEX: h is a
+ * weighted mean of the inputs), or sqrt(1 - alpha^2) (NORM: keeps the variance
+ * of independent inputs).
+ *   width: channels, 1 .. 65536.  dtype: of x, z, y and their gradients; the
+ *   gate, the state and every sum are fp32, as are bias and the states.
+ */
+typedef enum {
+  MSGLA_RECURRENCE_PLAIN = 0,
+  MSGLA_RECURRENCE_CONVEX = 1,
+  MSGLA_RECURRENCE_NORM = 2
+} msgla_recurrence_input;
+
+typedef struct {
+  int32_t width;
+  int32_t input; /* msgla_recurrence_input */
+  float gate_normalizer;
+  int32_t dtype; /* msgla_dtype */
+} msgla_recurrence_config;
+
+/* Device workspace of msgla_recurrence_forward / _backward for batch B and
+ * length L (bytes; may be 0 for the forward of a short sequence, and then
+ * workspace may be NULL).  (size_t)-1 for an invalid configuration or size. */
+size_t msgla_recurrence_workspace_bytes(const msgla_recurrence_config* cfg, int64_t B, int64_t L);
+size_t msgla_recurrence_backward_workspace_bytes(const msgla_recurrence_config* cfg, int64_t B, int64_t L);
+
+/*
+ * The recurrence over B sequences of L positions.
+ *   x, z [B][L][width] -> y [B][L][width]
+ *   bias [width] fp32, or NULL for 0
+ *   mask: NULL, or [B][L] bytes, nonzero for a token and 0 for padding.  At
+ *         padding the state passes unchanged, y is 0, and what x and z hold
+ *         there has no influence.  Padding may stand anywhere; a sequence may
+ *         hold no token at all.
+ *   h_in: state [B][width] fp32 before the first position, or NULL for 0
+ *   h_out: NULL, or receives the state [B][width] after the last position; may
+ *         be h_in.
+ * B * L is at most 2^28.  The result does not depend on the schedule beyond
+ * rounding and is the same bit for bit from call to call.
+ */
+msgla_status msgla_recurrence_forward(const msgla_recurrence_config* cfg, const msgla_rows* x,
+                                      const msgla_rows* z, const float* bias, const uint8_t* mask,
+                                      const float* h_in, int64_t B, int64_t L, const msgla_rows* y,
+                                      float* h_out, void* workspace, size_t workspace_bytes,
+                                      void* stream);
+
+/*
+ * Its vector-Jacobian product: from dy = dLoss/dy and dh_out = dLoss/dh_out
+ * (NULL for 0; dy may be NULL for 0 when dh_out is given),
+ *     dh_t = dy_t + alpha_{t+1} dh_{t+1}  (+ dh_out at the last position)
+ *     dx_t = beta_t dh_t
+ *     dz_t = dh_t (alpha_t h_{t-1} + (dbeta_t / dlog alpha_t) x_t) sigmoid(-z_t - bias) / gate_normalizer
+ * with 0 for dx, dz and dy at padding (what dy holds there has no influence).
+ * dbias [width] (sum of dz before it is rounded) and dh_in [B][width] are fp32,
+ * overwritten, and may be NULL.  x, z, bias, mask and h_in are the forward's;
+ * the states are computed again.  dh_in may be dh_out.  With NORM, dz is 0
+ * where 1 - alpha^2 is 0 in fp32 (z + bias above about 88), where the formula
+ * has a zero over a zero.
+ */
+msgla_status msgla_recurrence_backward(const msgla_recurrence_config* cfg, const msgla_rows* x,
+                                       const msgla_rows* z, const float* bias, const uint8_t* mask,
+                                       const float* h_in, const msgla_rows* dy, const float* dh_out,
+                                       int64_t B, int64_t L, const msgla_rows* dx,
+                                       const msgla_rows* dz, float* dbias, float* dh_in,
+                                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* One streaming step of B sequences: the recurrence at L = 1 in one launch
+ * without a workspace (stride_t is not read).  mask: NULL or [B].  h_in and
+ * h_out [B][width] fp32 are required and may be the same buffer. */
+msgla_status msgla_recurrence_step(const msgla_recurrence_config* cfg, const msgla_rows* x_t,
+                                   const msgla_rows* z_t, const float* bias, const uint8_t* mask,
+                                   const float* h_in, int64_t B, const msgla_rows* y_t, float* h_out,
+                                   void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,7 +12,7 @@ import ctypes
 import os
 from typing import Optional, Sequence
 
-from .config import BF16, F32, MsglaConfig
+from .config import BF16, F32, MsglaConfig, RECURRENCE_INPUTS, RecurrenceConfig
 
 MAX_BRANCHES = 8
 N_STAGES = 6
@@ -28,6 +28,8 @@ SYMBOLS = (
     "msgla_forward", "msgla_forward_timed", "msgla_decode_workspace_bytes", "msgla_decode_step",
     "msgla_fusion_weights", "msgla_state_query", "msgla_forward_noalloc",
     "msgla_backward_workspace_bytes", "msgla_backward", "msgla_forward_train", "msgla_backward_saved",
+    "msgla_recurrence_workspace_bytes", "msgla_recurrence_backward_workspace_bytes",
+    "msgla_recurrence_forward", "msgla_recurrence_backward", "msgla_recurrence_step",
 )
 NOALLOC_WORKSPACE_BYTES = 192 << 20  # MSGLA_NOALLOC_WORKSPACE_BYTES
 
@@ -80,6 +82,15 @@ class CStateInfo(ctypes.Structure):
                 ("position", ctypes.c_int64)]
 
 
+class CRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64)]
+
+
+class CRecurrenceConfig(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("input", ctypes.c_int32), ("gate_normalizer", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
+
+
 class CStageEvents(ctypes.Structure):
     _fields_ = [("start", ctypes.c_void_p * N_STAGES), ("stop", ctypes.c_void_p * N_STAGES)]
 
@@ -121,6 +132,15 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                 vp, sz, vp]),
         "msgla_forward_train": (ctypes.c_int, [cfgp, vp, vp, vp, i64, i64, vp, vp, sz, vp]),
     }
+    rows, rec = ctypes.POINTER(CRows), ctypes.POINTER(CRecurrenceConfig)
+    sig.update({
+        "msgla_recurrence_workspace_bytes": (sz, [rec, i64, i64]),
+        "msgla_recurrence_backward_workspace_bytes": (sz, [rec, i64, i64]),
+        "msgla_recurrence_forward": (ctypes.c_int, [rec, rows, rows, vp, vp, vp, i64, i64, rows, vp, vp, sz, vp]),
+        "msgla_recurrence_backward": (ctypes.c_int, [rec, rows, rows, vp, vp, vp, rows, vp, i64, i64, rows, rows,
+                                                     vp, vp, vp, sz, vp]),
+        "msgla_recurrence_step": (ctypes.c_int, [rec, rows, rows, vp, vp, vp, i64, rows, vp, vp]),
+    })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -294,3 +314,123 @@ def msgla_forward_noalloc(cfg: MsglaConfig, packed, x, B: int, L: int, out, stat
                                               _ptr(mask), B, L, _ptr(out), _ptr(state_in),
                                               _ptr(state_out), _stream(stream))
     _check("msgla_forward_noalloc", st)
+
+
+# ---- sequence operators beside the layer ----------------------------------------
+# Tensors are checked here against what the C entry points assume of the
+# pointers they get; a ValueError names the argument.
+
+def _storage(cfg):
+    import torch
+    return torch.bfloat16 if cfg.dtype == BF16 else torch.float32
+
+
+def _tensor(name: str, t, shape, dtype, device, contiguous=False):
+    """t itself, on `device` (given as a tensor's), of this shape and type, its last dimension dense."""
+    if t.device != device or t.device.type != "cuda":
+        raise ValueError(f"{name} must be on {device}, a ROCm device: it is on {t.device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}: it is {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}: it has {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be dense")
+    return t
+
+
+def _f32(name: str, t, shape, device):
+    import torch
+    return None if t is None else _tensor(name, t, shape, torch.float32, device, contiguous=True)
+
+
+def _apart(name: str, t):
+    """An output whose rows do not overlap (no broadcast dimension of more than one entry)."""
+    size = 1
+    for n, s in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1), key=lambda p: p[1]):
+        if s < size:
+            raise ValueError(f"the rows of {name} overlap")
+        size = s * (n - 1) + size
+    return t
+
+
+def _rows(t) -> CRows:
+    """[B, L, width], or [B, width] as rows of one position."""
+    return CRows(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0)
+
+
+_REC_CACHE: dict = {}
+
+
+def c_recurrence_config(cfg: RecurrenceConfig) -> CRecurrenceConfig:
+    c = _REC_CACHE.get(cfg)
+    if c is None:
+        c = _REC_CACHE[cfg] = CRecurrenceConfig(cfg.width, RECURRENCE_INPUTS.index(cfg.input), cfg.gate_normalizer,
+                                                1 if cfg.dtype == BF16 else 0)
+    return c
+
+
+def msgla_recurrence_workspace_bytes(cfg: RecurrenceConfig, B: int, L: int) -> int:
+    return load_library().msgla_recurrence_workspace_bytes(ctypes.byref(c_recurrence_config(cfg)), B, L)
+
+
+def msgla_recurrence_backward_workspace_bytes(cfg: RecurrenceConfig, B: int, L: int) -> int:
+    return load_library().msgla_recurrence_backward_workspace_bytes(ctypes.byref(c_recurrence_config(cfg)), B, L)
+
+
+def _recurrence_inputs(cfg, x, z, bias, mask, h_in, dims):
+    import torch
+    if x.dim() != dims:
+        raise ValueError(f"x must have {dims} dimensions: it has {x.dim()}")
+    shape = (*x.shape[:-1], cfg.width)
+    _tensor("x", x, shape, _storage(cfg), x.device)
+    _tensor("z", z, shape, _storage(cfg), x.device)
+    _f32("bias", bias, (cfg.width,), x.device)
+    _f32("h_in", h_in, (shape[0], cfg.width), x.device)
+    if mask is not None:
+        _tensor("mask", mask, shape[:-1], torch.uint8, x.device, contiguous=True)
+    return shape
+
+
+def msgla_recurrence_forward(cfg: RecurrenceConfig, x, z, y, workspace, bias=None, mask=None, h_in=None, h_out=None,
+                             stream=None):
+    """x, z, y: [B, L, width] (any strides with a dense last dimension); bias [width], h_in and h_out
+    [B, width] fp32; mask: [B, L] uint8."""
+    shape = _recurrence_inputs(cfg, x, z, bias, mask, h_in, 3)
+    _apart("y", _tensor("y", y, shape, _storage(cfg), x.device))
+    _f32("h_out", h_out, (shape[0], cfg.width), x.device)
+    st = load_library().msgla_recurrence_forward(
+        ctypes.byref(c_recurrence_config(cfg)), _rows(x), _rows(z), _ptr(bias), _ptr(mask), _ptr(h_in), shape[0],
+        shape[1], _rows(y), _ptr(h_out), _ptr(workspace), 0 if workspace is None else workspace.numel() *
+        workspace.element_size(), _stream(stream))
+    _check("msgla_recurrence_forward", st)
+
+
+def msgla_recurrence_backward(cfg: RecurrenceConfig, x, z, dy, dx, dz, workspace, bias=None, mask=None, h_in=None,
+                              dh_out=None, dbias=None, dh_in=None, stream=None):
+    """dy (or None for 0), dx, dz: as x; dh_out, dh_in: [B, width] fp32; dbias: [width] fp32."""
+    shape = _recurrence_inputs(cfg, x, z, bias, mask, h_in, 3)
+    if dy is not None:
+        _tensor("dy", dy, shape, _storage(cfg), x.device)
+    for name, t in (("dx", dx), ("dz", dz)):
+        _apart(name, _tensor(name, t, shape, _storage(cfg), x.device))
+    _f32("dh_out", dh_out, (shape[0], cfg.width), x.device)
+    _f32("dh_in", dh_in, (shape[0], cfg.width), x.device)
+    _f32("dbias", dbias, (cfg.width,), x.device)
+    st = load_library().msgla_recurrence_backward(
+        ctypes.byref(c_recurrence_config(cfg)), _rows(x), _rows(z), _ptr(bias), _ptr(mask), _ptr(h_in),
+        None if dy is None else _rows(dy), _ptr(dh_out), shape[0], shape[1], _rows(dx), _rows(dz), _ptr(dbias),
+        _ptr(dh_in), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("msgla_recurrence_backward", st)
+
+
+def msgla_recurrence_step(cfg: RecurrenceConfig, x_t, z_t, y_t, h_in, h_out, bias=None, mask=None, stream=None):
+    """x_t, z_t, y_t: [B, width]; h_in, h_out: [B, width] fp32 (may be one tensor); mask: [B] uint8."""
+    shape = _recurrence_inputs(cfg, x_t, z_t, bias, mask, h_in, 2)
+    _apart("y_t", _tensor("y_t", y_t, shape, _storage(cfg), x_t.device))
+    _f32("h_out", h_out, shape, x_t.device)
+    st = load_library().msgla_recurrence_step(
+        ctypes.byref(c_recurrence_config(cfg)), _rows(x_t), _rows(z_t), _ptr(bias), _ptr(mask), _ptr(h_in), shape[0],
+        _rows(y_t), _ptr(h_out), _stream(stream))
+    _check("msgla_recurrence_step", st)

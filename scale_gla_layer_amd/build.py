@@ -35,6 +35,8 @@ SOURCES = [
     "k_backward.hip",
     "k_bwd_gemm.hip",
     "api_backward.cpp",
+    "k_recurrence.hip",
+    "api_recurrence.cpp",
 ]
 
 # rocBLAS: the backward's plain products (weight and input gradients)

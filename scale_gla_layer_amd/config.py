@@ -58,6 +58,30 @@ class MsglaConfig:
         return sum(h * self.d_k * self.d_v for h in self.heads)
 
 
+RECURRENCE_INPUTS = ("plain", "convex", "norm")
+
+
+@dataclasses.dataclass(frozen=True)
+class RecurrenceConfig:
+    """Gated linear recurrence h_t = alpha_t h_{t-1} + beta_t x_t per channel, with
+    log alpha_t = logsigmoid(z_t + bias) / gate_normalizer and beta 1 ("plain"),
+    1 - alpha ("convex") or sqrt(1 - alpha^2) ("norm")."""
+    width: int
+    input: str = "plain"
+    gate_normalizer: float = 16.0
+    dtype: str = BF16
+
+    def __post_init__(self):
+        if not 1 <= self.width <= 65536:
+            raise ValueError("width must be 1 .. 65536")
+        if self.input not in RECURRENCE_INPUTS:
+            raise ValueError(f"input must be one of {RECURRENCE_INPUTS}")
+        if not 0 < self.gate_normalizer <= 3.0e38:
+            raise ValueError("gate_normalizer must be positive and finite")
+        if self.dtype not in (F32, BF16):
+            raise ValueError(f"dtype must be {F32!r} or {BF16!r}")
+
+
 @dataclasses.dataclass(frozen=True)
 class Workload:
     name: str

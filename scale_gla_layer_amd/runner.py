@@ -3,12 +3,13 @@ weights with torch, packs the weights once, owns the workspace, and calls the
 binding.  No arithmetic of the layer happens here."""
 from __future__ import annotations
 
+import contextlib
 from typing import Optional
 
 import numpy as np
 
 from . import binding
-from .config import BF16, MsglaConfig
+from .config import BF16, MsglaConfig, RecurrenceConfig
 from .synth import LayerWeights, storage_array
 
 
@@ -197,6 +198,76 @@ class DecodeGraph:
         self.x.copy_(x_t)
         self.graph.replay()
         return self.out
+
+
+@contextlib.contextmanager
+def _launching_on(t):
+    """Makes t's device the current one, on which the library launches; yields that device's current stream."""
+    torch = _torch()
+    if t.device.type != "cuda":
+        raise ValueError(f"tensors must be on a ROCm device: got one on {t.device}")
+    if t.device.index == torch.cuda.current_device():
+        yield torch.cuda.current_stream().cuda_stream
+        return
+    with torch.cuda.device(t.device):
+        yield torch.cuda.current_stream().cuda_stream
+
+
+def _workspace(n: int, device):
+    """Memory for one call on the current stream, from torch's allocator, which hands it out again in
+    stream order: calls on several streams and captured graphs share none."""
+    return _torch().empty(n, dtype=_torch().uint8, device=device) if n else None
+
+
+class DeviceRecurrence:
+    """The gated linear recurrence on device tensors.  Every call runs on the current stream of its
+    tensors' device, allocates what it returns unless given, and may be captured in a graph."""
+
+    def __init__(self, cfg: RecurrenceConfig):
+        self.cfg = cfg
+
+    def _sizes(self, x, query):
+        if x.dim() != 3:
+            raise ValueError(f"x must be [B, L, width]: it has {x.dim()} dimensions")
+        n = query(self.cfg, x.shape[0], x.shape[1])
+        if n == 2 ** 64 - 1:
+            raise ValueError(f"invalid batch/length B={x.shape[0]} L={x.shape[1]}")
+        return _workspace(n, x.device)
+
+    def forward(self, x, z, bias=None, mask=None, h_in=None, y=None, h_out=None):
+        """x, z [B, L, width] -> (y [B, L, width], state after the last position [B, width] fp32)."""
+        torch = _torch()
+        with _launching_on(x) as stream:
+            ws = self._sizes(x, binding.msgla_recurrence_workspace_bytes)
+            y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+            if h_out is None:
+                h_out = torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)
+            binding.msgla_recurrence_forward(self.cfg, x, z, y, ws, bias, mask, h_in, h_out, stream)
+        return y, h_out
+
+    def backward(self, x, z, dy, bias=None, mask=None, h_in=None, dh_out=None, dx=None, dz=None):
+        """(dx, dz, dbias, dh_in) from dy [B, L, width] (or None for 0) and dh_out [B, width] (or None):
+        dbias is None without a bias, dh_in without h_in."""
+        torch = _torch()
+        with _launching_on(x) as stream:
+            ws = self._sizes(x, binding.msgla_recurrence_backward_workspace_bytes)
+            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+            dz = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dz is None else dz
+            dbias = None if bias is None else torch.empty_like(bias)
+            dh_in = None if h_in is None else torch.empty_like(h_in)
+            binding.msgla_recurrence_backward(self.cfg, x, z, dy, dx, dz, ws, bias, mask, h_in, dh_out, dbias, dh_in,
+                                              stream)
+        return dx, dz, dbias, dh_in
+
+    def step(self, x_t, z_t, h, bias=None, mask=None, y_t=None, h_out=None):
+        """One token of every sequence: x_t, z_t [B, width], h [B, width] fp32 -> (y_t, state).
+        The state is renewed in place unless h_out is given."""
+        torch = _torch()
+        h_out = h if h_out is None else h_out
+        with _launching_on(x_t) as stream:
+            y_t = torch.empty(x_t.shape, dtype=x_t.dtype, device=x_t.device) if y_t is None else y_t
+            binding.msgla_recurrence_step(self.cfg, x_t, z_t, y_t, h, h_out, bias, mask, stream)
+        return y_t, h_out
 
 
 def read_state(cfg: MsglaConfig, state, B: int) -> dict:

@@ -1,0 +1,117 @@
+"""CPU: the 64-bit recurrence's gradients against central differences, its
+closed form for constant gates, and the refusals of the C entry points and of
+the device handle."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from scale_gla_layer_amd import binding
+from scale_gla_layer_amd.config import RECURRENCE_INPUTS, RecurrenceConfig
+from tests import recurrence_ref as ref
+
+
+@pytest.mark.parametrize("mode", RECURRENCE_INPUTS)
+def test_gradients_against_differences(mode):
+    rng = np.random.default_rng(5)
+    B, L, D, gamma = 2, 9, 3, 4.0
+    v = {"x": rng.normal(size=(B, L, D)), "z": rng.normal(size=(B, L, D)), "bias": rng.normal(size=D),
+         "h_in": rng.normal(size=(B, D))}
+    mask = np.ones((B, L), np.uint8)
+    mask[0, 3], mask[1, 7:] = 0, 0
+    dy, dh = rng.normal(size=(B, L, D)), rng.normal(size=(B, D))
+
+    def loss(**kw):
+        a = {**v, **kw}
+        out = ref.forward(a["x"], a["z"], a["bias"], gamma, mode, mask, a["h_in"])[0]
+        return (out["y"] * dy).sum() + (out["h_out"] * dh).sum()
+
+    g = ref.backward(v["x"], v["z"], dy, v["bias"], gamma, mode, mask, v["h_in"], dh)[0]
+    for name in v:
+        grad, step = g["d" + name], 1e-5
+        for at in np.ndindex(v[name].shape):
+            up, down = v[name].copy(), v[name].copy()
+            up[at] += step
+            down[at] -= step
+            diff = (loss(**{name: up}) - loss(**{name: down})) / (2 * step)
+            # the third derivatives here are of order 10: step^2 times that, and 1e-16 / step of rounding
+            assert abs(diff - grad[at]) < 1e-8, (name, at)
+
+
+@pytest.mark.parametrize("mode", RECURRENCE_INPUTS)
+def test_constant_gate_is_a_geometric_sum(mode):
+    L = 40
+    x = np.ones((1, L, 1))
+    z = np.full((1, L, 1), 0.3)
+    out = ref.forward(x, z, np.zeros(1), 2.0, mode)[0]
+    a = (1 / (1 + np.exp(-0.3))) ** 0.5
+    beta = {"plain": 1.0, "convex": 1 - a, "norm": np.sqrt(1 - a * a)}[mode]
+    want = beta * (1 - a ** np.arange(1, L + 1)) / (1 - a)
+    assert np.allclose(out["y"][0, :, 0], want, rtol=1e-13)
+
+
+def _raw(**kw):
+    c = dict(width=64, input=0, gate_normalizer=16.0, dtype=1)
+    c.update(kw)
+    return binding.CRecurrenceConfig(c["width"], c["input"], c["gate_normalizer"], c["dtype"])
+
+
+BAD_SIZE = 2 ** 64 - 1
+
+
+@pytest.mark.parametrize("bad", [dict(width=0), dict(width=65537), dict(input=3), dict(input=-1), dict(dtype=2),
+                                 dict(gate_normalizer=0.0), dict(gate_normalizer=-1.0),
+                                 dict(gate_normalizer=float("nan")), dict(gate_normalizer=float("inf"))])
+def test_invalid_configurations(bad):
+    lib = binding.load_library()
+    c = ctypes.byref(_raw(**bad))
+    assert lib.msgla_recurrence_workspace_bytes(c, 1, 8) == BAD_SIZE
+    assert lib.msgla_recurrence_backward_workspace_bytes(c, 1, 8) == BAD_SIZE
+    r = ctypes.byref(binding.CRows(4096, 512, 64))
+    assert lib.msgla_recurrence_forward(c, r, r, None, None, None, 1, 8, r, None, None, 0, None) == 1
+    assert lib.msgla_recurrence_step(c, r, r, None, None, 4096, 1, r, 4096, None) == 1
+
+
+@pytest.mark.parametrize("B,L", [(0, 8), (1, 0), (-1, 8), (1, (1 << 24) + 1), (1 << 16, 1 << 13)])
+def test_invalid_sizes(B, L):
+    lib = binding.load_library()
+    assert lib.msgla_recurrence_workspace_bytes(ctypes.byref(_raw()), B, L) == BAD_SIZE
+    r = ctypes.byref(binding.CRows(4096, 512, 64))
+    assert lib.msgla_recurrence_forward(ctypes.byref(_raw()), r, r, None, None, None, B, L, r, None, 4096, 1 << 62,
+                                        None) == 1
+
+
+def test_bad_arguments_return_before_anything_is_enqueued():
+    lib = binding.load_library()
+    c = ctypes.byref(_raw())
+    rows = lambda p=4096, b=512, t=64: ctypes.byref(binding.CRows(p, b, t))  # noqa: E731
+    ok = rows()
+    B, L = 2, 200
+    need = lib.msgla_recurrence_workspace_bytes(c, B, L)
+    fwd = lambda x=ok, z=ok, y=ok, bias=None, ws=4096, n=need: lib.msgla_recurrence_forward(  # noqa: E731
+        c, x, z, bias, None, None, B, L, y, None, ws, n, None)
+    assert fwd(x=None) == 1 and fwd(z=rows(0)) == 1 and fwd(y=rows(4097)) == 1
+    assert fwd(x=rows(4096, -1)) == 1 and fwd(x=rows(4096, 512, -64)) == 1
+    assert fwd(bias=4098) == 1 and fwd(ws=None) == 1 and fwd(ws=4104) == 1
+    assert fwd(n=need - 1) == 3
+    back = lib.msgla_recurrence_backward_workspace_bytes(c, B, L)
+    bwd = lambda dy=ok, dh=None, dx=ok, n=back: lib.msgla_recurrence_backward(  # noqa: E731
+        c, ok, ok, None, None, None, dy, dh, B, L, dx, ok, None, None, 4096, n, None)
+    assert bwd(dy=None) == 1 and bwd(dx=None) == 1 and bwd(dx=rows(0)) == 1 and bwd(n=back - 1) == 3
+    step = lambda h=4096, y=ok: lib.msgla_recurrence_step(c, ok, ok, None, None, h, B, y, 4096, None)  # noqa: E731
+    assert step(h=None) == 1 and step(y=None) == 1 and step(h=4097) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(width=0), dict(input="gate"), dict(gate_normalizer=0.0), dict(dtype="f16"),
+                                dict(gate_normalizer=float("nan"))])
+def test_configuration_class_refuses(kw):
+    with pytest.raises(ValueError):
+        RecurrenceConfig(**{"width": 64, **kw})
+
+
+def test_handle_refuses_host_tensors():
+    import torch
+    from scale_gla_layer_amd.runner import DeviceRecurrence
+    x = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="ROCm device"):
+        DeviceRecurrence(RecurrenceConfig(64)).forward(x, x)
