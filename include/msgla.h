@@ -482,6 +482,126 @@ msgla_status msgla_recurrence_step(const msgla_recurrence_config* cfg, const msg
                                    const float* h_in, int64_t B, const msgla_rows* y_t, float* h_out,
                                    void* stream);
 
+/*
+ * Attention over selected blocks.  The keys of a sequence are cut into blocks of
+ * `block` positions, as the layer's coarse branches cut it for pooling; each
+ * query attends, with softmax weights, the keys at or before its own position
+ * in at most n_select of them.  Which ones is decided per query and key-value
+ * head: the first n_first blocks and the n_recent ones that end with the
+ * query's own always, and of the others those of the highest score
+ *     s(t, j) = (sum over the group's heads of q_t) . c_j,
+ * c_j the mean of block j's keys; equal scores go to the lower index and a NaN
+ * ranks as minus infinity.  Query head g of heads_q uses key-value head
+ * g / (heads_q / heads_kv).
+ * Requirements: heads_q a multiple of heads_kv, at most 1024; d_k a multiple of
+ * 8 up to 128, d_v one up to 256; block 32, 64 or 128; n_select 1 .. 64;
+ * n_first >= 0, n_recent >= 1, n_first + n_recent <= n_select; scale finite
+ * (1 / sqrt(d_k) as a rule).  dtype: of q, k, v, the output and their
+ * gradients; bf16 inputs meet on bf16 matrix cores with fp32 sums (softmax
+ * weights and their gradients are rounded to bf16 for the products), fp32 ones
+ * on fp32 matrix cores; scores for the selection are fp64 sums.
+ */
+typedef struct {
+  int32_t heads_q, heads_kv;
+  int32_t d_k, d_v;
+  int32_t block;
+  int32_t n_select, n_first, n_recent;
+  float scale;
+  int32_t dtype; /* msgla_dtype */
+} msgla_block_config;
+
+/* Heads of a tensor [B][L][heads][width] with dense rows: row (b, t, h) starts
+ * at data + b stride_b + t stride_t + h stride_h elements.  data is 16-byte
+ * aligned, and strides are multiples of 16 bytes and not negative; rows of an
+ * output may not overlap one another or an input. */
+typedef struct {
+  void* data;
+  int64_t stride_b, stride_t, stride_h;
+} msgla_heads;
+
+/*
+ * Positions.  All calls take the keys' positions 0 .. S - 1 (S: a cache's
+ * capacity, or the length of a training batch; at most 2^24) and two device
+ * arrays [B] int32 that may be NULL:
+ *   start: position of query row 0 (row i stands at start[b] + i); NULL: 0
+ *   lens:  keys that sequence b has, at most S; NULL: S
+ * A query row at a position below 0 or not below lens[b] is padding: it selects
+ * nothing, its output row is 0, its lse minus infinity and its gradient 0.  What
+ * k and v hold behind lens[b] is not used.
+ * sel [B][heads_kv][L][n_select] int32 holds each query's blocks in ascending
+ * order, then -1.  An entry counts if it names a block at or before the query's
+ * own and is greater than every entry that counted before it; other entries
+ * are ignored, so any contents are safe.
+ * means [B][heads_kv][ceil(S / block)][d_k] fp32.
+ */
+
+/* Mean key of every whole block (all of its positions below lens[b]); a row of
+ * a block that is not whole is written as 0.  from: NULL, or [B] int32: blocks
+ * that end at or before position from[b] are left as they are. */
+msgla_status msgla_block_means(const msgla_block_config* cfg, const msgla_heads* k,
+                               const int32_t* lens, const int32_t* from, int64_t B, int64_t S,
+                               float* means, void* stream);
+
+/* The blocks of every query.  Only blocks before the query's own are scored, so
+ * the means of whole blocks suffice. */
+msgla_status msgla_block_select(const msgla_block_config* cfg, const msgla_heads* q,
+                                const float* means, const int32_t* start, const int32_t* lens,
+                                int64_t B, int64_t L, int64_t S, int32_t* sel, void* stream);
+
+/* Device workspace (bytes) of msgla_block_attention, its backward and its step;
+ * may be 0 for the first (workspace may then be NULL); (size_t)-1 for an
+ * invalid configuration or size. */
+size_t msgla_block_attention_workspace_bytes(const msgla_block_config* cfg, int64_t B, int64_t L, int64_t S);
+size_t msgla_block_attention_backward_workspace_bytes(const msgla_block_config* cfg, int64_t B, int64_t L,
+                                                      int64_t S);
+size_t msgla_block_attention_step_workspace_bytes(const msgla_block_config* cfg, int64_t B, int64_t S);
+
+/*
+ * The attention: q [B][L][heads_q][d_k], k [B][S][heads_kv][d_k],
+ * v [B][S][heads_kv][d_v] -> out [B][L][heads_q][d_v], and, unless lse is NULL,
+ * lse [B][heads_q][L] fp32, the natural logarithm of each row's sum of
+ * exp(scale q . k).  A row without a key is 0 with lse minus infinity.
+ * L may be 1 (decoding with a selection of the caller's) or a chunk of a
+ * longer sequence (start).
+ */
+msgla_status msgla_block_attention(const msgla_block_config* cfg, const msgla_heads* q,
+                                   const msgla_heads* k, const msgla_heads* v, const int32_t* sel,
+                                   const int32_t* start, const int32_t* lens, int64_t B, int64_t L,
+                                   int64_t S, const msgla_heads* out, float* lse, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+
+/*
+ * Its vector-Jacobian product for a given selection (the choice itself has no
+ * gradient): from dout [B][L][heads_q][d_v], with the forward's inputs, out and
+ * lse, writes dq, and dk and dv for all S positions (0 where nothing attends).
+ * The result is the same bit for bit from call to call.
+ */
+msgla_status msgla_block_attention_backward(const msgla_block_config* cfg, const msgla_heads* q,
+                                            const msgla_heads* k, const msgla_heads* v,
+                                            const int32_t* sel, const int32_t* start,
+                                            const int32_t* lens, const msgla_heads* out,
+                                            const float* lse, const msgla_heads* dout, int64_t B,
+                                            int64_t L, int64_t S, const msgla_heads* dq,
+                                            const msgla_heads* dk, const msgla_heads* dv,
+                                            void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One streaming step of B sequences: puts each one's new key and value (k_t
+ * [B][heads_kv][d_k], v_t [B][heads_kv][d_v]) at position pos[b] of its caches
+ * k, v, renews the mean of the block that this completes, selects the blocks of
+ * q_t [B][heads_q][d_k] and attends them -> out_t [B][heads_q][d_v].  stride_t of
+ * the four _t tensors is not read.  pos [B] int32 (device) is the number of
+ * tokens before this one; the caller advances it.  The means of the blocks
+ * before pos[b]'s are those of msgla_block_means or of earlier steps.  A
+ * position outside [0, S) puts nothing and gives an output row of 0.
+ */
+msgla_status msgla_block_attention_step(const msgla_block_config* cfg, const msgla_heads* q_t,
+                                        const msgla_heads* k_t, const msgla_heads* v_t,
+                                        const int32_t* pos, int64_t B, int64_t S,
+                                        const msgla_heads* k, const msgla_heads* v, float* means,
+                                        const msgla_heads* out_t, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,7 +12,7 @@ import ctypes
 import os
 from typing import Optional, Sequence
 
-from .config import BF16, F32, MsglaConfig, RECURRENCE_INPUTS, RecurrenceConfig
+from .config import BF16, F32, BlockAttentionConfig, MsglaConfig, RECURRENCE_INPUTS, RecurrenceConfig
 
 MAX_BRANCHES = 8
 N_STAGES = 6
@@ -30,6 +30,9 @@ SYMBOLS = (
     "msgla_backward_workspace_bytes", "msgla_backward", "msgla_forward_train", "msgla_backward_saved",
     "msgla_recurrence_workspace_bytes", "msgla_recurrence_backward_workspace_bytes",
     "msgla_recurrence_forward", "msgla_recurrence_backward", "msgla_recurrence_step",
+    "msgla_block_means", "msgla_block_select", "msgla_block_attention_workspace_bytes",
+    "msgla_block_attention_backward_workspace_bytes", "msgla_block_attention_step_workspace_bytes",
+    "msgla_block_attention", "msgla_block_attention_backward", "msgla_block_attention_step",
 )
 NOALLOC_WORKSPACE_BYTES = 192 << 20  # MSGLA_NOALLOC_WORKSPACE_BYTES
 
@@ -91,6 +94,16 @@ class CRecurrenceConfig(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class CHeads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_t", ctypes.c_int64),
+                ("stride_h", ctypes.c_int64)]
+
+
+class CBlockConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads_q", "heads_kv", "d_k", "d_v", "block", "n_select", "n_first",
+                                              "n_recent")] + [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
 class CStageEvents(ctypes.Structure):
     _fields_ = [("start", ctypes.c_void_p * N_STAGES), ("stop", ctypes.c_void_p * N_STAGES)]
 
@@ -140,6 +153,20 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "msgla_recurrence_backward": (ctypes.c_int, [rec, rows, rows, vp, vp, vp, rows, vp, i64, i64, rows, rows,
                                                      vp, vp, vp, sz, vp]),
         "msgla_recurrence_step": (ctypes.c_int, [rec, rows, rows, vp, vp, vp, i64, rows, vp, vp]),
+    })
+    heads, blk = ctypes.POINTER(CHeads), ctypes.POINTER(CBlockConfig)
+    sig.update({
+        "msgla_block_means": (ctypes.c_int, [blk, heads, vp, vp, i64, i64, vp, vp]),
+        "msgla_block_select": (ctypes.c_int, [blk, heads, vp, vp, vp, i64, i64, i64, vp, vp]),
+        "msgla_block_attention_workspace_bytes": (sz, [blk, i64, i64, i64]),
+        "msgla_block_attention_backward_workspace_bytes": (sz, [blk, i64, i64, i64]),
+        "msgla_block_attention_step_workspace_bytes": (sz, [blk, i64, i64]),
+        "msgla_block_attention": (ctypes.c_int, [blk, heads, heads, heads, vp, vp, vp, i64, i64, i64, heads, vp, vp,
+                                                 sz, vp]),
+        "msgla_block_attention_backward": (ctypes.c_int, [blk, heads, heads, heads, vp, vp, vp, heads, vp, heads, i64,
+                                                          i64, i64, heads, heads, heads, vp, sz, vp]),
+        "msgla_block_attention_step": (ctypes.c_int, [blk, heads, heads, heads, vp, i64, i64, heads, heads, vp, heads,
+                                                      vp, sz, vp]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -434,3 +461,135 @@ def msgla_recurrence_step(cfg: RecurrenceConfig, x_t, z_t, y_t, h_in, h_out, bia
         ctypes.byref(c_recurrence_config(cfg)), _rows(x_t), _rows(z_t), _ptr(bias), _ptr(mask), _ptr(h_in), shape[0],
         _rows(y_t), _ptr(h_out), _stream(stream))
     _check("msgla_recurrence_step", st)
+
+
+def _heads(name: str, t) -> CHeads:
+    """[B, L, heads, width], or [B, heads, width] as rows of one position."""
+    strides = [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
+    if t.data_ptr() % 16 or any(s * t.element_size() % 16 for s in strides):
+        raise ValueError(f"rows of {name} must start at multiples of 16 bytes")
+    return CHeads(t.data_ptr(), strides[0], strides[1] if t.dim() == 4 else 0, strides[-1])
+
+
+def _i32(name: str, t, shape, device):
+    import torch
+    return None if t is None else _tensor(name, t, shape, torch.int32, device, contiguous=True)
+
+
+_BLOCK_CACHE: dict = {}
+
+
+def c_block_config(cfg: BlockAttentionConfig) -> CBlockConfig:
+    c = _BLOCK_CACHE.get(cfg)
+    if c is None:
+        c = _BLOCK_CACHE[cfg] = CBlockConfig(cfg.heads_q, cfg.heads_kv, cfg.d_k, cfg.d_v, cfg.block, cfg.n_select,
+                                             cfg.n_first, cfg.n_recent, cfg.scale, 1 if cfg.dtype == BF16 else 0)
+    return c
+
+
+def block_count(cfg: BlockAttentionConfig, S: int) -> int:
+    return (S + cfg.block - 1) // cfg.block
+
+
+def msgla_block_attention_workspace_bytes(cfg: BlockAttentionConfig, B: int, L: int, S: int) -> int:
+    return load_library().msgla_block_attention_workspace_bytes(ctypes.byref(c_block_config(cfg)), B, L, S)
+
+
+def msgla_block_attention_backward_workspace_bytes(cfg: BlockAttentionConfig, B: int, L: int, S: int) -> int:
+    return load_library().msgla_block_attention_backward_workspace_bytes(ctypes.byref(c_block_config(cfg)), B, L, S)
+
+
+def msgla_block_attention_step_workspace_bytes(cfg: BlockAttentionConfig, B: int, S: int) -> int:
+    return load_library().msgla_block_attention_step_workspace_bytes(ctypes.byref(c_block_config(cfg)), B, S)
+
+
+def _dims(name: str, t, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{name} must have {n} dimensions: it has {t.dim()}")
+    return t
+
+
+def msgla_block_means(cfg: BlockAttentionConfig, k, means, lens=None, start_from=None, stream=None):
+    """k [B, S, heads_kv, d_k] -> means [B, heads_kv, blocks, d_k] fp32; lens, start_from: [B] int32."""
+    B, S = _dims("k", k, 4).shape[:2]
+    _tensor("k", k, (B, S, cfg.heads_kv, cfg.d_k), _storage(cfg), k.device)
+    _f32("means", means, (B, cfg.heads_kv, block_count(cfg, S), cfg.d_k), k.device)
+    _i32("lens", lens, (B,), k.device)
+    _i32("start_from", start_from, (B,), k.device)
+    st = load_library().msgla_block_means(ctypes.byref(c_block_config(cfg)), _heads("k", k), _ptr(lens),
+                                          _ptr(start_from), B, S, _ptr(means), _stream(stream))
+    _check("msgla_block_means", st)
+
+
+def msgla_block_select(cfg: BlockAttentionConfig, q, means, S: int, sel, start=None, lens=None, stream=None):
+    """q [B, L, heads_q, d_k] -> sel [B, heads_kv, L, n_select] int32."""
+    B, L = _dims("q", q, 4).shape[:2]
+    _tensor("q", q, (B, L, cfg.heads_q, cfg.d_k), _storage(cfg), q.device)
+    _f32("means", means, (B, cfg.heads_kv, block_count(cfg, S), cfg.d_k), q.device)
+    _i32("sel", sel, (B, cfg.heads_kv, L, cfg.n_select), q.device)
+    _i32("start", start, (B,), q.device)
+    _i32("lens", lens, (B,), q.device)
+    st = load_library().msgla_block_select(ctypes.byref(c_block_config(cfg)), _heads("q", q), _ptr(means), _ptr(start),
+                                           _ptr(lens), B, L, S, _ptr(sel), _stream(stream))
+    _check("msgla_block_select", st)
+
+
+def _block_inputs(cfg, q, k, v, sel, start, lens):
+    B, L = _dims("q", q, 4).shape[:2]
+    S, dt, dev = _dims("k", k, 4).shape[1], _storage(cfg), q.device
+    _tensor("q", q, (B, L, cfg.heads_q, cfg.d_k), dt, dev)
+    _tensor("k", k, (B, S, cfg.heads_kv, cfg.d_k), dt, dev)
+    _tensor("v", v, (B, S, cfg.heads_kv, cfg.d_v), dt, dev)
+    _i32("sel", sel, (B, cfg.heads_kv, L, cfg.n_select), dev)
+    _i32("start", start, (B,), dev)
+    _i32("lens", lens, (B,), dev)
+    return B, L, S
+
+
+def msgla_block_attention(cfg: BlockAttentionConfig, q, k, v, sel, out, lse, workspace, start=None, lens=None,
+                          stream=None):
+    """q [B, L, heads_q, d_k], k [B, S, heads_kv, d_k], v [B, S, heads_kv, d_v] -> out [B, L, heads_q, d_v] and
+    lse [B, heads_q, L] fp32 (or None)."""
+    B, L, S = _block_inputs(cfg, q, k, v, sel, start, lens)
+    _apart("out", _tensor("out", out, (B, L, cfg.heads_q, cfg.d_v), _storage(cfg), q.device))
+    _f32("lse", lse, (B, cfg.heads_q, L), q.device)
+    st = load_library().msgla_block_attention(
+        ctypes.byref(c_block_config(cfg)), _heads("q", q), _heads("k", k), _heads("v", v), _ptr(sel), _ptr(start),
+        _ptr(lens), B, L, S, _heads("out", out), _ptr(lse), _ptr(workspace),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("msgla_block_attention", st)
+
+
+def msgla_block_attention_backward(cfg: BlockAttentionConfig, q, k, v, sel, out, lse, dout, dq, dk, dv, workspace,
+                                   start=None, lens=None, stream=None):
+    B, L, S = _block_inputs(cfg, q, k, v, sel, start, lens)
+    for name, t in (("out", out), ("dout", dout)):
+        _tensor(name, t, (B, L, cfg.heads_q, cfg.d_v), _storage(cfg), q.device)
+    _f32("lse", lse, (B, cfg.heads_q, L), q.device)
+    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        _apart(name, _tensor(name, t, like.shape, like.dtype, q.device))
+    st = load_library().msgla_block_attention_backward(
+        ctypes.byref(c_block_config(cfg)), _heads("q", q), _heads("k", k), _heads("v", v), _ptr(sel), _ptr(start),
+        _ptr(lens), _heads("out", out), _ptr(lse), _heads("dout", dout), B, L, S, _heads("dq", dq), _heads("dk", dk),
+        _heads("dv", dv), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("msgla_block_attention_backward", st)
+
+
+def msgla_block_attention_step(cfg: BlockAttentionConfig, q_t, k_t, v_t, k, v, means, pos, out_t, workspace,
+                               stream=None):
+    """q_t [B, heads_q, d_k], k_t [B, heads_kv, d_k], v_t [B, heads_kv, d_v], caches k [B, S, heads_kv, d_k] and
+    v [B, S, heads_kv, d_v], means [B, heads_kv, blocks, d_k] fp32, pos [B] int32 -> out_t [B, heads_q, d_v]."""
+    B, S, dt, dev = q_t.shape[0], _dims("k", k, 4).shape[1], _storage(cfg), q_t.device
+    _tensor("q_t", q_t, (B, cfg.heads_q, cfg.d_k), dt, dev)
+    _tensor("k_t", k_t, (B, cfg.heads_kv, cfg.d_k), dt, dev)
+    _tensor("v_t", v_t, (B, cfg.heads_kv, cfg.d_v), dt, dev)
+    _apart("k", _tensor("k", k, (B, S, cfg.heads_kv, cfg.d_k), dt, dev))
+    _apart("v", _tensor("v", v, (B, S, cfg.heads_kv, cfg.d_v), dt, dev))
+    _f32("means", means, (B, cfg.heads_kv, block_count(cfg, S), cfg.d_k), dev)
+    _i32("pos", pos, (B,), dev)
+    _apart("out_t", _tensor("out_t", out_t, (B, cfg.heads_q, cfg.d_v), dt, dev))
+    st = load_library().msgla_block_attention_step(
+        ctypes.byref(c_block_config(cfg)), _heads("q_t", q_t), _heads("k_t", k_t), _heads("v_t", v_t), _ptr(pos), B, S,
+        _heads("k", k), _heads("v", v), _ptr(means), _heads("out_t", out_t), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("msgla_block_attention_step", st)

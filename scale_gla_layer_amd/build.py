@@ -37,6 +37,10 @@ SOURCES = [
     "api_backward.cpp",
     "k_recurrence.hip",
     "api_recurrence.cpp",
+    "k_block_select.hip",
+    "k_block_attention.hip",
+    "k_block_grad.hip",
+    "api_block.cpp",
 ]
 
 # rocBLAS: the backward's plain products (weight and input gradients)

@@ -83,6 +83,41 @@ class RecurrenceConfig:
 
 
 @dataclasses.dataclass(frozen=True)
+class BlockAttentionConfig:
+    """Attention over selected blocks of keys: each query attends the first ``n_first`` blocks of
+    ``block`` positions, the ``n_recent`` ones that end with its own, and those whose mean key scores
+    highest against the sum of its group's queries, ``n_select`` in all.  ``scale`` None: 1 / sqrt(d_k)."""
+    heads_q: int
+    heads_kv: int
+    d_k: int
+    d_v: int
+    block: int = 64
+    n_select: int = 16
+    n_first: int = 1
+    n_recent: int = 2
+    scale: Optional[float] = None
+    dtype: str = BF16
+
+    def __post_init__(self):
+        if self.heads_kv < 1 or not self.heads_kv <= self.heads_q <= 1024 or self.heads_q % self.heads_kv:
+            raise ValueError("heads_q must be a multiple of heads_kv, at most 1024")
+        if not 8 <= self.d_k <= 128 or self.d_k % 8 or not 8 <= self.d_v <= 256 or self.d_v % 8:
+            raise ValueError("d_k must be a multiple of 8 up to 128, d_v one up to 256")
+        if self.block not in (32, 64, 128):
+            raise ValueError("block must be 32, 64 or 128")
+        if not 1 <= self.n_select <= 64:
+            raise ValueError("n_select must be 1 .. 64")
+        if self.n_first < 0 or self.n_recent < 1 or self.n_first + self.n_recent > self.n_select:
+            raise ValueError("n_first >= 0, n_recent >= 1 and n_first + n_recent <= n_select are required")
+        if self.scale is None:
+            object.__setattr__(self, "scale", self.d_k ** -0.5)
+        if not abs(self.scale) <= 3.0e38:
+            raise ValueError("scale must be finite")
+        if self.dtype not in (F32, BF16):
+            raise ValueError(f"dtype must be {F32!r} or {BF16!r}")
+
+
+@dataclasses.dataclass(frozen=True)
 class Workload:
     name: str
     cfg: MsglaConfig

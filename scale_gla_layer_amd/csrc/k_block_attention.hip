@@ -1,0 +1,293 @@
+// Attention over each query's selected blocks: forward, and the gradient of
+// the queries.  o = softmax(scale q K^T) V over the keys at or before the query
+// in its blocks, by one pass with a running maximum and sum.
+//
+// One wave takes a tile of 16 rows and walks the union of its queries' blocks,
+// 32 keys a step; a row that has not chosen a block is masked there.  Where
+// there are few tiles (decoding), a tile's blocks are dealt to several waves
+// whose partial outputs a second kernel joins.
+#include "block_device.hpp"
+
+namespace msgla {
+
+namespace {
+
+template <typename T, int DKP> struct Qfrag {
+  static constexpr int N = DKP * (int)sizeof(T) / 64;
+  u32x4 f[N];
+  __device__ void load(const char* row, int width, int lane, bool in) {
+#pragma unroll
+    for (int s = 0; s < N; ++s) f[s] = in ? blk_ld(row, 64 * s + 16 * (lane >> 4), width) : zero16();
+  }
+};
+
+__device__ __forceinline__ const char* at(const BlkHeads& t, int64_t b, int64_t i, int64_t h) {
+  return t.p + b * t.sb + i * t.st + h * t.sh;
+}
+__device__ __forceinline__ char* out_at(const BlkHeads& t, int64_t b, int64_t i, int64_t h) {
+  return t.p + b * t.sb + i * t.st + h * t.sh;
+}
+
+template <typename T, int DKP, int DVP>
+__global__ __launch_bounds__(64) void k_block_forward(const BlkParams P) {
+  __shared__ int lists[BLK_ROWS * BLK_LIST];
+  __shared__ __attribute__((aligned(16))) char vs[BLK_KEYS * blk_pitch<T, DVP>()];
+  const int lane = threadIdx.x, r = lane & 15, a = lane >> 4;
+  const int64_t work = blockIdx.x;
+  const int64_t tile = work / P.parts;
+  const int part = (int)(work - tile * P.parts);
+  const BlkTile t(P, tile);
+  const BlkRow row = t.row(P, r);
+  blk_lists(P, t, lists, lane);
+  Qfrag<T, DKP> q;
+  q.load(at(P.q, row.b, row.in ? row.i : 0, row.in ? row.head : 0), P.dkw * sizeof(T), lane, row.in);
+  __syncthreads();
+  const int* mine = lists + (row.i - t.i0) * BLK_LIST;
+  int cur = row.in && row.p >= 0 ? *mine : BLK_END, seen = 0;
+  int last = row.p;  // the tile's last position
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) last = max(last, __shfl_xor(last, o));
+  float m = -__builtin_inff(), l = 0.f;
+  f32x4 acc[DVP / 16];
+#pragma unroll
+  for (int d = 0; d < DVP / 16; ++d) acc[d] = zero4();
+  const float sc = P.scale * BLK_LOG2E;
+  const int vw = P.dvw * (int)sizeof(T), kw = P.dkw * (int)sizeof(T);
+  for (;;) {
+    const int j = blk_row_min(cur);
+    if (j == BLK_END) break;
+    const bool member = cur == j;
+    if (member) cur = *++mine;
+    if (seen++ % P.parts != part) continue;
+    const int first = j << P.lgT;
+    for (int k0 = first; k0 < first + (1 << P.lgT) && k0 <= last; k0 += BLK_KEYS) {
+      __syncthreads();
+      // rows behind the tile's last position have weight 0 in every row: zeroes, whatever is there
+      blk_stage<T, DVP, 64>(vs, BLK_KEYS, vw, lane, [&](int i) {
+        return k0 + i <= last ? at(P.v, t.b, k0 + i, t.h) : nullptr;
+      });
+      float p[2][4];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        const char* kr = at(P.k, t.b, min(k0 + 16 * kt + r, P.S - 1), t.h);
+        f32x4 s = zero4();
+#pragma unroll
+        for (int w = 0; w < Qfrag<T, DKP>::N; ++w) s = mma_slab<T>(blk_ld(kr, 64 * w + 16 * a, kw), q.f[w], s);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          p[kt][i] = member && k0 + 16 * kt + 4 * a + i <= row.p ? s[i] * sc : -__builtin_inff();
+      }
+      float mx = m;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(p[0][i], p[1][i]));
+      mx = blk_quad_max(mx);
+      const float ref = mx == -__builtin_inff() ? 0.f : mx;  // nothing to attend yet
+      const float corr = __builtin_amdgcn_exp2f(m - ref);
+      m = mx;
+      l *= corr;
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          p[kt][i] = __builtin_amdgcn_exp2f(p[kt][i] - ref);
+          l += p[kt][i];
+        }
+#pragma unroll
+      for (int d = 0; d < DVP / 16; ++d) acc[d] *= corr;
+      __syncthreads();
+#pragma unroll
+      for (int s = 0; s < BLK_KEYS / blk_slab<T>(); ++s) {
+        const u32x4 w = blk_pack<T>(p, s);
+#pragma unroll
+        for (int d = 0; d < DVP / 16; ++d)
+          acc[d] = mma_slab<T>(blk_column<T>(vs, blk_pitch<T, DVP>(), s * blk_slab<T>(), d, lane), w, acc[d]);
+      }
+    }
+  }
+  l = blk_quad_sum(l);
+  if (P.parts > 1) {
+    const int64_t pr = (tile * P.parts + part) * BLK_ROWS + r;
+    if (a == 0) {
+      P.pm[2 * pr] = m;
+      P.pm[2 * pr + 1] = l;
+    }
+#pragma unroll
+    for (int d = 0; d < DVP / 16; ++d) {
+      const float v[4] = {acc[d][0], acc[d][1], acc[d][2], acc[d][3]};
+      st16(P.po + pr * DVP + 16 * d + 4 * a, pack16<float>(v));
+    }
+    return;
+  }
+  if (!row.in) return;
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // no key: 0; a NaN stays
+  char* o = out_at(P.o, row.b, row.i, row.head);
+#pragma unroll
+  for (int d = 0; d < DVP / 16; ++d) {
+    const int c = 16 * d + 4 * a;
+    const float v[4] = {acc[d][0] * inv, acc[d][1] * inv, acc[d][2] * inv, acc[d][3] * inv};
+    if (c < P.dvw) blk_st4<T>(o + c * sizeof(T), v);
+  }
+  if (P.lse && a == 0)
+    P.lse[((int64_t)row.b * P.Hq + row.head) * P.L + row.i] = l == 0.f ? -__builtin_inff() : m * BLK_LN2 + logf(l);
+}
+
+// Joins a row's partial outputs.
+template <typename T, int DVP> __global__ __launch_bounds__(64) void k_block_join(const BlkParams P) {
+  const int64_t tile = blockIdx.x / BLK_ROWS;
+  const int r = (int)(blockIdx.x % BLK_ROWS), lane = threadIdx.x;
+  const BlkRow row = BlkTile(P, tile).row(P, r);
+  if (!row.in) return;
+  const int64_t pr = tile * P.parts * BLK_ROWS + r;
+  float m = -__builtin_inff(), l = 0.f, o[DVP / 64];
+  for (int k = 0; k < P.parts; ++k) m = fmaxf(m, P.pm[2 * (pr + k * BLK_ROWS)]);
+  const float ref = m == -__builtin_inff() ? 0.f : m;
+#pragma unroll
+  for (int d = 0; d < DVP / 64; ++d) o[d] = 0.f;
+  for (int k = 0; k < P.parts; ++k) {
+    const int64_t at = pr + k * BLK_ROWS;
+    const float w = __builtin_amdgcn_exp2f(P.pm[2 * at] - ref);
+    l += w * P.pm[2 * at + 1];
+#pragma unroll
+    for (int d = 0; d < DVP / 64; ++d) o[d] += w * P.po[at * DVP + 64 * d + lane];
+  }
+  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+  T* out = reinterpret_cast<T*>(out_at(P.o, row.b, row.i, row.head));
+#pragma unroll
+  for (int d = 0; d < DVP / 64; ++d)
+    if (64 * d + lane < P.dvw) out[64 * d + lane] = from_f32<T>(o[d] * inv);
+  if (P.lse && lane == 0)
+    P.lse[((int64_t)row.b * P.Hq + row.head) * P.L + row.i] = l == 0.f ? -__builtin_inff() : m * BLK_LN2 + logf(l);
+}
+
+// delta = sum_c dout_c out_c of every row: what the softmax's gradient subtracts.
+// 16 lanes take a row.
+template <typename T> __global__ __launch_bounds__(256) void k_block_delta(const BlkParams P) {
+  const int64_t n = (int64_t)P.B * P.Hq * P.L, i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int c = threadIdx.x & 15;
+  if (i >= n) return;
+  const int64_t bh = i / P.L, t = i - bh * P.L, b = bh / P.Hq, h = bh - b * P.Hq;
+  const char *x = at(P.o, b, t, h), *y = at(P.dout, b, t, h);
+  float s = 0.f;
+  if (blk_position(P, (int)b, (int)t) >= 0)
+    for (int k = 16 * c; k < P.dvw * (int)sizeof(T); k += 256) {
+      float u[per16<T>()], v[per16<T>()];
+      unpack16<T>(ld16(x + k), u);
+      unpack16<T>(ld16(y + k), v);
+#pragma unroll
+      for (int e = 0; e < per16<T>(); ++e) s += u[e] * v[e];
+    }
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o);
+  if (c == 0) P.delta[i] = s;
+}
+
+// dq = scale sum_j p_j (do . v_j - delta) k_j, the tiles and steps of the forward.
+template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_block_dq(const BlkParams P) {
+  __shared__ int lists[BLK_ROWS * BLK_LIST];
+  __shared__ __attribute__((aligned(16))) char ks[BLK_KEYS * blk_pitch<T, DKP>()];
+  const int lane = threadIdx.x, r = lane & 15, a = lane >> 4;
+  const BlkTile t(P, blockIdx.x);
+  const BlkRow row = t.row(P, r);
+  blk_lists(P, t, lists, lane);
+  Qfrag<T, DKP> q;
+  Qfrag<T, DVP> g;
+  const int vw = P.dvw * (int)sizeof(T), kw = P.dkw * (int)sizeof(T);
+  const bool live = row.in && row.p >= 0;
+  q.load(at(P.q, row.b, live ? row.i : 0, live ? row.head : 0), kw, lane, live);
+  g.load(at(P.dout, row.b, live ? row.i : 0, live ? row.head : 0), vw, lane, live);
+  __syncthreads();
+  const int* mine = lists + (row.i - t.i0) * BLK_LIST;
+  int cur = live ? *mine : BLK_END;
+  int last = row.p;
+#pragma unroll
+  for (int o = 1; o < 16; o <<= 1) last = max(last, __shfl_xor(last, o));
+  const int64_t lr = ((int64_t)row.b * P.Hq + row.head) * P.L + row.i;
+  const float lse = live ? P.lse_in[lr] * BLK_LOG2E : 0.f, delta = live ? P.delta[lr] : 0.f;
+  f32x4 acc[DKP / 16];
+#pragma unroll
+  for (int d = 0; d < DKP / 16; ++d) acc[d] = zero4();
+  const float sc = P.scale * BLK_LOG2E;
+  for (;;) {
+    const int j = blk_row_min(cur);
+    if (j == BLK_END) break;
+    const bool member = cur == j;
+    if (member) cur = *++mine;
+    const int first = j << P.lgT;
+    for (int k0 = first; k0 < first + (1 << P.lgT) && k0 <= last; k0 += BLK_KEYS) {
+      __syncthreads();
+      blk_stage<T, DKP, 64>(ks, BLK_KEYS, kw, lane, [&](int i) {
+        return k0 + i <= last ? at(P.k, t.b, k0 + i, t.h) : nullptr;
+      });
+      __syncthreads();
+      float ds[2][4];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt) {
+        const char* kr = ks + (16 * kt + r) * blk_pitch<T, DKP>();
+        const char* vr = at(P.v, t.b, min(k0 + 16 * kt + r, P.S - 1), t.h);
+        f32x4 s = zero4(), dp = zero4();
+#pragma unroll
+        for (int w = 0; w < Qfrag<T, DKP>::N; ++w) s = mma_slab<T>(ld16(kr + 64 * w + 16 * a), q.f[w], s);
+#pragma unroll
+        for (int w = 0; w < Qfrag<T, DVP>::N; ++w) dp = mma_slab<T>(blk_ld(vr, 64 * w + 16 * a, vw), g.f[w], dp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = __builtin_amdgcn_exp2f(s[i] * sc - lse);
+          ds[kt][i] = member && k0 + 16 * kt + 4 * a + i <= row.p ? p * (dp[i] - delta) * P.scale : 0.f;
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < BLK_KEYS / blk_slab<T>(); ++s) {
+        const u32x4 w = blk_pack<T>(ds, s);
+#pragma unroll
+        for (int d = 0; d < DKP / 16; ++d)
+          acc[d] = mma_slab<T>(blk_column<T>(ks, blk_pitch<T, DKP>(), s * blk_slab<T>(), d, lane), w, acc[d]);
+      }
+    }
+  }
+  if (!row.in) return;
+  char* o = out_at(P.dq, row.b, row.i, row.head);
+#pragma unroll
+  for (int d = 0; d < DKP / 16; ++d) {
+    const int c = 16 * d + 4 * a;
+    const float v[4] = {acc[d][0], acc[d][1], acc[d][2], acc[d][3]};
+    if (c < P.dkw) blk_st4<T>(o + c * sizeof(T), v);
+  }
+}
+
+template <typename T, int DKP, int DVP> struct Run {
+  static void forward(const BlkParams& P, hipStream_t st) {
+    hipLaunchKernelGGL((k_block_forward<T, DKP, DVP>), dim3((unsigned)(P.tiles * P.parts)), dim3(64), 0, st, P);
+    if (P.parts > 1)
+      hipLaunchKernelGGL((k_block_join<T, DVP>), dim3((unsigned)(P.tiles * BLK_ROWS)), dim3(64), 0, st, P);
+  }
+  static void dq(const BlkParams& P, hipStream_t st) {
+    const int64_t rows = (int64_t)P.B * P.Hq * P.L;
+    hipLaunchKernelGGL(k_block_delta<T>, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, P);
+    hipLaunchKernelGGL((k_block_dq<T, DKP, DVP>), dim3((unsigned)P.tiles), dim3(64), 0, st, P);
+  }
+};
+
+template <typename T, int DKP, class F> void by_dv(int dv, F f) {
+  if (blk_dvp(dv) == 64) f(Run<T, DKP, 64>());
+  else if (blk_dvp(dv) == 128) f(Run<T, DKP, 128>());
+  else f(Run<T, DKP, 256>());
+}
+template <class F> void dispatch(const BlkParams& P, bool bf16_path, F f) {
+  const bool k64 = blk_dkp(P.dkw) == 64;
+  if (bf16_path) k64 ? by_dv<bf16, 64>(P.dvw, f) : by_dv<bf16, 128>(P.dvw, f);
+  else k64 ? by_dv<float, 64>(P.dvw, f) : by_dv<float, 128>(P.dvw, f);
+}
+
+}  // namespace
+
+hipError_t launch_block_forward(const BlkParams& P, bool bf16_path, hipStream_t st) {
+  dispatch(P, bf16_path, [&](auto r) { r.forward(P, st); });
+  return hipGetLastError();
+}
+
+hipError_t launch_block_dq(const BlkParams& P, bool bf16_path, hipStream_t st) {
+  dispatch(P, bf16_path, [&](auto r) { r.dq(P, st); });
+  return hipGetLastError();
+}
+
+}  // namespace msgla

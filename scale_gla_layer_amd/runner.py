@@ -9,7 +9,7 @@ from typing import Optional
 import numpy as np
 
 from . import binding
-from .config import BF16, MsglaConfig, RecurrenceConfig
+from .config import BF16, BlockAttentionConfig, MsglaConfig, RecurrenceConfig
 from .synth import LayerWeights, storage_array
 
 
@@ -268,6 +268,80 @@ class DeviceRecurrence:
             y_t = torch.empty(x_t.shape, dtype=x_t.dtype, device=x_t.device) if y_t is None else y_t
             binding.msgla_recurrence_step(self.cfg, x_t, z_t, y_t, h, h_out, bias, mask, stream)
         return y_t, h_out
+
+
+class DeviceBlockAttention:
+    """Block selection and the attention over the selected blocks, on device tensors.  Every call
+    runs on the current stream of its tensors' device, allocates what it returns unless given, and may
+    be captured in a graph."""
+
+    def __init__(self, cfg: BlockAttentionConfig):
+        self.cfg = cfg
+
+    def _room(self, query, device, *sizes):
+        n = query(self.cfg, *sizes)
+        if n == 2 ** 64 - 1:
+            raise ValueError(f"invalid sizes {sizes}")
+        return _workspace(n, device)
+
+    def means(self, k, lens=None, start_from=None, means=None):
+        """Mean keys of the whole blocks of k [B, S, heads_kv, d_k]: [B, heads_kv, blocks, d_k] fp32.
+        start_from [B] int32 (with a means of earlier calls): blocks that end at or before it are kept."""
+        torch = _torch()
+        if start_from is not None and means is None:
+            raise ValueError("start_from keeps rows of a means that must be given")
+        with _launching_on(k) as stream:
+            if means is None:
+                means = torch.empty((k.shape[0], self.cfg.heads_kv, binding.block_count(self.cfg, k.shape[1]),
+                                     self.cfg.d_k), dtype=torch.float32, device=k.device)
+            binding.msgla_block_means(self.cfg, k, means, lens, start_from, stream)
+        return means
+
+    def select(self, q, means, start=None, lens=None, sel=None):
+        """The blocks of every query of q [B, L, heads_q, d_k]: [B, heads_kv, L, n_select] int32."""
+        torch = _torch()
+        with _launching_on(q) as stream:
+            if sel is None:
+                sel = torch.empty((q.shape[0], self.cfg.heads_kv, q.shape[1], self.cfg.n_select), dtype=torch.int32,
+                                  device=q.device)
+            binding.msgla_block_select(self.cfg, q, means, means.shape[2] * self.cfg.block, sel, start, lens, stream)
+        return sel
+
+    def forward(self, q, k, v, sel, start=None, lens=None, out=None, lse=None):
+        """(out [B, L, heads_q, d_v], lse [B, heads_q, L] fp32)."""
+        torch = _torch()
+        with _launching_on(q) as stream:
+            B, L = q.shape[:2]
+            ws = self._room(binding.msgla_block_attention_workspace_bytes, q.device, B, L, k.shape[1])
+            if out is None:
+                out = torch.empty((B, L, self.cfg.heads_q, self.cfg.d_v), dtype=q.dtype, device=q.device)
+            if lse is None:
+                lse = torch.empty((B, self.cfg.heads_q, L), dtype=torch.float32, device=q.device)
+            binding.msgla_block_attention(self.cfg, q, k, v, sel, out, lse, ws, start, lens, stream)
+        return out, lse
+
+    def backward(self, q, k, v, sel, out, lse, dout, start=None, lens=None, dq=None, dk=None, dv=None):
+        """(dq, dk, dv) for the forward's inputs, out and lse."""
+        torch = _torch()
+        with _launching_on(q) as stream:
+            ws = self._room(binding.msgla_block_attention_backward_workspace_bytes, q.device, q.shape[0], q.shape[1],
+                            k.shape[1])
+            dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if d is None else d
+                          for t, d in ((q, dq), (k, dk), (v, dv)))
+            binding.msgla_block_attention_backward(self.cfg, q, k, v, sel, out, lse, dout, dq, dk, dv, ws, start, lens,
+                                                   stream)
+        return dq, dk, dv
+
+    def step(self, q_t, k_t, v_t, k, v, means, pos, out_t=None):
+        """One token of every sequence: puts k_t, v_t at pos [B] int32 of the caches, renews the means, selects
+        and attends: out_t [B, heads_q, d_v].  The caller advances pos."""
+        torch = _torch()
+        with _launching_on(q_t) as stream:
+            ws = self._room(binding.msgla_block_attention_step_workspace_bytes, q_t.device, q_t.shape[0], k.shape[1])
+            if out_t is None:
+                out_t = torch.empty((q_t.shape[0], self.cfg.heads_q, self.cfg.d_v), dtype=q_t.dtype, device=q_t.device)
+            binding.msgla_block_attention_step(self.cfg, q_t, k_t, v_t, k, v, means, pos, out_t, ws, stream)
+        return out_t
 
 
 def read_state(cfg: MsglaConfig, state, B: int) -> dict:
