@@ -39,6 +39,7 @@ SOURCES = [
     "api_recurrence.cpp",
     "k_block_select.hip",
     "k_block_attention.hip",
+    "k_block_tiles.hip",
     "k_block_grad.hip",
     "api_block.cpp",
 ]

@@ -68,6 +68,8 @@ BlkParams blk_params(const msgla_block_config* c, int64_t B, int64_t L, int64_t 
 
 int es_of(const msgla_block_config* c) { return c->dtype == MSGLA_BF16 ? 2 : 4; }
 
+bool use_tiles(const BlkParams& P) { return P.tiles >= 1024 && P.nb <= BLK_TILES_MAX; }
+
 struct Take {
   size_t cur = 0;
   size_t operator()(size_t bytes) {
@@ -217,7 +219,9 @@ msgla_status msgla_block_attention(const msgla_block_config* cfg, const msgla_he
   P.lens = lens;
   P.lse = lse;
   set_fwd(P, w, workspace);
-  HIP_TRY(launch_block_forward(P, es == 2, static_cast<hipStream_t>(stream)));
+  hipStream_t st = static_cast<hipStream_t>(stream);
+  if (use_tiles(P)) HIP_TRY(launch_block_tiles(P, false, es == 2, st));
+  else HIP_TRY(launch_block_forward(P, es == 2, st));
   return MSGLA_OK;
 }
 
@@ -267,7 +271,9 @@ msgla_status msgla_block_attention_backward(const msgla_block_config* cfg, const
   P.max_items = w.max_items;
   P.max_parts = w.max_parts;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  HIP_TRY(launch_block_dq(P, es == 2, st));
+  HIP_TRY(launch_block_delta(P, es == 2, st));
+  if (use_tiles(P)) HIP_TRY(launch_block_tiles(P, true, es == 2, st));
+  else HIP_TRY(launch_block_dq(P, es == 2, st));
   HIP_TRY(launch_block_dkdv(P, es == 2, st));
   return MSGLA_OK;
 }

@@ -261,8 +261,6 @@ template <typename T, int DKP, int DVP> struct Run {
       hipLaunchKernelGGL((k_block_join<T, DVP>), dim3((unsigned)(P.tiles * BLK_ROWS)), dim3(64), 0, st, P);
   }
   static void dq(const BlkParams& P, hipStream_t st) {
-    const int64_t rows = (int64_t)P.B * P.Hq * P.L;
-    hipLaunchKernelGGL(k_block_delta<T>, dim3((unsigned)((rows + 15) / 16)), dim3(256), 0, st, P);
     hipLaunchKernelGGL((k_block_dq<T, DKP, DVP>), dim3((unsigned)P.tiles), dim3(64), 0, st, P);
   }
 };
@@ -282,6 +280,13 @@ template <class F> void dispatch(const BlkParams& P, bool bf16_path, F f) {
 
 hipError_t launch_block_forward(const BlkParams& P, bool bf16_path, hipStream_t st) {
   dispatch(P, bf16_path, [&](auto r) { r.forward(P, st); });
+  return hipGetLastError();
+}
+
+hipError_t launch_block_delta(const BlkParams& P, bool bf16_path, hipStream_t st) {
+  const dim3 grid((unsigned)(((int64_t)P.B * P.Hq * P.L + 15) / 16));
+  if (bf16_path) hipLaunchKernelGGL(k_block_delta<bf16>, grid, dim3(256), 0, st, P);
+  else hipLaunchKernelGGL(k_block_delta<float>, grid, dim3(256), 0, st, P);
   return hipGetLastError();
 }
 

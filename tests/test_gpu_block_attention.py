@@ -97,6 +97,34 @@ def test_training(hq, hkv, dk, dv, block, n, L, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,dk,dv,block,n,B,L", [
+    (4, 4, 64, 64, 32, 4, 8, 520), (8, 4, 128, 128, 64, 4, 8, 300), (12, 4, 80, 96, 32, 6, 8, 171),
+    (64, 4, 128, 256, 64, 4, 2, 150), (40, 2, 64, 128, 128, 3, 1, 277), (16, 4, 128, 64, 128, 2, 4, 290),
+    (8, 2, 32, 256, 64, 20, 1, 2100)])
+def test_many_queries(hq, hkv, dk, dv, block, n, B, L, dtype):
+    """Enough tiles for a workgroup's waves to share keys and values; padding and chunks among them."""
+    cfg = _cfg(hq, hkv, dk, dv, block, n, min(1, n - 2), 2, dtype)
+    _case(cfg, B, L, seed=L)
+    rng = np.random.default_rng(L)
+    lens = rng.integers(0, L + 1, B)
+    _case(cfg, B, L, lens=lens, seed=L + 1)
+    start = rng.integers(0, 100, B)
+    _case(cfg, B, L, S=L + 77, start=start, lens=np.minimum(start + L, L + 60), seed=L + 2)
+
+
+def test_many_queries_with_any_selection():
+    cfg = _cfg(8, 4, 64, 64, 32, 8)
+    rng = np.random.default_rng(13)
+    B, L = 8, 260
+    sel = rng.integers(-2, 10, (B, 4, L, 8))
+    sel[rng.random(sel.shape) < 0.1] = 2 ** 31 - 1
+    sel[rng.random(sel.shape) < 0.1] = -2 ** 31
+    sel[0, 0, :100] = -1
+    sel[0, 1, :100] = sel[0, 1, :100, :1]
+    _case(cfg, B, L, sel=sel.astype(np.int32), seed=9)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("lens", [[300, 129, 64, 1], [0, 300, 7, 250]])
 def test_padded_batches(lens, dtype):
     _case(_cfg(6, 2, 64, 96, 32, 5, dtype=dtype), 4, 300, lens=lens, seed=5)
