@@ -396,8 +396,8 @@ msgla_status msgla_backward_saved(const msgla_config* cfg, const void* packed, c
  * row (b, t) starts at data + b * stride_b + t * stride_t elements.  A slice of
  * a wider tensor (one projection's columns) is such a view.  Strides are not
  * negative; rows of an output may not overlap one another or an input.  data is
- * aligned to the element; rows whose starts are all multiples of four elements
- * take the vector path. */
+ * aligned to the element; rows that all start at even elements take the
+ * vector path. */
 typedef struct {
   void* data;
   int64_t stride_b, stride_t;

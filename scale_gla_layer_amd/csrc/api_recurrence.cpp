@@ -21,27 +21,47 @@ bool rec_batch_ok(int64_t B, int64_t L) {
 }
 
 struct RecWs {
-  size_t agg, rev, dbp, total;
-  int nch;
+  size_t words, counters, entry, dbp, total;
+  int nch, groups;
+  int64_t n_maps, n_ends;  // words of one direction
 };
 
 RecWs rec_ws(const msgla_recurrence_config* c, int64_t B, int64_t L, bool backward) {
   RecWs w{};
   size_t cur = 0;
-  auto take = [&](size_t floats) {
+  auto take = [&](size_t bytes) {
     const size_t o = cur;
-    cur += align256(floats * 4);
+    cur += align256(bytes);
     return o;
   };
   w.nch = (int)((L + REC_CHUNK - 1) / REC_CHUNK);
-  const size_t per = (size_t)B * w.nch * c->width;
-  if (w.nch > 1) w.agg = take(2 * per);
-  if (backward) {
-    if (w.nch > 1) w.rev = take(per);
-    w.dbp = take(per);
+  w.groups = (w.nch + REC_GROUP - 1) / REC_GROUP;
+  const int64_t row = B * (int64_t)c->width;
+  w.n_maps = row * w.nch;
+  w.n_ends = row * w.groups;
+  if (w.nch > 1) {
+    w.words = take((size_t)((backward ? 2 : 1) * (w.n_maps + w.n_ends) + 1) * 8);  // an even number is cleared
+    w.counters = take((size_t)B * cdiv(c->width, 64) * 8);
+    if (backward) w.entry = take((size_t)w.n_maps * 4);
   }
+  if (backward) w.dbp = take((size_t)w.n_maps * 4);
   w.total = cur;
   return w;
+}
+
+void set_ws(RecParams& P, const RecWs& w, void* ws, bool backward) {
+  P.nch = w.nch;
+  P.groups = w.groups;
+  if (w.nch > 1) {
+    P.maps = at<uint64_t>(ws, w.words);
+    P.ends = P.maps + w.n_maps;
+    P.rmaps = P.ends + w.n_ends;
+    P.rends = P.rmaps + w.n_maps;
+    P.words = ((backward ? 2 : 1) * (w.n_maps + w.n_ends) + 1) / 2 * 2;
+    P.counters = at<uint32_t>(ws, w.counters);
+    P.entry = at<float>(ws, w.entry);
+  }
+  if (backward) P.dbp = at<float>(ws, w.dbp);
 }
 
 bool rows_ok(const msgla_rows* r, int es) {
@@ -52,12 +72,12 @@ bool f32_ok(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
 RecRows rows_of(const msgla_rows* r) { return r ? RecRows{r->data, r->stride_b, r->stride_t} : RecRows{}; }
 
-// Whether every row starts at a multiple of four elements (loads of 8 or 16 bytes).
+// Whether every row starts at an even element (loads of 4 or 8 bytes).
 bool rows_vec(const msgla_rows* r, int es) {
-  return !r || !r->data || (reinterpret_cast<uintptr_t>(r->data) % (4 * es) == 0 && r->stride_b % 4 == 0 && r->stride_t % 4 == 0);
+  return !r || !r->data || (reinterpret_cast<uintptr_t>(r->data) % (2 * es) == 0 && r->stride_b % 2 == 0 && r->stride_t % 2 == 0);
 }
 
-bool f32_vec(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool f32_vec(const void* p) { return reinterpret_cast<uintptr_t>(p) % 8 == 0; }
 
 // One workgroup takes 64 lanes' channels; the grid is one-dimensional.
 bool grid_ok(const RecParams& P) { return (int64_t)P.slabs * P.nch * P.B <= 0x7fffffff; }
@@ -86,7 +106,7 @@ msgla_status msgla_recurrence_forward(const msgla_recurrence_config* cfg, const 
   const RecWs w = rec_ws(cfg, B, L, false);
   if (w.total && (!workspace || !aligned16(workspace))) return MSGLA_ERR_INVALID_ARG;
   if (workspace_bytes < w.total) return MSGLA_ERR_WORKSPACE;
-  const bool vec = cfg->width % 4 == 0 && rows_vec(x, es) && rows_vec(z, es) && rows_vec(y, es) &&
+  const bool vec = cfg->width % 2 == 0 && rows_vec(x, es) && rows_vec(z, es) && rows_vec(y, es) &&
                    f32_vec(bias) && f32_vec(h_in) && f32_vec(h_out);
   RecParams P{};
   P.x = rows_of(x);
@@ -96,12 +116,11 @@ msgla_status msgla_recurrence_forward(const msgla_recurrence_config* cfg, const 
   P.mask = mask;
   P.h_in = h_in;
   P.h_out = h_out;
-  if (w.total) P.agg = at<float>(workspace, w.agg);
   P.B = (int)B;
   P.L = (int)L;
   P.D = cfg->width;
-  P.nch = w.nch;
-  P.slabs = cdiv(P.D, vec ? 256 : 64);
+  set_ws(P, w, workspace, false);
+  P.slabs = cdiv(P.D, vec ? 128 : 64);
   P.inv_gamma = 1.0f / cfg->gate_normalizer;
   if (!grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   HIP_TRY(launch_recurrence_forward(P, cfg->input, es == 2, vec, static_cast<hipStream_t>(stream)));
@@ -122,7 +141,7 @@ msgla_status msgla_recurrence_backward(const msgla_recurrence_config* cfg, const
   const RecWs w = rec_ws(cfg, B, L, true);
   if (!workspace || !aligned16(workspace)) return MSGLA_ERR_INVALID_ARG;
   if (workspace_bytes < w.total) return MSGLA_ERR_WORKSPACE;
-  const bool vec = cfg->width % 4 == 0 && rows_vec(x, es) && rows_vec(z, es) && rows_vec(dy, es) &&
+  const bool vec = cfg->width % 2 == 0 && rows_vec(x, es) && rows_vec(z, es) && rows_vec(dy, es) &&
                    rows_vec(dx, es) && rows_vec(dz, es) && f32_vec(bias) && f32_vec(h_in) && f32_vec(dh_out) &&
                    f32_vec(dbias) && f32_vec(dh_in);
   RecParams P{};
@@ -137,16 +156,11 @@ msgla_status msgla_recurrence_backward(const msgla_recurrence_config* cfg, const
   P.dh_out = dh_out;
   P.dbias = dbias;
   P.dh_in = dh_in;
-  P.nch = w.nch;
-  if (P.nch > 1) {
-    P.agg = at<float>(workspace, w.agg);
-    P.rev = at<float>(workspace, w.rev);
-  }
-  P.dbp = at<float>(workspace, w.dbp);
+  set_ws(P, w, workspace, true);
   P.B = (int)B;
   P.L = (int)L;
   P.D = cfg->width;
-  P.slabs = cdiv(P.D, vec ? 256 : 64);
+  P.slabs = cdiv(P.D, vec ? 128 : 64);
   P.inv_gamma = 1.0f / cfg->gate_normalizer;
   if (!grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   HIP_TRY(launch_recurrence_backward(P, cfg->input, es == 2, vec, static_cast<hipStream_t>(stream)));
@@ -163,9 +177,9 @@ msgla_status msgla_recurrence_step(const msgla_recurrence_config* cfg, const msg
       !f32_ok(h_in) || !f32_ok(h_out))
     return MSGLA_ERR_INVALID_ARG;
   auto row_vec = [&](const msgla_rows* r) {  // stride_t is not read
-    return reinterpret_cast<uintptr_t>(r->data) % (4 * es) == 0 && r->stride_b % 4 == 0;
+    return reinterpret_cast<uintptr_t>(r->data) % (2 * es) == 0 && r->stride_b % 2 == 0;
   };
-  const bool vec = cfg->width % 4 == 0 && row_vec(x_t) && row_vec(z_t) && row_vec(y_t) && f32_vec(bias) &&
+  const bool vec = cfg->width % 2 == 0 && row_vec(x_t) && row_vec(z_t) && row_vec(y_t) && f32_vec(bias) &&
                    f32_vec(h_in) && f32_vec(h_out);
   RecParams P{};
   P.x = rows_of(x_t);
@@ -179,7 +193,7 @@ msgla_status msgla_recurrence_step(const msgla_recurrence_config* cfg, const msg
   P.L = 1;
   P.D = cfg->width;
   P.nch = 1;
-  P.slabs = cdiv(P.D, vec ? 256 : 64);
+  P.slabs = cdiv(P.D, vec ? 128 : 64);
   P.inv_gamma = 1.0f / cfg->gate_normalizer;
   if (!grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   HIP_TRY(launch_recurrence_step(P, cfg->input, es == 2, vec, static_cast<hipStream_t>(stream)));

@@ -2,17 +2,30 @@
 //
 //   log alpha_t = logsigmoid(z_t + b) / gamma,   h_t = alpha_t h_{t-1} + beta_t x_t
 //
-// Two affine maps h -> A h + H compose to (A2 A1, A2 H1 + H2), so the sequence
-// is cut into chunks of REC_CHUNK positions: one pass forms every chunk's map
-// (its decay product A and its state H from zero), a short pass runs the maps
-// one after the other per channel and leaves each chunk's entry state, and a
-// last pass walks the chunks again from those.  The backward's carry
-// c = alpha_{t+1} dh_{t+1} obeys the same recurrence from the other end with
-// the same decays, c -> A c + R, so its chunks are walked in the same passes.
-// A workgroup is one chunk of one slab of channels: wave w holds positions
-// 8 w .. 8 w + 7 of it in registers, all loads in flight at once, and the
-// waves' maps meet in LDS.  HBM-bound: a few tens of instructions an element
-// against 6 (forward) and 10 (backward) bytes of bf16.
+// Two affine maps h -> A h + H compose to (A2 A1, A2 H1 + H2), so a workgroup
+// reduces its REC_CHUNK positions of 64 VEC channels to one map (decay product
+// A, state from zero H) and needs only the state that enters it to finish: its
+// positions stay in registers meanwhile, and x and z are read once.  The maps
+// pass between workgroups through memory, one 64-bit word {A, H} a channel:
+// each workgroup publishes its own, then waits for those before it back to the
+// last group boundary (every REC_GROUP chunks) and for the state there, which
+// the group's last workgroup publishes.  So a sequence costs one wait per group
+// rather than one per chunk, and always the same sums in the same order.
+//   Every wait ends: a workgroup learns its chunk from a counter of its chain
+// (one sequence's slab of channels), so the chunks before it have workgroups
+// that are already running; those publish their maps before they wait, and wait
+// only for chunks still further back.
+//   The words need no fences: a word is one atomic store that carries all that
+// its reader wants, and starts as all ones, which no map is (a NaN decay is
+// stored as the quiet NaN).
+//   The backward's carry c = alpha_{t+1} dh_{t+1} obeys the same recurrence from
+// the other end, c -> A c + R.  It runs first the forward without y, which
+// leaves every chunk's entry state, then the chunks from the last to the first.
+// Bound by HBM and, nearly as much, by the gate's arithmetic (about 45 vector
+// instruction slots an element with NORM), which is why it is worth reading and
+// evaluating once.
+#include <type_traits>
+
 #include "device_common.hpp"
 #include "recurrence.hpp"
 
@@ -20,26 +33,30 @@ namespace msgla {
 
 namespace {
 
-constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
 // ---- one thread's VEC consecutive channels of a row --------------------------
 
 template <typename T, int VEC> struct RowLoad;
-template <> struct RowLoad<bf16, 4> {
+template <> struct RowLoad<bf16, 2> {
+  typedef uint32_t raw;
+  static __device__ __forceinline__ void unpack(raw r, float* f) {
+    f[0] = u2f(r << 16);
+    f[1] = u2f(r & 0xffff0000u);
+  }
+  static __device__ __forceinline__ raw pack(const float* f) {
+    typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+    return __builtin_bit_cast(uint32_t, bf16x2{(bf16)f[0], (bf16)f[1]});
+  }
+};
+template <> struct RowLoad<float, 2> {
   typedef u32x2 raw;
   static __device__ __forceinline__ void unpack(raw r, float* f) {
     const uint32_t a = r[0], b = r[1];
-    f[0] = u2f(a << 16);
-    f[1] = u2f(a & 0xffff0000u);
-    f[2] = u2f(b << 16);
-    f[3] = u2f(b & 0xffff0000u);
+    f[0] = u2f(a);
+    f[1] = u2f(b);
   }
-  static __device__ __forceinline__ raw pack(const float* f) { return pack8<bf16>(f); }
-};
-template <> struct RowLoad<float, 4> {
-  typedef u32x4 raw;
-  static __device__ __forceinline__ void unpack(raw r, float* f) { unpack16<float>(r, f); }
-  static __device__ __forceinline__ raw pack(const float* f) { return pack16<float>(f); }
+  static __device__ __forceinline__ raw pack(const float* f) { return pack8<float>(f); }
 };
 template <typename T> struct RowLoad<T, 1> {
   typedef T raw;
@@ -60,54 +77,50 @@ __device__ __forceinline__ void store_row(const RecRows& r, int64_t b, int t, in
 }
 
 template <int VEC> __device__ __forceinline__ void load_f32(const float* p, float* f) {
-  if constexpr (VEC == 4) unpack16<float>(ld16(p), f);
-  else f[0] = *p;
+  RowLoad<float, VEC>::unpack(*reinterpret_cast<const typename RowLoad<float, VEC>::raw*>(p), f);
 }
 template <int VEC> __device__ __forceinline__ void store_f32(float* p, const float* f) {
-  if constexpr (VEC == 4) st16(p, pack16<float>(f));
-  else *p = f[0];
+  *reinterpret_cast<typename RowLoad<float, VEC>::raw*>(p) = RowLoad<float, VEC>::pack(f);
 }
 
 // ---- the gate ------------------------------------------------------------------
 
-// -expm1(y) for y <= 0: the series to y^8 above -0.5 (its tail is below
-// 2^-26 of the sum there), 1 - e elsewhere, with e = exp(y) given.
+// -expm1(y) for y <= 0, given e = exp(y): the series to y^6 / 720 above -1/4 (its
+// next term is below 2^-24 of the sum there), 1 - e below, where e's rounding is
+// less than 2^-21 of the difference.
 __device__ __forceinline__ float neg_expm1(float y, float e) {
-  float s = 1.f + y * (1.f / 8.f);
-  s = 1.f + y * (1.f / 7.f) * s;
-  s = 1.f + y * (1.f / 6.f) * s;
-  s = 1.f + y * (1.f / 5.f) * s;
-  s = 1.f + y * (1.f / 4.f) * s;
-  s = 1.f + y * (1.f / 3.f) * s;
-  s = 1.f + y * (1.f / 2.f) * s;
-  return y > -0.5f ? -y * s : 1.f - e;
+  float s = y * (1.f / 720.f) + 1.f / 120.f;
+  s = s * y + 1.f / 24.f;
+  s = s * y + 1.f / 6.f;
+  s = s * y + 0.5f;
+  s = s * y + 1.f;
+  return y > -0.25f ? -y * s : 1.f - e;
 }
 
 struct Gate {
   float alpha, beta;
 };
 
-// E = exp(-|z|) gives both logs' pieces: logsigmoid(z) = min(z, 0) - log1p(E),
-// log1p(E) = 2 atanh(E / (2 + E)) by its series (E / (2 + E) <= 1/3: the terms
-// up to the 13th power leave 1e-8 of the sum), so small E keeps its relative
-// accuracy, which 1 - alpha hangs on.
+// With E = exp(-|z|), logsigmoid(z) = min(z, 0) - log(1 + E).  log2(1 + E) / E
+// on [0, 1] by a polynomial of degree 8 fitted to its relative error (3e-8), so
+// that a small E, which 1 - alpha hangs on, keeps its relative accuracy.
 template <int MODE> __device__ __forceinline__ Gate gate(float z, float inv_gamma, float& E) {
   E = __builtin_amdgcn_exp2f(-fabsf(z) * LOG2E);
-  const float s = E * __builtin_amdgcn_rcpf(2.f + E), w = s * s;
-  float q = 1.f / 13.f;
-  q = q * w + 1.f / 11.f;
-  q = q * w + 1.f / 9.f;
-  q = q * w + 1.f / 7.f;
-  q = q * w + 1.f / 5.f;
-  q = q * w + 1.f / 3.f;
-  const float la = (fminf(z, 0.f) - 2.f * (s + s * w * q)) * inv_gamma;
+  float q = 0.007549172880588877f;
+  q = q * E - 0.04256702485905678f;
+  q = q * E + 0.11285613290977259f;
+  q = q * E - 0.1971189186662436f;
+  q = q * E + 0.27564138814486205f;
+  q = q * E - 0.3584084662973025f;
+  q = q * E + 0.48069295654396693f;
+  q = q * E - 0.7213402079704885f;
+  q = q * E + 1.442694997434065f;
+  const float la = (fminf(z, 0.f) * LOG2E - E * q) * inv_gamma;  // log2 alpha; a NaN z comes back through E
   Gate g;
-  g.alpha = __builtin_amdgcn_exp2f(la * LOG2E);
+  g.alpha = __builtin_amdgcn_exp2f(la);
   if constexpr (MODE == 0) g.beta = 1.f;
-  if constexpr (MODE == 1) g.beta = neg_expm1(la, g.alpha);
-  if constexpr (MODE == 2) g.beta = sqrtf(neg_expm1(2.f * la, g.alpha * g.alpha));
-  // fminf drops a NaN z; the sum brings it back
-  if (z != z) g.alpha = g.beta = z;
+  if constexpr (MODE == 1) g.beta = neg_expm1(la * LN2, g.alpha);
+  if constexpr (MODE == 2) g.beta = __builtin_amdgcn_sqrtf(neg_expm1(la * (2.f * LN2), g.alpha * g.alpha));
   return g;
 }
 
@@ -115,324 +128,409 @@ template <int MODE> __device__ __forceinline__ Gate gate(float z, float inv_gamm
 template <int MODE> __device__ __forceinline__ float slope(const Gate& g) {
   if constexpr (MODE == 0) return 0.f;
   if constexpr (MODE == 1) return -g.alpha;
-  return g.beta == 0.f ? 0.f : -g.alpha * g.alpha / g.beta;
+  return g.beta == 0.f ? 0.f : -g.alpha * g.alpha * __builtin_amdgcn_rcpf(g.beta);
 }
 
-// ---- where a thread stands -----------------------------------------------------
+// ---- words between workgroups -----------------------------------------------------
 
-template <int VEC> struct Place {
-  int b, chunk, t0, c, cl;  // cl: the channel that is loaded where c is past the last
+constexpr uint64_t NOT_YET = ~0ull;
+
+__device__ __forceinline__ uint64_t make_word(float a, float h) {
+  const uint32_t u = a != a ? 0x7fc00000u : f2u(a);
+  return (uint64_t)u << 32 | f2u(h);
+}
+__device__ __forceinline__ void publish(uint64_t* p, uint64_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t await(uint64_t* p) {
+  uint64_t v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  while (v == NOT_YET) {
+    __builtin_amdgcn_s_sleep(1);
+    v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  return v;
+}
+__device__ __forceinline__ float word_a(uint64_t v) { return u2f((uint32_t)(v >> 32)); }
+__device__ __forceinline__ float word_h(uint64_t v) { return u2f((uint32_t)v); }
+
+// All words of the passes (16 bytes a thread), and their chains' counters.
+__global__ __launch_bounds__(256) void k_rec_init(uint64_t* words, int64_t pairs, uint32_t* counters, int64_t n) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < pairs) st16(words + 2 * i, u32x4{~0u, ~0u, ~0u, ~0u});
+  if (i < n) counters[i] = 0;
+}
+
+// ---- a chunk -------------------------------------------------------------------
+
+// Where a workgroup stands: `step` chunks have begun before it in its chain.
+template <int VEC, int NW> struct Place {
+  int b, step, lane, wave, c, cl;  // cl: the channel that is loaded where c is past the last
   bool on;
-  __device__ Place(const RecParams& P) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int slab = blockIdx.x % P.slabs, rest = blockIdx.x / P.slabs;
-    chunk = rest % P.nch;
-    b = rest / P.nch;
-    t0 = chunk * REC_CHUNK + wave * REC_T;
-    c = (slab * 64 + lane) * VEC;
+  __device__ Place(const RecParams& P, uint32_t* counters) {
+    __shared__ int ticket;
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int chains = P.slabs * P.B, chain = blockIdx.x % chains;
+    step = 0;
+    if (P.nch > 1) {
+      if (threadIdx.x == 0)
+        ticket = (int)__hip_atomic_fetch_add(&counters[chain], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __syncthreads();
+      step = __builtin_amdgcn_readfirstlane(ticket);
+    }
+    b = chain / P.slabs;
+    c = ((chain % P.slabs) * 64 + lane) * VEC;
     on = c < P.D;
     cl = on ? c : 0;
   }
 };
 
-template <int VEC> __device__ __forceinline__ void load_bias(const RecParams& P, int cl, float* bias) {
-#pragma unroll
-  for (int e = 0; e < VEC; ++e) bias[e] = 0.f;
-  if (P.bias) load_f32<VEC>(P.bias + cl, bias);
+// bit i: position t0 + i is a token (the same in every lane; lane i looks at its own)
+template <int NT> __device__ __forceinline__ uint32_t tokens(const RecParams& P, int b, int t0) {
+  const int lane = threadIdx.x & 63, t = t0 + lane;
+  const bool in = lane < NT && t < P.L;
+  return (uint32_t)__ballot(in && (!P.mask || P.mask[(int64_t)b * P.L + (in ? t : 0)]));
 }
 
-// bit i: position t0 + i is a token
-__device__ __forceinline__ uint32_t tokens(const RecParams& P, int b, int t0) {
-  uint32_t m = 0;
+// What enters the sequence, for the chunks of the first group.  Read before the
+// workgroup publishes its map: the chunk that writes the sequence's result, which
+// may go to the same memory, has waited for all of these.
+template <int VEC> __device__ __forceinline__ void load_begin(const float* p, int64_t at, int step, float* begin) {
 #pragma unroll
-  for (int i = 0; i < REC_T; ++i) {
-    const int t = t0 + i;
-    if (t < P.L && (!P.mask || P.mask[(int64_t)b * P.L + t])) m |= 1u << i;
-  }
-  return m;
+  for (int e = 0; e < VEC; ++e) begin[e] = 0.f;
+  if (p && step < REC_GROUP) load_f32<VEC>(p + at, begin);
 }
+
+// The value that enters chunk `step` of the chain: the state at the last group
+// boundary run through the maps since.  Wave w fetches map w (and w + NW, ..)
+// of the group; a barrier; every lane runs them.
+template <int VEC, int NW> struct Chain {
+  float a[REC_GROUP][64 * VEC], h[REC_GROUP][64 * VEC];
+
+  // maps: {A, H} words [step][D] of this sequence, ends: state words [group][D]
+  __device__ void fetch(const RecParams& P, const Place<VEC, NW>& at, uint64_t* maps, uint64_t* ends,
+                        const float* begin) {
+    const int g = at.step / REC_GROUP, n = at.step % REC_GROUP;
+    for (int k = at.wave; k <= n; k += NW)  // k == n: the state at the boundary
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float x = 1.f, y = begin[e];
+        if (at.on && k < n) {
+          const uint64_t v = await(maps + (int64_t)(g * REC_GROUP + k) * P.D + at.c + e);
+          x = word_a(v);
+          y = word_h(v);
+        } else if (at.on && g > 0) {
+          y = word_h(await(ends + (int64_t)(g - 1) * P.D + at.c + e));
+        }
+        a[k][e * 64 + at.lane] = x;
+        h[k][e * 64 + at.lane] = y;
+      }
+  }
+  __device__ void run(const Place<VEC, NW>& at, float* state) const {
+    const int n = at.step % REC_GROUP;
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      float s = h[n][e * 64 + at.lane];
+      for (int k = 0; k < n; ++k) s = a[k][e * 64 + at.lane] * s + h[k][e * 64 + at.lane];
+      state[e] = s;
+    }
+  }
+};
 
 // ---- forward ---------------------------------------------------------------------
 
-// OUT: walk the chunk from its entry state and write y; otherwise write its map.
-template <typename T, int VEC, int MODE, bool OUT>
-__global__ __launch_bounds__(64 * REC_WAVES) void k_rec_forward(const RecParams P) {
-  __shared__ float sA[REC_WAVES][64 * VEC], sH[REC_WAVES][64 * VEC];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Place<VEC> at(P);
-  float bias[VEC], entry[VEC];
-  load_bias<VEC>(P, at.cl, bias);
-  const int64_t ch = ((int64_t)at.b * P.nch + at.chunk) * P.D + at.cl;
+// Y: writes y and h_out.  Otherwise leaves the chunks' entry states for the backward.
+template <typename T, int VEC, int MODE, bool Y>
+__global__ __launch_bounds__(64 * REC_FWD_WAVES) void k_rec_forward(const RecParams P) {
+  constexpr int NW = REC_FWD_WAVES, NT = REC_CHUNK / NW;
+  __shared__ float sA[NW][64 * VEC], sH[NW][64 * VEC];
+  __shared__ Chain<VEC, NW> chain;
+  const Place<VEC, NW> at(P, P.counters);
+  const int t0 = at.step * REC_CHUNK + at.wave * NT;
+  float bias[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) entry[e] = 0.f;
-  if constexpr (OUT) {
-    if (P.nch > 1) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) entry[e] = P.agg[2 * (ch + e) + 1];
-    } else if (P.h_in) {
-      load_f32<VEC>(P.h_in + (int64_t)at.b * P.D + at.cl, entry);
-    }
-  }
-  typename RowLoad<T, VEC>::raw rx[REC_T], rz[REC_T];
-#pragma unroll
-  for (int i = 0; i < REC_T; ++i) {
-    const int t = min(at.t0 + i, P.L - 1);
-    rx[i] = load_row<T, VEC>(P.x, at.b, t, at.cl);
-    rz[i] = load_row<T, VEC>(P.z, at.b, t, at.cl);
-  }
-  const uint32_t tok = tokens(P, at.b, at.t0);
-  float A[VEC], H[VEC], al[REC_T][VEC], u[REC_T][VEC];
+  for (int e = 0; e < VEC; ++e) bias[e] = 0.f;
+  if (P.bias) load_f32<VEC>(P.bias + at.cl, bias);
+  const uint32_t tok = tokens<NT>(P, at.b, t0);
+  float A[VEC], H[VEC], al[NT][VEC], u[NT][VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) A[e] = 1.f, H[e] = 0.f;
+  if (tok) {
+    typename RowLoad<T, VEC>::raw rx[NT], rz[NT];
 #pragma unroll
-  for (int i = 0; i < REC_T; ++i) {
-    float x[VEC], z[VEC];
-    RowLoad<T, VEC>::unpack(rx[i], x);
-    RowLoad<T, VEC>::unpack(rz[i], z);
-    const bool on = tok >> i & 1;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float E;
-      const Gate g = gate<MODE>(z[e] + bias[e], P.inv_gamma, E);
-      al[i][e] = on ? g.alpha : 1.f;
-      u[i][e] = on ? g.beta * x[e] : 0.f;
-      A[e] *= al[i][e];
-      H[e] = al[i][e] * H[e] + u[i][e];
+    for (int i = 0; i < NT; ++i) {
+      const int t = min(t0 + i, P.L - 1);
+      rx[i] = load_row<T, VEC>(P.x, at.b, t, at.cl);
+      rz[i] = load_row<T, VEC>(P.z, at.b, t, at.cl);
     }
-  }
+    auto walk = [&](auto full) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) sA[wave][e * 64 + lane] = A[e], sH[wave][e * 64 + lane] = H[e];
-  __syncthreads();
-  if constexpr (!OUT) {
-    if (wave != 0 || !at.on) return;
+      for (int i = 0; i < NT; ++i) {
+        float x[VEC], z[VEC];
+        RowLoad<T, VEC>::unpack(rx[i], x);
+        RowLoad<T, VEC>::unpack(rz[i], z);
+        const bool on = full.value || (tok >> i & 1);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float a = A[e], h = H[e];
-#pragma unroll
-      for (int w = 1; w < REC_WAVES; ++w) {
-        const float aw = sA[w][e * 64 + lane];
-        h = aw * h + sH[w][e * 64 + lane];
-        a *= aw;
+        for (int e = 0; e < VEC; ++e) {
+          float E;
+          const Gate g = gate<MODE>(z[e] + bias[e], P.inv_gamma, E);
+          al[i][e] = on ? g.alpha : 1.f;
+          u[i][e] = on ? g.beta * x[e] : 0.f;
+          A[e] *= al[i][e];
+          H[e] = al[i][e] * H[e] + u[i][e];
+        }
       }
-      P.agg[2 * (ch + e)] = a;
-      P.agg[2 * (ch + e) + 1] = h;
-    }
+    };
+    if (tok == (1u << NT) - 1) walk(std::true_type());
+    else walk(std::false_type());
+  }
+  float state[VEC], begin[VEC];
+  const int64_t seq = (int64_t)at.b * P.D + at.cl;
+  load_begin<VEC>(P.h_in, seq, at.step, begin);
+  uint64_t* maps = P.maps + (int64_t)at.b * P.nch * P.D;
+  uint64_t* ends = P.ends + (int64_t)at.b * P.groups * P.D;
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) sA[at.wave][e * 64 + at.lane] = A[e], sH[at.wave][e * 64 + at.lane] = H[e];
+  if (P.nch == 1) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) state[e] = begin[e];
+    __syncthreads();
   } else {
-    float h[VEC];
+    __syncthreads();
+    if (at.wave == 0 && at.step + 1 < P.nch) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float a = A[e], h = H[e];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+          const float aw = sA[w][e * 64 + at.lane];
+          h = aw * h + sH[w][e * 64 + at.lane];
+          a *= aw;
+        }
+        if (at.on) publish(maps + (int64_t)at.step * P.D + at.c + e, make_word(a, h));
+      }
+    }
+    chain.fetch(P, at, maps, ends, begin);
+    __syncthreads();
+    chain.run(at, state);
+  }
+  if constexpr (!Y) {
+    if (at.wave == 0 && at.on) store_f32<VEC>(P.entry + ((int64_t)at.b * P.nch + at.step) * P.D + at.c, state);
+  }
+  // the state that leaves the chunk goes out first: others wait for it
+  const bool boundary = at.step % REC_GROUP == REC_GROUP - 1 && at.step + 1 < P.nch;
+  const bool final = Y && at.step == P.nch - 1 && P.h_out;
+  float h[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    h[e] = state[e];
+    for (int w = 0; w < at.wave; ++w) h[e] = sA[w][e * 64 + at.lane] * h[e] + sH[w][e * 64 + at.lane];
+  }
+  if (at.wave == NW - 1 && at.on && (boundary || final)) {
+    float end[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      h[e] = entry[e];
-      for (int w = 0; w < wave; ++w) h[e] = sA[w][e * 64 + lane] * h[e] + sH[w][e * 64 + lane];
+      end[e] = A[e] * h[e] + H[e];
+      if (boundary) publish(ends + (int64_t)(at.step / REC_GROUP) * P.D + at.c + e, make_word(0.f, end[e]));
     }
+    if (final) store_f32<VEC>(P.h_out + (int64_t)at.b * P.D + at.c, end);
+  }
+  if constexpr (Y) {
     if (!at.on) return;
 #pragma unroll
-    for (int i = 0; i < REC_T; ++i) {
+    for (int i = 0; i < NT; ++i) {
       float y[VEC];
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        h[e] = al[i][e] * h[e] + u[i][e];
+        if (tok) h[e] = al[i][e] * h[e] + u[i][e];
         y[e] = tok >> i & 1 ? h[e] : 0.f;
       }
-      if (at.t0 + i < P.L) store_row<T, VEC>(P.y, at.b, at.t0 + i, at.c, y);
+      if (t0 + i < P.L) store_row<T, VEC>(P.y, at.b, t0 + i, at.c, y);
     }
-    if (P.nch == 1 && P.h_out && wave == REC_WAVES - 1) store_f32<VEC>(P.h_out + (int64_t)at.b * P.D + at.c, h);
-  }
-}
-
-// Runs the chunks' maps per channel: agg's second entry becomes the chunk's
-// entry state and, backward, rev the carry that enters it from the right.
-template <bool BACKWARD> __global__ __launch_bounds__(64) void k_rec_carry(const RecParams P) {
-  const int64_t i = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  if (i >= (int64_t)P.B * P.D) return;
-  const int64_t b = i / P.D, c = i - b * P.D;
-  float2* agg = reinterpret_cast<float2*>(P.agg) + b * P.nch * P.D + c;
-  constexpr int AHEAD = 8;
-  if (!BACKWARD || P.nch > 1) {
-    float h = P.h_in ? P.h_in[i] : 0.f;
-    for (int k0 = 0; k0 < P.nch; k0 += AHEAD) {
-      float2 m[AHEAD];
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) m[k] = agg[(int64_t)min(k0 + k, P.nch - 1) * P.D];
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (k0 + k < P.nch) {
-          agg[(int64_t)(k0 + k) * P.D].y = h;
-          h = m[k].x * h + m[k].y;
-        }
-    }
-    if (!BACKWARD && P.h_out) P.h_out[i] = h;
-  }
-  if constexpr (BACKWARD) {
-    float* rev = P.rev + b * P.nch * P.D + c;
-    float r = P.dh_out ? P.dh_out[i] : 0.f;
-    for (int k0 = P.nch - 1; k0 >= 0; k0 -= AHEAD) {
-      float a[AHEAD], m[AHEAD];
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k) {
-        const int64_t at = (int64_t)max(k0 - k, 0) * P.D;
-        a[k] = agg[at].x;
-        m[k] = rev[at];
-      }
-#pragma unroll
-      for (int k = 0; k < AHEAD; ++k)
-        if (k0 - k >= 0) {
-          rev[(int64_t)(k0 - k) * P.D] = r;
-          r = a[k] * r + m[k];
-        }
-    }
-    if (P.dh_in) P.dh_in[i] = r;
   }
 }
 
 // ---- backward --------------------------------------------------------------------
 
-template <typename T, int VEC, int MODE, bool OUT>
-__global__ __launch_bounds__(64 * REC_WAVES) void k_rec_backward(const RecParams P) {
-  __shared__ float sA[REC_WAVES][64 * VEC], sH[REC_WAVES][64 * VEC], sR[REC_WAVES][64 * VEC];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const Place<VEC> at(P);
-  float bias[VEC], entry[VEC], carry[VEC];
-  load_bias<VEC>(P, at.cl, bias);
-  const int64_t ch = ((int64_t)at.b * P.nch + at.chunk) * P.D + at.cl, bd = (int64_t)at.b * P.D + at.cl;
+// Chunks from the last to the first; P.entry holds their entry states.
+template <typename T, int VEC, int MODE>
+__global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecParams P) {
+  constexpr int NW = REC_BWD_WAVES, NT = REC_CHUNK / NW;
+  __shared__ float sA[NW][64 * VEC], sH[NW][64 * VEC], sR[NW][64 * VEC];
+  __shared__ Chain<VEC, NW> chain;
+  const Place<VEC, NW> at(P, P.counters + (int64_t)P.slabs * P.B);
+  const int chunk = P.nch - 1 - at.step, t0 = chunk * REC_CHUNK + at.wave * NT;
+  const int64_t seq = (int64_t)at.b * P.D + at.cl, ch = ((int64_t)at.b * P.nch + chunk) * P.D + at.cl;
+  float bias[VEC], state[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) entry[e] = carry[e] = 0.f;
-  if constexpr (OUT) {
-    if (P.nch > 1) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) entry[e] = P.agg[2 * (ch + e) + 1];
-      load_f32<VEC>(P.rev + ch, carry);
-    } else {
-      if (P.h_in) load_f32<VEC>(P.h_in + bd, entry);
-      if (P.dh_out) load_f32<VEC>(P.dh_out + bd, carry);
-    }
-  }
-  typename RowLoad<T, VEC>::raw rx[REC_T], rz[REC_T], rd[REC_T];
-#pragma unroll
-  for (int i = 0; i < REC_T; ++i) {
-    const int t = min(at.t0 + i, P.L - 1);
-    rx[i] = load_row<T, VEC>(P.x, at.b, t, at.cl);
-    rz[i] = load_row<T, VEC>(P.z, at.b, t, at.cl);
-    rd[i] = typename RowLoad<T, VEC>::raw{};
-    if (P.dy.p) rd[i] = load_row<T, VEC>(P.dy, at.b, t, at.cl);
-  }
-  const uint32_t tok = tokens(P, at.b, at.t0);
-  const uint32_t tod = P.dy.p ? tok : 0u;  // where dy counts
-  float A[VEC], H[VEC], R[VEC], al[REC_T][VEC];
+  for (int e = 0; e < VEC; ++e) bias[e] = state[e] = 0.f;
+  if (P.bias) load_f32<VEC>(P.bias + at.cl, bias);
+  if (P.nch > 1) load_f32<VEC>(P.entry + ch, state);
+  else if (P.h_in) load_f32<VEC>(P.h_in + seq, state);
+  const uint32_t tok = tokens<NT>(P, at.b, t0);
+  // per position: alpha, dbeta/dlog alpha x, sigmoid(-z) / gamma, beta, dy
+  float A[VEC], H[VEC], R[VEC], al[NT][VEC], be[NT][VEC], sl[NT][VEC], sg[NT][VEC], dy[NT][VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) A[e] = 1.f, H[e] = R[e] = 0.f;
+  typename RowLoad<T, VEC>::raw rx[NT];
+  if (tok) {
+    typename RowLoad<T, VEC>::raw rz[NT], rd[NT];
 #pragma unroll
-  for (int i = 0; i < REC_T; ++i) {
-    float x[VEC], z[VEC], d[VEC];
-    RowLoad<T, VEC>::unpack(rx[i], x);
-    RowLoad<T, VEC>::unpack(rz[i], z);
-    RowLoad<T, VEC>::unpack(rd[i], d);
-    const bool on = tok >> i & 1;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float E;
-      const Gate g = gate<MODE>(z[e] + bias[e], P.inv_gamma, E);
-      const float a = on ? g.alpha : 1.f;
-      al[i][e] = a;
-      A[e] *= a;
-      H[e] = a * H[e] + (on ? g.beta * x[e] : 0.f);
-      R[e] += A[e] * (tod >> i & 1 ? d[e] : 0.f);  // dy_t reaches the front through alpha_{t0} .. alpha_t
+    for (int i = 0; i < NT; ++i) {
+      const int t = min(t0 + i, P.L - 1);
+      rx[i] = load_row<T, VEC>(P.x, at.b, t, at.cl);
+      rz[i] = load_row<T, VEC>(P.z, at.b, t, at.cl);
+      rd[i] = typename RowLoad<T, VEC>::raw{};
+      if (P.dy.p) rd[i] = load_row<T, VEC>(P.dy, at.b, t, at.cl);
     }
-  }
+    auto walk = [&](auto full) {
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) {
-    sA[wave][e * 64 + lane] = A[e];
-    sH[wave][e * 64 + lane] = H[e];
-    sR[wave][e * 64 + lane] = R[e];
-  }
-  __syncthreads();
-  if constexpr (!OUT) {
-    if (wave != 0 || !at.on) return;
+      for (int i = 0; i < NT; ++i) {
+        float x[VEC], z[VEC], d[VEC];
+        RowLoad<T, VEC>::unpack(rx[i], x);
+        RowLoad<T, VEC>::unpack(rz[i], z);
+        RowLoad<T, VEC>::unpack(rd[i], d);
+        const bool on = full.value || (tok >> i & 1);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float a = A[e], h = H[e], r = R[e];
-#pragma unroll
-      for (int w = 1; w < REC_WAVES; ++w) {
-        const float aw = sA[w][e * 64 + lane];
-        h = aw * h + sH[w][e * 64 + lane];
-        r += a * sR[w][e * 64 + lane];
-        a *= aw;
+        for (int e = 0; e < VEC; ++e) {
+          const float zb = z[e] + bias[e];
+          float E;
+          const Gate g = gate<MODE>(zb, P.inv_gamma, E);
+          al[i][e] = on ? g.alpha : 1.f;
+          be[i][e] = on ? g.beta : 0.f;
+          sl[i][e] = on ? slope<MODE>(g) * x[e] : 0.f;
+          sg[i][e] = on ? (zb < 0.f ? 1.f : E) * __builtin_amdgcn_rcpf(1.f + E) * P.inv_gamma : 0.f;
+          dy[i][e] = on ? d[e] : 0.f;
+          A[e] *= al[i][e];
+          H[e] = al[i][e] * H[e] + (on ? g.beta * x[e] : 0.f);
+          R[e] += A[e] * dy[i][e];  // dy_t reaches the front through alpha_{t0} .. alpha_t
+        }
       }
-      P.agg[2 * (ch + e)] = a;
-      P.agg[2 * (ch + e) + 1] = h;
-      P.rev[ch + e] = r;
-    }
-    return;
+    };
+    if (tok == (1u << NT) - 1) walk(std::true_type());
+    else walk(std::false_type());
   }
-  float h[VEC], cr[VEC], hb[REC_T][VEC], db[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
-    h[e] = entry[e];
-    for (int w = 0; w < wave; ++w) h[e] = sA[w][e * 64 + lane] * h[e] + sH[w][e * 64 + lane];
-    cr[e] = carry[e];
-    for (int w = REC_WAVES - 1; w > wave; --w) cr[e] = sA[w][e * 64 + lane] * cr[e] + sR[w][e * 64 + lane];
+    sA[at.wave][e * 64 + at.lane] = A[e];
+    sH[at.wave][e * 64 + at.lane] = H[e];
+    sR[at.wave][e * 64 + at.lane] = R[e];
+  }
+  float carry[VEC], begin[VEC];
+  load_begin<VEC>(P.dh_out, seq, at.step, begin);
+  uint64_t* maps = P.rmaps + (int64_t)at.b * P.nch * P.D;
+  uint64_t* ends = P.rends + (int64_t)at.b * P.groups * P.D;
+  if (P.nch == 1) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) carry[e] = begin[e];
+    __syncthreads();
+  } else {
+    __syncthreads();
+    if (at.wave == 0 && at.step + 1 < P.nch) {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        float a = A[e], r = R[e];
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+          r += a * sR[w][e * 64 + at.lane];
+          a *= sA[w][e * 64 + at.lane];
+        }
+        if (at.on) publish(maps + (int64_t)at.step * P.D + at.c + e, make_word(a, r));
+      }
+    }
+    chain.fetch(P, at, maps, ends, begin);
+    __syncthreads();
+    chain.run(at, carry);
+  }
+#pragma unroll
+  for (int e = 0; e < VEC; ++e)
+    for (int w = NW - 1; w > at.wave; --w) carry[e] = sA[w][e * 64 + at.lane] * carry[e] + sR[w][e * 64 + at.lane];
+  const bool boundary = at.step % REC_GROUP == REC_GROUP - 1 && at.step + 1 < P.nch;
+  const bool final = chunk == 0 && P.dh_in;
+  if (at.wave == 0 && at.on && (boundary || final)) {
+    float front[VEC];
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      front[e] = A[e] * carry[e] + R[e];
+      if (boundary) publish(ends + (int64_t)(at.step / REC_GROUP) * P.D + at.c + e, make_word(0.f, front[e]));
+    }
+    if (final) store_f32<VEC>(P.dh_in + seq, front);
+  }
+  float h[VEC], hb[NT][VEC], db[VEC];
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) {
+    h[e] = state[e];
+    for (int w = 0; w < at.wave; ++w) h[e] = sA[w][e * 64 + at.lane] * h[e] + sH[w][e * 64 + at.lane];
     db[e] = 0.f;
   }
-  // states before each position, then the gradients from the last to the first
+  if (tok) {
+    // alpha_t h_{t-1} + slope x, then the gradients from the last position to the first
 #pragma unroll
-  for (int i = 0; i < REC_T; ++i) {
-    float x[VEC], z[VEC];
-    RowLoad<T, VEC>::unpack(rx[i], x);
-    RowLoad<T, VEC>::unpack(rz[i], z);
+    for (int i = 0; i < NT; ++i) {
+      float x[VEC];
+      RowLoad<T, VEC>::unpack(rx[i], x);
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      float E;
-      const Gate g = gate<MODE>(z[e] + bias[e], P.inv_gamma, E);
-      hb[i][e] = h[e];
-      h[e] = al[i][e] * h[e] + (tok >> i & 1 ? g.beta * x[e] : 0.f);
+      for (int e = 0; e < VEC; ++e) {
+        const float decayed = al[i][e] * h[e];
+        hb[i][e] = (decayed + sl[i][e]) * sg[i][e];
+        h[e] = decayed + (tok >> i & 1 ? be[i][e] * x[e] : 0.f);
+      }
     }
   }
 #pragma unroll
-  for (int i = REC_T - 1; i >= 0; --i) {
-    float x[VEC], z[VEC], d[VEC], dx[VEC], dz[VEC];
-    RowLoad<T, VEC>::unpack(rx[i], x);
-    RowLoad<T, VEC>::unpack(rz[i], z);
-    RowLoad<T, VEC>::unpack(rd[i], d);
-    const bool on = tok >> i & 1;
+  for (int k = 0; k < NT; ++k) {
+    const int i = NT - 1 - k;
+    float dx[VEC], dz[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float zb = z[e] + bias[e];
-      float E;
-      const Gate g = gate<MODE>(zb, P.inv_gamma, E);
-      const float sig = (zb < 0.f ? 1.f : E) * __builtin_amdgcn_rcpf(1.f + E);  // sigmoid(-zb)
-      const float dh = cr[e] + (tod >> i & 1 ? d[e] : 0.f);
-      dx[e] = on ? g.beta * dh : 0.f;
-      dz[e] = on ? dh * (g.alpha * hb[i][e] + slope<MODE>(g) * x[e]) * (sig * P.inv_gamma) : 0.f;
-      db[e] += dz[e];
-      cr[e] = al[i][e] * dh;
+      dx[e] = dz[e] = 0.f;
+      if (tok) {
+        const float dh = carry[e] + dy[i][e];
+        const bool on = tok >> i & 1;
+        dx[e] = on ? be[i][e] * dh : 0.f;
+        dz[e] = on ? dh * hb[i][e] : 0.f;
+        db[e] += dz[e];
+        carry[e] = al[i][e] * dh;
+      }
     }
-    if (at.on && at.t0 + i < P.L) {
-      store_row<T, VEC>(P.dx, at.b, at.t0 + i, at.c, dx);
-      store_row<T, VEC>(P.dz, at.b, at.t0 + i, at.c, dz);
+    if (at.on && t0 + i < P.L) {
+      store_row<T, VEC>(P.dx, at.b, t0 + i, at.c, dx);
+      store_row<T, VEC>(P.dz, at.b, t0 + i, at.c, dz);
     }
   }
-  if (P.nch == 1 && P.dh_in && wave == 0 && at.on) store_f32<VEC>(P.dh_in + bd, cr);
   if (!P.dbias) return;
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) sA[wave][e * 64 + lane] = db[e];
+  for (int e = 0; e < VEC; ++e) sH[at.wave][e * 64 + at.lane] = db[e];
   __syncthreads();
-  if (wave == 0 && at.on) {
+  if (at.wave == 0 && at.on) {
 #pragma unroll
-    for (int w = 1; w < REC_WAVES; ++w)
+    for (int w = 1; w < NW; ++w)
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) db[e] += sA[w][e * 64 + lane];
+      for (int e = 0; e < VEC; ++e) db[e] += sH[w][e * 64 + at.lane];
     store_f32<VEC>(P.dbp + ch, db);
   }
 }
 
-// dbias: the partials of all chunks of all sequences, in 64 bits and a fixed order
+// dbias: the partials of all chunks of all sequences, in 64 bits and a fixed
+// order.  16 waves take every 16th row of 64 channels, four loads in flight.
 __global__ __launch_bounds__(1024) void k_rec_dbias(const RecParams P) {
   __shared__ double part[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
   const int64_t n = (int64_t)P.B * P.nch;
   double s = 0.0;
-  if (c < P.D)
-    for (int64_t i = wave; i < n; i += 16) s += (double)P.dbp[i * P.D + c];
+  if (c < P.D) {
+    const float* p = P.dbp + c;
+    int64_t i = wave;
+    for (; i + 48 < n; i += 64) {
+      float v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = p[(i + 16 * k) * P.D];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s += (double)v[k];
+    }
+    for (; i < n; i += 16) s += (double)p[i * P.D];
+  }
   part[wave][lane] = s;
   __syncthreads();
   if (wave || c >= P.D) return;
@@ -447,7 +545,9 @@ template <typename T, int VEC, int MODE> __global__ __launch_bounds__(64) void k
   if (c >= P.D) return;
   float bias[VEC], h[VEC], x[VEC], z[VEC], y[VEC];
   const auto rx = load_row<T, VEC>(P.x, b, 0, c), rz = load_row<T, VEC>(P.z, b, 0, c);
-  load_bias<VEC>(P, c, bias);
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) bias[e] = 0.f;
+  if (P.bias) load_f32<VEC>(P.bias + c, bias);
   load_f32<VEC>(P.h_in + (int64_t)b * P.D + c, h);
   const bool on = !P.mask || P.mask[b];
   RowLoad<T, VEC>::unpack(rx, x);
@@ -465,21 +565,22 @@ template <typename T, int VEC, int MODE> __global__ __launch_bounds__(64) void k
 }
 
 template <typename T, int VEC, int MODE> struct Launch {
+  static dim3 grid(const RecParams& P) { return dim3((unsigned)((int64_t)P.slabs * P.nch * P.B)); }
+  static void init(const RecParams& P, hipStream_t st) {
+    const int64_t pairs = P.words / 2, chains = 2 * (int64_t)P.slabs * P.B;
+    const int64_t n = pairs > chains ? pairs : chains;
+    hipLaunchKernelGGL(k_rec_init, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, st, P.maps, pairs, P.counters, chains);
+  }
   static void forward(const RecParams& P, hipStream_t st) {
-    const dim3 grid((unsigned)(P.slabs * P.nch * P.B)), block(64 * REC_WAVES);
-    if (P.nch > 1) {
-      hipLaunchKernelGGL((k_rec_forward<T, VEC, MODE, false>), grid, block, 0, st, P);
-      hipLaunchKernelGGL(k_rec_carry<false>, dim3((unsigned)(((int64_t)P.B * P.D + 63) / 64)), dim3(64), 0, st, P);
-    }
-    hipLaunchKernelGGL((k_rec_forward<T, VEC, MODE, true>), grid, block, 0, st, P);
+    if (P.nch > 1) init(P, st);
+    hipLaunchKernelGGL((k_rec_forward<T, VEC, MODE, true>), grid(P), dim3(64 * REC_FWD_WAVES), 0, st, P);
   }
   static void backward(const RecParams& P, hipStream_t st) {
-    const dim3 grid((unsigned)(P.slabs * P.nch * P.B)), block(64 * REC_WAVES);
     if (P.nch > 1) {
-      hipLaunchKernelGGL((k_rec_backward<T, VEC, MODE, false>), grid, block, 0, st, P);
-      hipLaunchKernelGGL(k_rec_carry<true>, dim3((unsigned)(((int64_t)P.B * P.D + 63) / 64)), dim3(64), 0, st, P);
+      init(P, st);
+      hipLaunchKernelGGL((k_rec_forward<T, VEC, MODE, false>), grid(P), dim3(64 * REC_FWD_WAVES), 0, st, P);
     }
-    hipLaunchKernelGGL((k_rec_backward<T, VEC, MODE, true>), grid, block, 0, st, P);
+    hipLaunchKernelGGL((k_rec_backward<T, VEC, MODE>), grid(P), dim3(64 * REC_BWD_WAVES), 0, st, P);
     if (P.dbias) hipLaunchKernelGGL(k_rec_dbias, dim3((P.D + 63) / 64), dim3(1024), 0, st, P);
   }
   static void step(const RecParams& P, hipStream_t st) {
@@ -494,8 +595,8 @@ template <typename T, int VEC, class F> void by_mode(int input, F f) {
   else f(Launch<T, VEC, 2>());
 }
 template <class F> void dispatch(int input, bool bf16_path, bool vec, F f) {
-  if (bf16_path) vec ? by_mode<bf16, 4>(input, f) : by_mode<bf16, 1>(input, f);
-  else vec ? by_mode<float, 4>(input, f) : by_mode<float, 1>(input, f);
+  if (bf16_path) vec ? by_mode<bf16, 2>(input, f) : by_mode<bf16, 1>(input, f);
+  else vec ? by_mode<float, 2>(input, f) : by_mode<float, 1>(input, f);
 }
 
 }  // namespace

@@ -10,9 +10,10 @@ struct RecRows {
   int64_t sb, st;  // element strides of a sequence and of a position
 };
 
-// A workgroup takes REC_CHUNK positions: REC_WAVES waves of REC_T positions
-// each, all on the same channels.
-constexpr int REC_T = 8, REC_WAVES = 8, REC_CHUNK = REC_T * REC_WAVES;
+// A workgroup takes REC_CHUNK positions, its waves equal parts of them one after
+// the other (fewer a wave backward, which keeps five values of each); every
+// REC_GROUP chunks the state itself passes between workgroups.
+constexpr int REC_CHUNK = 128, REC_FWD_WAVES = 8, REC_BWD_WAVES = 16, REC_GROUP = 16;
 
 struct RecParams {
   RecRows x, z, y;    // y: the forward's output
@@ -24,10 +25,13 @@ struct RecParams {
   const float* dh_out;
   float* dbias;
   float* dh_in;
-  float* agg;      // [B][nch][D][2]: a chunk's decay product and its state from zero, then its entry state
-  float* rev;      // [B][nch][D]: a chunk's gradient carry from zero, then the carry that enters it
-  float* dbp;      // [B * nch][D]: dbias partials
-  int B, L, D, nch, slabs;
+  uint64_t *maps, *ends;    // [B][nch][D] chunk maps {A, H}, [B][groups][D] states {0, h}
+  uint64_t *rmaps, *rends;  // the same from the other end; the four lie one after the other
+  int64_t words;            // of the four (forward: of the two)
+  uint32_t* counters;       // [2][B slabs] chunks begun, forward and backward
+  float* entry;             // [B][nch][D] states that enter the chunks, for the backward
+  float* dbp;               // [B nch][D] dbias partials
+  int B, L, D, nch, groups, slabs;
   float inv_gamma;
 };
 
