@@ -22,8 +22,9 @@ bool rec_batch_ok(int64_t B, int64_t L) {
 
 struct RecWs {
   size_t words, counters, entry, dbp, total;
-  int nch, groups;
-  int64_t n_maps, n_ends;  // words of one direction
+  int nch, groups, nchb, groupsb;
+  int64_t row;      // channels of a batch
+  int64_t n_words;  // words of all chunks and groups
 };
 
 RecWs rec_ws(const msgla_recurrence_config* c, int64_t B, int64_t L, bool backward) {
@@ -35,33 +36,36 @@ RecWs rec_ws(const msgla_recurrence_config* c, int64_t B, int64_t L, bool backwa
     return o;
   };
   w.nch = (int)((L + REC_CHUNK - 1) / REC_CHUNK);
-  w.groups = (w.nch + REC_GROUP - 1) / REC_GROUP;
-  const int64_t row = B * (int64_t)c->width;
-  w.n_maps = row * w.nch;
-  w.n_ends = row * w.groups;
-  if (w.nch > 1) {
-    w.words = take((size_t)((backward ? 2 : 1) * (w.n_maps + w.n_ends) + 1) * 8);  // an even number is cleared
+  w.groups = cdiv(w.nch, REC_GROUP);
+  w.nchb = backward ? (int)((L + REC_BCHUNK - 1) / REC_BCHUNK) : 0;
+  w.groupsb = cdiv(w.nchb, REC_GROUP);
+  const int64_t row = w.row = B * (int64_t)c->width;
+  w.n_words = (row * ((int64_t)w.nch + w.groups + w.nchb + w.groupsb) + 1) / 2 * 2;  // an even number is cleared
+  if (w.nch > 1 || w.nchb > 1) {
+    w.words = take((size_t)w.n_words * 8);
     w.counters = take((size_t)B * cdiv(c->width, 64) * 8);
-    if (backward) w.entry = take((size_t)w.n_maps * 4);
   }
-  if (backward) w.dbp = take((size_t)w.n_maps * 4);
+  if (w.nchb > 1) w.entry = take((size_t)row * w.nchb * 4);
+  if (backward) w.dbp = take((size_t)row * w.nchb * 4);
   w.total = cur;
   return w;
 }
 
-void set_ws(RecParams& P, const RecWs& w, void* ws, bool backward) {
+void set_ws(RecParams& P, const RecWs& w, void* ws) {
   P.nch = w.nch;
   P.groups = w.groups;
-  if (w.nch > 1) {
+  P.nchb = w.nchb;
+  P.groupsb = w.groupsb;
+  if (w.nch > 1 || w.nchb > 1) {
     P.maps = at<uint64_t>(ws, w.words);
-    P.ends = P.maps + w.n_maps;
-    P.rmaps = P.ends + w.n_ends;
-    P.rends = P.rmaps + w.n_maps;
-    P.words = ((backward ? 2 : 1) * (w.n_maps + w.n_ends) + 1) / 2 * 2;
+    P.ends = P.maps + w.row * w.nch;
+    P.rmaps = P.ends + w.row * w.groups;
+    P.rends = P.rmaps + w.row * w.nchb;
+    P.words = w.n_words;
     P.counters = at<uint32_t>(ws, w.counters);
-    P.entry = at<float>(ws, w.entry);
   }
-  if (backward) P.dbp = at<float>(ws, w.dbp);
+  if (w.nchb > 1) P.entry = at<float>(ws, w.entry);
+  if (w.nchb > 0) P.dbp = at<float>(ws, w.dbp);
 }
 
 bool rows_ok(const msgla_rows* r, int es) {
@@ -80,7 +84,7 @@ bool rows_vec(const msgla_rows* r, int es) {
 bool f32_vec(const void* p) { return reinterpret_cast<uintptr_t>(p) % 8 == 0; }
 
 // One workgroup takes 64 lanes' channels; the grid is one-dimensional.
-bool grid_ok(const RecParams& P) { return (int64_t)P.slabs * P.nch * P.B <= 0x7fffffff; }
+bool grid_ok(const RecParams& P) { return (int64_t)P.slabs * std::max(P.nch, P.nchb) * P.B <= 0x7fffffff; }
 
 }  // namespace
 
@@ -119,7 +123,7 @@ msgla_status msgla_recurrence_forward(const msgla_recurrence_config* cfg, const 
   P.B = (int)B;
   P.L = (int)L;
   P.D = cfg->width;
-  set_ws(P, w, workspace, false);
+  set_ws(P, w, workspace);
   P.slabs = cdiv(P.D, vec ? 128 : 64);
   P.inv_gamma = 1.0f / cfg->gate_normalizer;
   if (!grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
@@ -156,7 +160,7 @@ msgla_status msgla_recurrence_backward(const msgla_recurrence_config* cfg, const
   P.dh_out = dh_out;
   P.dbias = dbias;
   P.dh_in = dh_in;
-  set_ws(P, w, workspace, true);
+  set_ws(P, w, workspace);
   P.B = (int)B;
   P.L = (int)L;
   P.D = cfg->width;

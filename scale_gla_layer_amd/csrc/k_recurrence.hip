@@ -98,7 +98,7 @@ __device__ __forceinline__ float neg_expm1(float y, float e) {
 }
 
 struct Gate {
-  float alpha, beta;
+  float alpha, beta, rbeta;  // rbeta: 1 / beta, with NORM
 };
 
 // With E = exp(-|z|), logsigmoid(z) = min(z, 0) - log(1 + E).  log2(1 + E) / E
@@ -120,7 +120,11 @@ template <int MODE> __device__ __forceinline__ Gate gate(float z, float inv_gamm
   g.alpha = __builtin_amdgcn_exp2f(la);
   if constexpr (MODE == 0) g.beta = 1.f;
   if constexpr (MODE == 1) g.beta = neg_expm1(la * LN2, g.alpha);
-  if constexpr (MODE == 2) g.beta = __builtin_amdgcn_sqrtf(neg_expm1(la * (2.f * LN2), g.alpha * g.alpha));
+  if constexpr (MODE == 2) {
+    const float b2 = neg_expm1(la * (2.f * LN2), g.alpha * g.alpha);
+    g.rbeta = __builtin_amdgcn_rsqf(b2);
+    g.beta = b2 == 0.f ? 0.f : b2 * g.rbeta;
+  }
   return g;
 }
 
@@ -128,7 +132,7 @@ template <int MODE> __device__ __forceinline__ Gate gate(float z, float inv_gamm
 template <int MODE> __device__ __forceinline__ float slope(const Gate& g) {
   if constexpr (MODE == 0) return 0.f;
   if constexpr (MODE == 1) return -g.alpha;
-  return g.beta == 0.f ? 0.f : -g.alpha * g.alpha * __builtin_amdgcn_rcpf(g.beta);
+  return g.beta == 0.f ? 0.f : -g.alpha * g.alpha * g.rbeta;
 }
 
 // ---- words between workgroups -----------------------------------------------------
@@ -166,13 +170,13 @@ __global__ __launch_bounds__(256) void k_rec_init(uint64_t* words, int64_t pairs
 template <int VEC, int NW> struct Place {
   int b, step, lane, wave, c, cl;  // cl: the channel that is loaded where c is past the last
   bool on;
-  __device__ Place(const RecParams& P, uint32_t* counters) {
+  __device__ Place(const RecParams& P, uint32_t* counters, int nch) {
     __shared__ int ticket;
     lane = threadIdx.x & 63;
     wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int chains = P.slabs * P.B, chain = blockIdx.x % chains;
     step = 0;
-    if (P.nch > 1) {
+    if (nch > 1) {
       if (threadIdx.x == 0)
         ticket = (int)__hip_atomic_fetch_add(&counters[chain], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __syncthreads();
@@ -241,11 +245,11 @@ template <int VEC, int NW> struct Chain {
 
 // Y: writes y and h_out.  Otherwise leaves the chunks' entry states for the backward.
 template <typename T, int VEC, int MODE, bool Y>
-__global__ __launch_bounds__(64 * REC_FWD_WAVES) void k_rec_forward(const RecParams P) {
-  constexpr int NW = REC_FWD_WAVES, NT = REC_CHUNK / NW;
+__global__ __launch_bounds__(64 * REC_WAVES) void k_rec_forward(const RecParams P) {
+  constexpr int NW = REC_WAVES, NT = REC_NT;
   __shared__ float sA[NW][64 * VEC], sH[NW][64 * VEC];
   __shared__ Chain<VEC, NW> chain;
-  const Place<VEC, NW> at(P, P.counters);
+  const Place<VEC, NW> at(P, P.counters, P.nch);
   const int t0 = at.step * REC_CHUNK + at.wave * NT;
   float bias[VEC];
 #pragma unroll
@@ -314,9 +318,6 @@ __global__ __launch_bounds__(64 * REC_FWD_WAVES) void k_rec_forward(const RecPar
     __syncthreads();
     chain.run(at, state);
   }
-  if constexpr (!Y) {
-    if (at.wave == 0 && at.on) store_f32<VEC>(P.entry + ((int64_t)at.b * P.nch + at.step) * P.D + at.c, state);
-  }
   // the state that leaves the chunk goes out first: others wait for it
   const bool boundary = at.step % REC_GROUP == REC_GROUP - 1 && at.step + 1 < P.nch;
   const bool final = Y && at.step == P.nch - 1 && P.h_out;
@@ -325,6 +326,10 @@ __global__ __launch_bounds__(64 * REC_FWD_WAVES) void k_rec_forward(const RecPar
   for (int e = 0; e < VEC; ++e) {
     h[e] = state[e];
     for (int w = 0; w < at.wave; ++w) h[e] = sA[w][e * 64 + at.lane] * h[e] + sH[w][e * 64 + at.lane];
+  }
+  if constexpr (!Y) {
+    const int k = at.step * (REC_CHUNK / REC_BCHUNK) + at.wave / REC_BWAVES;
+    if (at.wave % REC_BWAVES == 0 && k < P.nchb && at.on) store_f32<VEC>(P.entry + ((int64_t)at.b * P.nchb + k) * P.D + at.c, h);
   }
   if (at.wave == NW - 1 && at.on && (boundary || final)) {
     float end[VEC];
@@ -354,27 +359,27 @@ __global__ __launch_bounds__(64 * REC_FWD_WAVES) void k_rec_forward(const RecPar
 
 // Chunks from the last to the first; P.entry holds their entry states.
 template <typename T, int VEC, int MODE>
-__global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecParams P) {
-  constexpr int NW = REC_BWD_WAVES, NT = REC_CHUNK / NW;
+__global__ __launch_bounds__(64 * REC_BWAVES) void k_rec_backward(const RecParams P) {
+  constexpr int NW = REC_BWAVES, NT = REC_NT;
   __shared__ float sA[NW][64 * VEC], sH[NW][64 * VEC], sR[NW][64 * VEC];
   __shared__ Chain<VEC, NW> chain;
-  const Place<VEC, NW> at(P, P.counters + (int64_t)P.slabs * P.B);
-  const int chunk = P.nch - 1 - at.step, t0 = chunk * REC_CHUNK + at.wave * NT;
-  const int64_t seq = (int64_t)at.b * P.D + at.cl, ch = ((int64_t)at.b * P.nch + chunk) * P.D + at.cl;
+  const Place<VEC, NW> at(P, P.counters + (int64_t)P.slabs * P.B, P.nchb);
+  const int chunk = P.nchb - 1 - at.step, t0 = chunk * REC_BCHUNK + at.wave * NT;
+  const int64_t seq = (int64_t)at.b * P.D + at.cl, ch = ((int64_t)at.b * P.nchb + chunk) * P.D + at.cl;
   float bias[VEC], state[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) bias[e] = state[e] = 0.f;
   if (P.bias) load_f32<VEC>(P.bias + at.cl, bias);
-  if (P.nch > 1) load_f32<VEC>(P.entry + ch, state);
+  if (P.nchb > 1) load_f32<VEC>(P.entry + ch, state);
   else if (P.h_in) load_f32<VEC>(P.h_in + seq, state);
   const uint32_t tok = tokens<NT>(P, at.b, t0);
-  // per position: alpha, dbeta/dlog alpha x, sigmoid(-z) / gamma, beta, dy
-  float A[VEC], H[VEC], R[VEC], al[NT][VEC], be[NT][VEC], sl[NT][VEC], sg[NT][VEC], dy[NT][VEC];
+  // per position: alpha, beta, dbeta/dlog alpha x, sigmoid(-z) / gamma; x and dy stay packed
+  float A[VEC], H[VEC], R[VEC], al[NT][VEC], be[NT][VEC], sl[NT][VEC], sg[NT][VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) A[e] = 1.f, H[e] = R[e] = 0.f;
-  typename RowLoad<T, VEC>::raw rx[NT];
+  typename RowLoad<T, VEC>::raw rx[NT], rd[NT];
   if (tok) {
-    typename RowLoad<T, VEC>::raw rz[NT], rd[NT];
+    typename RowLoad<T, VEC>::raw rz[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
       const int t = min(t0 + i, P.L - 1);
@@ -400,10 +405,9 @@ __global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecPa
           be[i][e] = on ? g.beta : 0.f;
           sl[i][e] = on ? slope<MODE>(g) * x[e] : 0.f;
           sg[i][e] = on ? (zb < 0.f ? 1.f : E) * __builtin_amdgcn_rcpf(1.f + E) * P.inv_gamma : 0.f;
-          dy[i][e] = on ? d[e] : 0.f;
           A[e] *= al[i][e];
           H[e] = al[i][e] * H[e] + (on ? g.beta * x[e] : 0.f);
-          R[e] += A[e] * dy[i][e];  // dy_t reaches the front through alpha_{t0} .. alpha_t
+          R[e] += A[e] * (on ? d[e] : 0.f);  // dy_t reaches the front through alpha_{t0} .. alpha_t
         }
       }
     };
@@ -418,15 +422,15 @@ __global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecPa
   }
   float carry[VEC], begin[VEC];
   load_begin<VEC>(P.dh_out, seq, at.step, begin);
-  uint64_t* maps = P.rmaps + (int64_t)at.b * P.nch * P.D;
-  uint64_t* ends = P.rends + (int64_t)at.b * P.groups * P.D;
-  if (P.nch == 1) {
+  uint64_t* maps = P.rmaps + (int64_t)at.b * P.nchb * P.D;
+  uint64_t* ends = P.rends + (int64_t)at.b * P.groupsb * P.D;
+  if (P.nchb == 1) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) carry[e] = begin[e];
     __syncthreads();
   } else {
     __syncthreads();
-    if (at.wave == 0 && at.step + 1 < P.nch) {
+    if (at.wave == 0 && at.step + 1 < P.nchb) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         float a = A[e], r = R[e];
@@ -445,7 +449,7 @@ __global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecPa
 #pragma unroll
   for (int e = 0; e < VEC; ++e)
     for (int w = NW - 1; w > at.wave; --w) carry[e] = sA[w][e * 64 + at.lane] * carry[e] + sR[w][e * 64 + at.lane];
-  const bool boundary = at.step % REC_GROUP == REC_GROUP - 1 && at.step + 1 < P.nch;
+  const bool boundary = at.step % REC_GROUP == REC_GROUP - 1 && at.step + 1 < P.nchb;
   const bool final = chunk == 0 && P.dh_in;
   if (at.wave == 0 && at.on && (boundary || final)) {
     float front[VEC];
@@ -456,7 +460,7 @@ __global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecPa
     }
     if (final) store_f32<VEC>(P.dh_in + seq, front);
   }
-  float h[VEC], hb[NT][VEC], db[VEC];
+  float h[VEC], db[VEC];
 #pragma unroll
   for (int e = 0; e < VEC; ++e) {
     h[e] = state[e];
@@ -472,7 +476,7 @@ __global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecPa
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float decayed = al[i][e] * h[e];
-        hb[i][e] = (decayed + sl[i][e]) * sg[i][e];
+        sl[i][e] = (decayed + sl[i][e]) * sg[i][e];
         h[e] = decayed + (tok >> i & 1 ? be[i][e] * x[e] : 0.f);
       }
     }
@@ -480,15 +484,16 @@ __global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecPa
 #pragma unroll
   for (int k = 0; k < NT; ++k) {
     const int i = NT - 1 - k;
-    float dx[VEC], dz[VEC];
+    float dx[VEC], dz[VEC], d[VEC];
+    if (tok) RowLoad<T, VEC>::unpack(rd[i], d);
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       dx[e] = dz[e] = 0.f;
       if (tok) {
-        const float dh = carry[e] + dy[i][e];
         const bool on = tok >> i & 1;
+        const float dh = carry[e] + (on ? d[e] : 0.f);
         dx[e] = on ? be[i][e] * dh : 0.f;
-        dz[e] = on ? dh * hb[i][e] : 0.f;
+        dz[e] = on ? dh * sl[i][e] : 0.f;
         db[e] += dz[e];
         carry[e] = al[i][e] * dh;
       }
@@ -517,7 +522,7 @@ __global__ __launch_bounds__(64 * REC_BWD_WAVES) void k_rec_backward(const RecPa
 __global__ __launch_bounds__(1024) void k_rec_dbias(const RecParams P) {
   __shared__ double part[16][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
-  const int64_t n = (int64_t)P.B * P.nch;
+  const int64_t n = (int64_t)P.B * P.nchb;
   double s = 0.0;
   if (c < P.D) {
     const float* p = P.dbp + c;
@@ -565,7 +570,7 @@ template <typename T, int VEC, int MODE> __global__ __launch_bounds__(64) void k
 }
 
 template <typename T, int VEC, int MODE> struct Launch {
-  static dim3 grid(const RecParams& P) { return dim3((unsigned)((int64_t)P.slabs * P.nch * P.B)); }
+  static dim3 grid(const RecParams& P, int nch) { return dim3((unsigned)((int64_t)P.slabs * nch * P.B)); }
   static void init(const RecParams& P, hipStream_t st) {
     const int64_t pairs = P.words / 2, chains = 2 * (int64_t)P.slabs * P.B;
     const int64_t n = pairs > chains ? pairs : chains;
@@ -573,14 +578,14 @@ template <typename T, int VEC, int MODE> struct Launch {
   }
   static void forward(const RecParams& P, hipStream_t st) {
     if (P.nch > 1) init(P, st);
-    hipLaunchKernelGGL((k_rec_forward<T, VEC, MODE, true>), grid(P), dim3(64 * REC_FWD_WAVES), 0, st, P);
+    hipLaunchKernelGGL((k_rec_forward<T, VEC, MODE, true>), grid(P, P.nch), dim3(64 * REC_WAVES), 0, st, P);
   }
   static void backward(const RecParams& P, hipStream_t st) {
-    if (P.nch > 1) {
+    if (P.nchb > 1) {
       init(P, st);
-      hipLaunchKernelGGL((k_rec_forward<T, VEC, MODE, false>), grid(P), dim3(64 * REC_FWD_WAVES), 0, st, P);
+      hipLaunchKernelGGL((k_rec_forward<T, VEC, MODE, false>), grid(P, P.nch), dim3(64 * REC_WAVES), 0, st, P);
     }
-    hipLaunchKernelGGL((k_rec_backward<T, VEC, MODE>), grid(P), dim3(64 * REC_BWD_WAVES), 0, st, P);
+    hipLaunchKernelGGL((k_rec_backward<T, VEC, MODE>), grid(P, P.nchb), dim3(64 * REC_BWAVES), 0, st, P);
     if (P.dbias) hipLaunchKernelGGL(k_rec_dbias, dim3((P.D + 63) / 64), dim3(1024), 0, st, P);
   }
   static void step(const RecParams& P, hipStream_t st) {
