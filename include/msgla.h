@@ -495,7 +495,7 @@ msgla_status msgla_recurrence_step(const msgla_recurrence_config* cfg, const msg
  * g / (heads_q / heads_kv).
  * Requirements: heads_q a multiple of heads_kv, at most 1024; d_k a multiple of
  * 8 up to 128, d_v one up to 256; block 32, 64 or 128; n_select 1 .. 64;
- * n_first >= 0, n_recent >= 1, n_first + n_recent <= n_select; scale finite
+ * n_first >= 0, n_recent >= 1, n_first + n_recent <= n_select; scale 1e-30 .. 1e30
  * (1 / sqrt(d_k) as a rule).  dtype: of q, k, v, the output and their
  * gradients; bf16 inputs meet on bf16 matrix cores with fp32 sums (softmax
  * weights and their gradients are rounded to bf16 for the products), fp32 ones

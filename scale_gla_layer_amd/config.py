@@ -111,8 +111,8 @@ class BlockAttentionConfig:
             raise ValueError("n_first >= 0, n_recent >= 1 and n_first + n_recent <= n_select are required")
         if self.scale is None:
             object.__setattr__(self, "scale", self.d_k ** -0.5)
-        if not abs(self.scale) <= 3.0e38:
-            raise ValueError("scale must be finite")
+        if not 1e-30 <= self.scale <= 1e30:
+            raise ValueError("scale must be positive, 1e-30 .. 1e30")
         if self.dtype not in (F32, BF16):
             raise ValueError(f"dtype must be {F32!r} or {BF16!r}")
 

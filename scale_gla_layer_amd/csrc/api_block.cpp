@@ -18,7 +18,7 @@ bool blk_config_ok(const msgla_block_config* c) {
   if (c->block != 32 && c->block != 64 && c->block != 128) return false;
   if (c->n_select < 1 || c->n_select > BLK_MAX_SEL || c->n_first < 0 || c->n_recent < 1) return false;
   if (c->n_first > c->n_select || c->n_recent > c->n_select - c->n_first) return false;
-  return c->scale - c->scale == 0.f;  // finite
+  return c->scale >= 1.0e-30f && c->scale <= 1.0e30f;
 }
 
 bool blk_sizes_ok(int64_t B, int64_t L, int64_t S) {

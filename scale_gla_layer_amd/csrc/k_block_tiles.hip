@@ -1,21 +1,32 @@
 // Attention over selected blocks for many queries: forward and the gradient of
 // the queries with keys and values shared by a workgroup.
 //
-// A workgroup takes NW * RT neighbouring tiles of 16 (query, head) rows, RT of
-// them a wave, and walks the union of all its queries' blocks in ascending
-// order, KT keys a unit.  A unit's keys and values are copied asynchronously
-// into one of two LDS stages while the other is worked on, with one barrier a
-// unit; a wave none of whose rows chose the block goes straight to the next
-// barrier.  The tiles' rows keep their outputs in registers throughout, so
-// what is paid per unit is one copy from L2 for the workgroup, one pass over
-// the LDS stage per wave, and the products.
+// A workgroup takes 7 or 15 neighbouring tiles of 16 (query, head) rows, one
+// a wave, and walks the union of all its queries' blocks in ascending order, KT
+// keys a unit.  One more wave copies each unit's keys and values once,
+// asynchronously, into a ring of LDS stages; the tiles' waves work on the units
+// that their own rows chose, each at its own pace.  What couples them are two
+// kinds of counters in LDS: `filled`, the units copied so far, and done[w], the
+// units wave w is finished with or does not need.  (With a barrier a unit
+// instead, every unit costs the time of one that all waves need, though with
+// selections that differ from query to query only a third of them do.)
+//   Every wait ends: a tile's wave waits for a unit only after it has counted all
+// earlier ones as done, and the copying wave counts every unit it has issued as
+// filled before it waits for a stage, which the waves free in order.
+//
+// Bound by vector instructions, which is why a unit is as long as a block (up to
+// 64 keys) and everything that is one value a unit is kept out of the lanes:
+// lists and their unions are bit maps that scalar instructions walk, the running
+// maximum follows a row's true one only when that has grown by more than 8 (in
+// units of log 2: weights stay below 2^8), and rows that have not chosen a block
+// are masked on the packed weights.
 //
 // Stage rows hold their 16-byte pieces XOR-swizzled by the row, so that both
 // readers are free of bank conflicts: 16 rows at one piece (the A operand of
 // S^T = K Q^T), and 16 rows' columns (the A operand of O^T = V^T P^T, through
-// the transpose read).  The running maximum follows a row's true one only when
-// that has grown by more than 8 (in units of log 2), so weights stay below 2^8
-// and the outputs are rescaled a few times in all instead of every unit.
+// the transpose read).
+#include <algorithm>
+
 #include "async_copy.hpp"
 #include "block_device.hpp"
 
@@ -23,23 +34,44 @@ namespace msgla {
 
 namespace {
 
-// A stage tile of rows of W pieces.
-template <int W> __device__ __forceinline__ constexpr int tile_key(int r) { return W == 8 ? (r >> 1) & 7 : r & 15; }
-
-// A wave's share of the copy of rows key0 .. key0 + KT - 1 (row `last` again
-// behind it: rows there have weight 0 and must hold numbers).  Pieces behind
-// the head's width repeat its first: they meet zeroes or columns that are not
-// stored.
-template <int W, int KT, int NW>
-__device__ __forceinline__ void copy_rows(const char* base, int64_t st, int key0, int last, int width, char* lds,
-                                          int wave, int lane) {
-  static_assert(KT * W % (64 * NW) == 0, "whole copy instructions for every wave");
-#pragma unroll
-  for (int k = 0; k < KT * W / 64 / NW; ++k) {
-    const int i = wave + k * NW, pc = 64 * i + lane, r = pc / W, p = (pc % W) ^ tile_key<W>(r);
-    dma16(base + (int64_t)min(key0 + r, last) * st + (p * 16 < width ? p * 16 : 0), lds + 1024 * i);
-  }
+// A stage tile of rows of W pieces: piece p of row r lies at p ^ tile_key(r).
+// Rows r .. r + 3 differ in bits that keep neighbouring pieces together, so the
+// 16 lanes of one transpose read (four rows, two pieces) meet eight different
+// 16-byte units, as do eight consecutive rows at one piece.
+template <int W> __device__ __forceinline__ constexpr int tile_key(int r) {
+  return W == 8 ? (r >> 1 & 1) << 1 | (r >> 2 & 1) << 2 | (r >> 3 & 1) : (r & 3) << 1 | (r >> 2 & 1) << 3 | (r >> 3 & 1);
 }
+
+// One wave's copy of rows key0 .. key0 + KT - 1 (row `last` again behind it: rows
+// there have weight 0 and must hold numbers).  Pieces behind the head's width
+// repeat its first: they meet zeroes or columns that are not stored.
+template <int W, int KT> struct RowCopy {
+  static constexpr int N = KT * W / 64;  // copy instructions
+  static_assert(KT * W % 64 == 0, "whole copy instructions");
+  const char* base;
+  int64_t st;
+  uint32_t off[N];  // the lane's bytes from the first row, where 32 bits hold them
+  __device__ RowCopy(const char* b, int64_t s, int width, int lane) : base(b), st(s) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int pc = 64 * i + lane, r = pc / W, p = (pc % W) ^ tile_key<W>(r);
+      off[i] = (uint32_t)r * (uint32_t)st + (p * 16 < width ? p * 16 : 0);
+    }
+  }
+  __device__ __forceinline__ void issue(int key0, int last, int width, char* lds, int lane) const {
+    if (key0 + KT - 1 <= last && st < (1 << 24)) {
+      const char* first = base + (int64_t)key0 * st;
+#pragma unroll
+      for (int i = 0; i < N; ++i) dma16(first + off[i], lds + 1024 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int pc = 64 * i + lane, r = pc / W, p = (pc % W) ^ tile_key<W>(r);
+        dma16(base + (int64_t)min(key0 + r, last) * st + (p * 16 < width ? p * 16 : 0), lds + 1024 * i);
+      }
+    }
+  }
+};
 
 // Column reader: slab s's rows at columns 16 t .. + 15 (layout of blk_column).
 template <typename T, int W> struct Columns;
@@ -88,274 +120,321 @@ template <int W> struct Rows {
   }
 };
 
-// The units of a workgroup: the set bits of `map` in ascending order, a block's
-// KT-key parts in turn, up to the last position.
-struct Units {
+// The set bits of a map of blocks, in ascending order.
+struct Blocks {
   const uint32_t* map;
-  int words, w = -1, j = 0, k0 = 0;
+  int words, w = -1;
   uint32_t bits = 0;
-  __device__ bool next(int lgT, int kt, int last) {
-    if (w >= 0 && k0 + kt < (j + 1) << lgT && k0 + kt <= last) {
-      k0 += kt;
-      return true;
-    }
+  __device__ Blocks(const uint32_t* m, int n) : map(m), words(n) {}
+  __device__ int next() {  // -1 at the end
     while (!bits) {
-      if (++w >= words) return false;
+      if (++w >= words) return -1;
       bits = __builtin_amdgcn_readfirstlane(map[w]);
     }
-    j = 32 * w + __builtin_ctz(bits);
+    const int b = __builtin_ctz(bits);
     bits &= bits - 1;
-    k0 = j << lgT;
-    return true;
+    return 32 * w + b;
   }
 };
 
 constexpr float GROWTH = 8.f;
+constexpr int TILE_WAVES_MAX = 15, MIN_STAGES = 2;
 
-template <typename T, int DKP, int DVP, int KT, int RT, int NW, bool GRAD>
-__global__ __launch_bounds__(64 * NW) void k_block_tiles(const BlkParams P) {
+// LDS counters between the waves of a workgroup
+struct Ring {
+  int filled;
+  int done[TILE_WAVES_MAX + 1];
+};
+// one LDS word read or written as it stands (LDS operations of a wave stay in order)
+__device__ __forceinline__ int ring_get(const int* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+__device__ __forceinline__ void ring_put(int* p, int v) {
+  asm volatile("" ::: "memory");
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+}
+
+// The copying wave: up to FLIGHT units under way at a time.
+template <typename T, int DKP, int DVP, int KT, int WAVES>
+__device__ __forceinline__ void fill_ring(const BlkParams& P, Ring* ring, char* ring_lds, int stages, Blocks blocks,
+                                          int last, const char* kbase, const char* vbase, int lane) {
+  constexpr int ES = sizeof(T), WK = DKP * ES / 16, WV = DVP * ES / 16;
+  constexpr int KB = KT * WK * 16, STAGE = KB + KT * WV * 16, COPIES = STAGE / 1024;
+  const RowCopy<WK, KT> kc(kbase, P.k.st, P.dkw * ES, lane);
+  const RowCopy<WV, KT> vc(vbase, P.v.st, P.dvw * ES, lane);
+  wait_vmcnt<0>();
+  int n = 0, stage = 0;
+  for (int j = blocks.next(); j >= 0; j = blocks.next())
+    for (int k0 = j << P.lgT; k0 < (j + 1) << P.lgT && k0 <= last; k0 += KT) {
+      auto is_free = [&] { return __all(lane >= WAVES || ring_get(&ring->done[lane]) > n - stages); };
+      if (!is_free()) {
+        wait_vmcnt<0>();
+        if (lane == 0) ring_put(&ring->filled, n);
+        do __builtin_amdgcn_s_sleep(1);
+        while (!is_free());
+      }
+      asm volatile("" ::: "memory");
+      char* st = ring_lds + stage * STAGE;
+      stage = stage + 1 == stages ? 0 : stage + 1;
+      kc.issue(k0, last, P.dkw * ES, st, lane);
+      vc.issue(k0, last, P.dvw * ES, st + KB, lane);
+      wait_vmcnt<COPIES < 64 ? COPIES : 0>();  // all units before this one have landed
+      if (lane == 0) ring_put(&ring->filled, n);
+      ++n;
+    }
+  wait_vmcnt<0>();
+  if (lane == 0) ring_put(&ring->filled, 0x7fffffff);
+}
+
+template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD>
+__global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) void k_block_tiles(const BlkParams P, int stages) {
   constexpr int ES = sizeof(T), WK = DKP * ES / 16, WV = DVP * ES / 16;
   constexpr int NK = DKP * ES / 64, NV = DVP * ES / 64, KEY_T = KT / 16, SLABS = KT / blk_slab<T>();
-  constexpr int KB = KT * WK * 16, STAGE = KB + KT * WV * 16, NT = NW * RT;
+  constexpr int KB = KT * WK * 16, STAGE = KB + KT * WV * 16, NT = WAVES, THREADS = 64 * (WAVES + 1);
   constexpr int OUT = GRAD ? DKP : DVP;  // width of the accumulated rows
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  uint32_t* map = reinterpret_cast<uint32_t*>(smem + 2 * STAGE);
   const int words = (P.nb + 31) / 32, pitch = P.n + 1;
-  uint16_t* lists = reinterpret_cast<uint16_t*>(map + words);  // [queries][n + 1], ended by 0xffff
   __shared__ int slast;
+  __shared__ Ring ring;
   const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, a = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int groups = (P.tiles_per_seq + NT - 1) / NT;
-  // each XCD takes one contiguous range of the groups, whose blocks meet in its L2
-  const int64_t work = (int64_t)(blockIdx.x % N_XCD) * (gridDim.x / N_XCD) + blockIdx.x / N_XCD;
-  if (work >= (int64_t)P.B * P.Hkv * groups) return;
-  const int64_t bh = work / groups;
-  // the last tiles, which have the most blocks, first
-  const int t0 = (groups - 1 - (int)(work - bh * groups)) * NT;
-  const int b = (int)(bh / P.Hkv), h = (int)(bh - (int64_t)b * P.Hkv);
+  // Work in order of length, the last tiles, which have the most blocks, first;
+  // an XCD (block id mod 8) keeps to its own sequences and heads, whose blocks
+  // meet in its L2.
+  const int groups = (P.tiles_per_seq + NT - 1) / NT, heads = P.B * P.Hkv;
+  int bh, rank;
+  if (heads >= N_XCD) {
+    const int x = blockIdx.x % N_XCD, s = blockIdx.x / N_XCD, mine = (heads - x + N_XCD - 1) / N_XCD;
+    rank = s / mine;
+    bh = x + N_XCD * (s - rank * mine);
+  } else {
+    rank = blockIdx.x / heads;
+    bh = blockIdx.x - rank * heads;
+  }
+  if (rank >= groups) return;
+  const int t0 = (groups - 1 - rank) * NT;
+  const int b = bh / P.Hkv, h = bh - b * P.Hkv;
   const int q0 = P.GT > 1 ? t0 / P.GT : t0 * P.QT;  // the first query
   const int qn = P.GT > 1 ? (t0 + NT - 1) / P.GT - q0 + 1 : NT * P.QT;
+  // maps of the blocks: all queries', and each tile's (of several tiles of one query: the query's)
+  uint32_t* map = reinterpret_cast<uint32_t*>(smem + stages * STAGE);
+  uint32_t* tmaps = map + words;
+  uint16_t* lists = reinterpret_cast<uint16_t*>(tmaps + NT * words);  // [queries][n + 1], ended by 0xffff
 
-  // lists and their union: the raw rows of sel through LDS (the stages are not in use yet)
-  for (int i = tid; i < words; i += 64 * NW) map[i] = 0;
-  if (tid == 0) slast = -1;
+  // the raw rows of sel through LDS (the stages are not in use yet)
+  for (int i = tid; i < (NT + 1) * words; i += THREADS) map[i] = 0;
+  if (tid == 0) slast = -1, ring.filled = 0;
+  if (tid < WAVES) ring.done[tid] = 0;
   int* raw = reinterpret_cast<int*>(smem);
   {
     const int rows = min(qn, P.L - q0);
-    const int32_t* sel = P.sel + (bh * P.L + q0) * P.n;
-    for (int i = tid; i < rows * P.n; i += 64 * NW) raw[i] = sel[i];
+    const int32_t* sel = P.sel + ((int64_t)bh * P.L + q0) * P.n;
+    for (int i = tid; i < rows * P.n; i += THREADS) raw[i] = sel[i];
   }
   __syncthreads();
-  for (int s = tid; s < qn; s += 64 * NW) {
+  for (int s = tid; s < qn; s += THREADS) {
     const int p = blk_position(P, b, q0 + s);
     uint16_t* l = lists + s * pitch;
+    uint32_t* own = tmaps + (P.GT > 1 ? s : s / P.QT) * words;
     l[blk_chosen(P, raw + s * P.n, p, [&](int n, int j) {
       l[n] = (uint16_t)j;
       atomicOr(&map[j >> 5], 1u << (j & 31));
+      atomicOr(&own[j >> 5], 1u << (j & 31));
     })] = 0xffff;
     if (p >= 0) atomicMax(&slast, p);
   }
-
-  const int kw = P.dkw * ES, vw = P.dvw * ES;
-  u32x4 q[RT][NK], g[GRAD ? RT : 1][GRAD ? NV : 1];
-  BlkRow row[RT];
-  float m[RT], l[RT];  // forward: the reference maximum and the sum; gradient: lse and delta
-  const uint16_t* at[RT];
-#pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    const int t = t0 + wave * RT + rt;
-    BlkTile tile(P, bh * P.tiles_per_seq + min(t, P.tiles_per_seq - 1));
-    row[rt] = tile.row(P, c16);
-    if (t >= P.tiles_per_seq) row[rt].in = false, row[rt].p = -1;
-    const bool live = row[rt].in && row[rt].p >= 0;
-    const int64_t i = live ? row[rt].i : 0, hd = live ? row[rt].head : 0;
-    const char* qr = P.q.p + b * P.q.sb + i * P.q.st + hd * P.q.sh;
-#pragma unroll
-    for (int s = 0; s < NK; ++s) q[rt][s] = live ? blk_ld(qr, 64 * s + 16 * a, kw) : zero16();
-    m[rt] = -__builtin_inff();
-    l[rt] = 0.f;
-    if constexpr (GRAD) {
-      const char* gr = P.dout.p + b * P.dout.sb + i * P.dout.st + hd * P.dout.sh;
-#pragma unroll
-      for (int s = 0; s < NV; ++s) g[rt][s] = live ? blk_ld(gr, 64 * s + 16 * a, vw) : zero16();
-      if (live) {
-        const int64_t lr = ((int64_t)b * P.Hq + hd) * P.L + i;
-        m[rt] = P.lse_in[lr] * BLK_LOG2E;
-        l[rt] = P.delta[lr];
-      }
-    }
-    at[rt] = lists + (live ? row[rt].i - q0 : 0) * pitch;
-  }
   __syncthreads();
   const int last = __builtin_amdgcn_readfirstlane(slast);
-  int cur[RT];
+  if (wave == WAVES) {
+    fill_ring<T, DKP, DVP, KT, WAVES>(P, &ring, smem, stages, Blocks(map, words), last, P.k.p + b * P.k.sb + h * P.k.sh,
+                               P.v.p + b * P.v.sb + h * P.v.sh, lane);
+    return;
+  }
+
+  const int kw = P.dkw * ES, vw = P.dvw * ES, t = t0 + wave;
+  BlkRow row = BlkTile(P, (int64_t)bh * P.tiles_per_seq + min(t, P.tiles_per_seq - 1)).row(P, c16);
+  if (t >= P.tiles_per_seq) row.in = false, row.p = -1;
+  const bool live = row.in && row.p >= 0;
+  u32x4 q[NK], g[GRAD ? NV : 1];
+  float nref = 0.f, l = 0.f;  // forward: minus the reference maximum, the sum; gradient: minus lse, delta
+  {
+    const int64_t li = live ? row.i : 0, hd = live ? row.head : 0;
+    const char* qr = P.q.p + b * P.q.sb + li * P.q.st + hd * P.q.sh;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) cur[rt] = row[rt].in && row[rt].p >= 0 ? *at[rt] : 0xffff;
-  f32x4 acc[RT][OUT / 16];
+    for (int s = 0; s < NK; ++s) q[s] = live ? blk_ld(qr, 64 * s + 16 * a, kw) : zero16();
+    if constexpr (GRAD) {
+      const char* gr = P.dout.p + b * P.dout.sb + li * P.dout.st + hd * P.dout.sh;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+      for (int s = 0; s < NV; ++s) g[s] = live ? blk_ld(gr, 64 * s + 16 * a, vw) : zero16();
+      const int64_t lr = ((int64_t)b * P.Hq + hd) * P.L + li;
+      nref = live ? -P.lse_in[lr] * BLK_LOG2E : 0.f;
+      l = live ? P.delta[lr] : 0.f;
+    }
+  }
+  const uint16_t* at = lists + (live ? row.i - q0 : 0) * pitch;
+  int cur = live ? *at : 0xffff;
+  f32x4 acc[OUT / 16];
 #pragma unroll
-    for (int d = 0; d < OUT / 16; ++d) acc[rt][d] = zero4();
-  const float sc = P.scale * BLK_LOG2E;
-  const char* kbase = P.k.p + b * P.k.sb + h * P.k.sh;
-  const char* vbase = P.v.p + b * P.v.sb + h * P.v.sh;
+  for (int d = 0; d < OUT / 16; ++d) acc[d] = zero4();
+  const float sc = P.scale * BLK_LOG2E, per_sc = 1.f / sc;
+  float grown = -__builtin_inff();  // a score above this moves the reference
   const Rows<WK> krow(lane);
   const Rows<WV> vrow(lane);
   const Columns<T, GRAD ? WK : WV> col(lane);
 
-  Units u;
-  u.map = map;
-  u.words = words;
-  bool more = u.next(P.lgT, KT, last);
-  auto issue = [&](int stage) {
-    char* st = smem + stage * STAGE;
-    copy_rows<WK, KT, NW>(kbase, P.k.st, u.k0, last, kw, st, wave, lane);
-    copy_rows<WV, KT, NW>(vbase, P.v.st, u.k0, last, vw, st + KB, wave, lane);
-  };
-  if (more) issue(0);
-  bool member[RT];
-  int block = -1;
-  for (int t = 0; more; ++t) {
-    const int j = u.j, k0 = u.k0;
-    more = u.next(P.lgT, KT, last);
-    wait_vmcnt<0>();
-    lds_barrier();
-    if (more) issue((t + 1) & 1);
-    if (j != block) {
-      block = j;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        member[rt] = cur[rt] == j;
-        if (member[rt]) cur[rt] = *++at[rt];
-      }
+  Blocks blocks(tmaps + (P.GT > 1 ? t / P.GT - q0 : wave) * words, words);
+  const int lg_units = P.lgT - (KT == 16 ? 4 : KT == 32 ? 5 : 6);  // units of a block
+  int before = 0, word = -1;  // blocks of the union in the words before the one that `before` was counted for
+  for (int j = blocks.next(); j >= 0; j = blocks.next()) {
+    // the block's place in the union
+    while (word < blocks.w) {
+      if (word >= 0) before += __builtin_popcount(__builtin_amdgcn_readfirstlane(map[word]));
+      ++word;
     }
-    bool any = false;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) any |= member[rt] && k0 <= row[rt].p;
-    if (!__any(any)) continue;
-    const char *ks = smem + (t & 1) * STAGE, *vs = ks + KB;
-    float p[RT][KEY_T][4];
-#pragma unroll
-    for (int kt = 0; kt < KEY_T; ++kt) {
-      f32x4 s[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s[rt] = zero4();
-#pragma unroll
-      for (int w = 0; w < NK; ++w) {
-        const u32x4 f = krow.read(ks, kt, w);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) s[rt] = mma_slab<T>(f, q[rt][w], s[rt]);
+    const int place = before + __builtin_popcount(__builtin_amdgcn_readfirstlane(map[word]) & ((1u << (j & 31)) - 1));
+    const bool member = cur == j;
+    if (member) cur = *++at;
+    const int first = j << P.lgT;
+    for (int sub = 0; sub < 1 << lg_units; ++sub) {
+      const int n = (place << lg_units) + sub, k0 = first + sub * KT;
+      const bool take = member && k0 <= row.p;
+      if (!__any(take)) break;
+      if (ring_get(&ring.filled) <= n) {
+        if (lane == 0) ring_put(&ring.done[wave], n);
+        do __builtin_amdgcn_s_sleep(1);
+        while (ring_get(&ring.filled) <= n);
       }
+      asm volatile("" ::: "memory");
+      const char *ks = smem + (n % stages) * STAGE, *vs = ks + KB;
+      f32x4 s[KEY_T];
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int lim = member[rt] ? row[rt].p - k0 - 16 * kt - 4 * a : -1;
+      for (int kt = 0; kt < KEY_T; ++kt) s[kt] = zero4();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[rt][kt][i] = i <= lim ? s[rt][i] * sc : -__builtin_inff();
-      }
-    }
-    if constexpr (!GRAD) {
+      for (int w = 0; w < NK; ++w)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        float mx = -__builtin_inff();
+        for (int kt = 0; kt < KEY_T; ++kt) s[kt] = mma_slab<T>(krow.read(ks, kt, w), q[w], s[kt]);
+      if (__any(take && k0 + KT - 1 > row.p)) {  // the own block: keys behind the query
 #pragma unroll
         for (int kt = 0; kt < KEY_T; ++kt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, p[rt][kt][i]);
-        mx = blk_quad_max(mx);
-        if (__any(mx > m[rt] + GROWTH)) {  // from minus infinity, anything has grown
-          const float n = fmaxf(m[rt], mx), ref = n == -__builtin_inff() ? 0.f : n;
-          const float corr = __builtin_amdgcn_exp2f(m[rt] - ref);
-          m[rt] = n;
-          l[rt] *= corr;
+          for (int i = 0; i < 4; ++i)
+            if (k0 + 16 * kt + 4 * a + i > row.p) s[kt][i] = -__builtin_inff();
+      }
+      float p[KEY_T][4];
+      if constexpr (!GRAD) {
+        float mx = s[0][0];
 #pragma unroll
-          for (int d = 0; d < OUT / 16; ++d) acc[rt][d] *= corr;
+        for (int kt = 0; kt < KEY_T; ++kt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx = fmaxf(mx, s[kt][i]);
+        if (__any(take && mx > grown)) {
+          const float m = grown == -__builtin_inff() ? grown : -nref;  // nothing yet: minus infinity
+          const float top = take ? fmaxf(m, blk_quad_max(mx) * sc) : m;
+          if (top != -__builtin_inff()) {
+            const float corr = __builtin_amdgcn_exp2f(m - top);
+            nref = -top;
+            grown = (top + GROWTH) * per_sc;
+            l *= corr;
+#pragma unroll
+            for (int d = 0; d < OUT / 16; ++d) acc[d] *= corr;
+          }
         }
-        const float ref = m[rt] == -__builtin_inff() ? 0.f : m[rt];
+        float sum = 0.f;
 #pragma unroll
         for (int kt = 0; kt < KEY_T; ++kt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            p[rt][kt][i] = __builtin_amdgcn_exp2f(p[rt][kt][i] - ref);
-            l[rt] += p[rt][kt][i];
+            p[kt][i] = __builtin_amdgcn_exp2f(s[kt][i] * sc + nref);
+            sum += p[kt][i];
           }
+        l += take ? sum : 0.f;
+      } else {
+#pragma unroll
+        for (int kt = 0; kt < KEY_T; ++kt) {
+          f32x4 dp = zero4();
+#pragma unroll
+          for (int w = 0; w < NV; ++w) dp = mma_slab<T>(vrow.read(vs, kt, w), g[w], dp);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[kt][i] = __builtin_amdgcn_exp2f(s[kt][i] * sc + nref) * (dp[i] - l);
+        }
       }
-    } else {
 #pragma unroll
-      for (int kt = 0; kt < KEY_T; ++kt) {
-        f32x4 dp[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) dp[rt] = zero4();
-#pragma unroll
-        for (int w = 0; w < NV; ++w) {
-          const u32x4 f = vrow.read(vs, kt, w);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) dp[rt] = mma_slab<T>(f, g[rt][w], dp[rt]);
+      for (int sl = 0; sl < SLABS; ++sl) {
+        u32x4 w, lo = zero16();
+        if constexpr (GRAD && ES == 2) {  // what the rounding to bf16 leaves goes through the product as well
+          const float v[8] = {p[2 * sl][0], p[2 * sl][1], p[2 * sl][2], p[2 * sl][3],
+                              p[2 * sl + 1][0], p[2 * sl + 1][1], p[2 * sl + 1][2], p[2 * sl + 1][3]};
+          split_bf16(v, w, lo);
+        } else {
+          w = blk_pack<T>(p, sl);
         }
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int i = 0; i < 4; ++i) {  // rows that have not chosen the block
+          w[i] = take ? w[i] : 0u;
+          lo[i] = take ? lo[i] : 0u;
+        }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const bool on = p[rt][kt][i] != -__builtin_inff();
-            p[rt][kt][i] = on ? __builtin_amdgcn_exp2f(p[rt][kt][i] - m[rt]) * (dp[rt][i] - l[rt]) * P.scale : 0.f;
-          }
+        for (int d = 0; d < OUT / 16; ++d) {
+          const u32x4 f = col.read(GRAD ? ks : vs, sl, d);
+          acc[d] = mma_slab<T>(f, w, acc[d]);
+          if constexpr (GRAD && ES == 2) acc[d] = mma_slab<T>(f, lo, acc[d]);
+          // without this all reads move ahead of the products, and registers spill
+          if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
+        }
       }
-    }
-#pragma unroll
-    for (int s = 0; s < SLABS; ++s) {
-      u32x4 w[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) w[rt] = blk_pack<T>(p[rt], s);
-#pragma unroll
-      for (int d = 0; d < OUT / 16; ++d) {
-        const u32x4 f = col.read(GRAD ? ks : vs, s, d);
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) acc[rt][d] = mma_slab<T>(f, w[rt], acc[rt][d]);
-      }
+      if (lane == 0) ring_put(&ring.done[wave], n + 1);
     }
   }
+  if (lane == 0) ring_put(&ring.done[wave], 0x7fffffff);
+  if constexpr (!GRAD) l = blk_quad_sum(l);
+  if (!row.in) return;
+  const BlkHeads& o = GRAD ? P.dq : P.o;
+  const int width = GRAD ? P.dkw : P.dvw;
+  char* out = o.p + row.b * o.sb + (int64_t)row.i * o.st + row.head * o.sh;
+  const float mul = GRAD ? P.scale : l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // no key: 0; a NaN stays
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    if constexpr (!GRAD) l[rt] = blk_quad_sum(l[rt]);
-    if (!row[rt].in) continue;
-    const BlkHeads& o = GRAD ? P.dq : P.o;
-    const int width = GRAD ? P.dkw : P.dvw;
-    char* out = o.p + row[rt].b * o.sb + (int64_t)row[rt].i * o.st + row[rt].head * o.sh;
-    const float inv = GRAD ? 1.f : l[rt] > 0.f ? 1.f / l[rt] : l[rt] == 0.f ? 0.f : l[rt];
-#pragma unroll
-    for (int d = 0; d < OUT / 16; ++d) {
-      const int c = 16 * d + 4 * a;
-      const float v[4] = {acc[rt][d][0] * inv, acc[rt][d][1] * inv, acc[rt][d][2] * inv, acc[rt][d][3] * inv};
-      if (c < width) blk_st4<T>(out + c * ES, v);
-    }
-    if (!GRAD && P.lse && a == 0)
-      P.lse[((int64_t)row[rt].b * P.Hq + row[rt].head) * P.L + row[rt].i] =
-          l[rt] == 0.f ? -__builtin_inff() : m[rt] * BLK_LN2 + logf(l[rt]);
+  for (int d = 0; d < OUT / 16; ++d) {
+    const int c = 16 * d + 4 * a;
+    const float v[4] = {acc[d][0] * mul, acc[d][1] * mul, acc[d][2] * mul, acc[d][3] * mul};
+    if (c < width) blk_st4<T>(out + c * ES, v);
   }
+  if (!GRAD && P.lse && a == 0)
+    P.lse[((int64_t)row.b * P.Hq + row.head) * P.L + row.i] = l == 0.f ? -__builtin_inff() : logf(l) - nref * BLK_LN2;
 }
 
-template <typename T, int DKP, int DVP, int KT, int RT, int NW, bool GRAD>
-hipError_t launch_t(const BlkParams& P, hipStream_t st) {
-  constexpr int STAGE = KT * (DKP + DVP) * (int)sizeof(T), NT = NW * RT;
+template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t launch_t(const BlkParams& P, hipStream_t st) {
+  constexpr int STAGE = KT * (DKP + DVP) * (int)sizeof(T), NT = WAVES;
   const int qn = P.GT > 1 ? NT / P.GT + 2 : NT * P.QT;
-  static_assert(NT * BLK_ROWS * BLK_MAX_SEL * 4 <= 2 * STAGE, "the raw selection fits the stages");
-  const int lds = 2 * STAGE + (P.nb + 31) / 32 * 4 + qn * (P.n + 1) * 2;
-  const auto kernel = &k_block_tiles<T, DKP, DVP, KT, RT, NW, GRAD>;
+  const int rest = (NT + 1) * ((P.nb + 31) / 32 * 4) + qn * (P.n + 1) * 2 + 1024;
+  constexpr int LDS = 160 * 1024;
+  constexpr int MOST = (NT + 1) * (BLK_TILES_MAX / 8) + NT * BLK_ROWS * (BLK_MAX_SEL + 1) * 2 + 1024;
+  static_assert((LDS - MOST) / STAGE >= MIN_STAGES && std::min((LDS - MOST) / STAGE, 8) * STAGE >= NT * BLK_ROWS * BLK_MAX_SEL * 4,
+                "beside the largest maps and lists there is a ring, in which the raw selection fits");
+  const int stages = std::min((LDS - rest) / STAGE, 8);
+  const int lds = stages * STAGE + rest;
+  const auto kernel = &k_block_tiles<T, DKP, DVP, KT, WAVES, GRAD>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  const int64_t groups = (P.tiles_per_seq + NT - 1) / NT, work = (int64_t)P.B * P.Hkv * groups;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)((work + N_XCD - 1) / N_XCD * N_XCD)), dim3(64 * NW), lds, st, P);
+  const int64_t groups = (P.tiles_per_seq + NT - 1) / NT, heads = (int64_t)P.B * P.Hkv;
+  const int64_t grid = heads >= N_XCD ? (heads + N_XCD - 1) / N_XCD * N_XCD * groups : heads * groups;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * (WAVES + 1)), lds, st, P, stages);
   return hipGetLastError();
 }
 
+// 15 tiles leave 128 registers a wave, 7 leave 256.  Units of 64 keys fit the
+// first in the forward at d_v up to 128 (227 us at B = 8, L = 2048, 16 / 4 heads
+// of 128, against 233 with 32 keys and 279 with 7 tiles of 64); elsewhere they
+// spill (d_v 256, one sequence of 16384, 8 / 2 heads: 508 us with 32 keys, 1899
+// with 64, 578 with 7 tiles of 64; gradient at B = 2, L = 4096: 246, 284, 289).
 template <typename T, int DKP, int DVP, bool GRAD> hipError_t by_block(const BlkParams& P, hipStream_t st) {
-  if constexpr (sizeof(T) == 2) {
-    if (P.lgT == 5) return launch_t<T, DKP, DVP, 32, 1, 4, GRAD>(P, st);
-    return launch_t<T, DKP, DVP, 64, 1, 8, GRAD>(P, st);
+  if constexpr (sizeof(T) == 4) {
+    return launch_t<T, DKP, DVP, 16, DVP == 256 || (GRAD && DKP == 128) ? 7 : 15, GRAD>(P, st);
   } else {
-    return launch_t<T, DKP, DVP, 32, 1, 4, GRAD>(P, st);
+    constexpr int KT = !GRAD && DVP <= 128 ? 64 : 32;
+    return P.lgT == 5 ? launch_t<T, DKP, DVP, 32, 15, GRAD>(P, st) : launch_t<T, DKP, DVP, KT, 15, GRAD>(P, st);
   }
 }
 template <typename T, int DKP, bool GRAD> hipError_t by_dv(const BlkParams& P, hipStream_t st) {

@@ -60,7 +60,7 @@ BAD_SIZE = 2 ** 64 - 1
     dict(heads_kv=0), dict(heads_q=7), dict(heads_q=1), dict(heads_q=1026), dict(d_k=4), dict(d_k=136), dict(d_k=60),
     dict(d_v=0), dict(d_v=264), dict(block=16), dict(block=96), dict(n_select=0), dict(n_select=65), dict(n_first=-1),
     dict(n_recent=0), dict(n_first=7), dict(n_first=2 ** 31 - 1, n_recent=2), dict(scale=float("nan")),
-    dict(scale=float("inf")), dict(dtype=2)])
+    dict(scale=float("inf")), dict(scale=0.0), dict(scale=-0.1), dict(dtype=2)])
 def test_invalid_configurations(bad):
     lib, c = binding.load_library(), _raw(**bad)
     assert lib.msgla_block_attention_workspace_bytes(c, 1, 8, 8) == BAD_SIZE
