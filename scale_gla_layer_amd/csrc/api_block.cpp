@@ -112,7 +112,9 @@ BwdWs bwd_ws(const BlkParams& P) {
   Take take;
   const size_t bh = (size_t)P.B * P.Hkv;
   const int64_t pairs = (int64_t)P.L * std::min(P.n, P.nb);
-  w.seg = std::max(64, 1024 / P.G);  // about 1024 rows an item
+  // about 1536 work items, of 128 to 2048 rows: fewer leave CUs idle, more write partial sums
+  const int64_t even = (int64_t)P.B * P.Hkv * pairs / 1536;
+  w.seg = (int)std::max<int64_t>(std::max(1, 128 / P.G), std::min<int64_t>(even, std::max(1, 2048 / P.G)));
   w.W = cdiv(P.L, 64);
   w.max_items = (int)(P.nb + pairs / w.seg);
   w.max_parts = (int)std::min<int64_t>(w.max_items, 2 * (pairs / w.seg));  // blocks of more than seg queries

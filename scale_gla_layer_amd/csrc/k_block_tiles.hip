@@ -1,7 +1,7 @@
 // Attention over selected blocks for many queries: forward and the gradient of
 // the queries with keys and values shared by a workgroup.
 //
-// A workgroup takes 7 or 15 neighbouring tiles of 16 (query, head) rows, one
+// A workgroup takes 15 (or 3) neighbouring tiles of 16 (query, head) rows, one
 // a wave, and walks the union of all its queries' blocks in ascending order, KT
 // keys a unit.  One more wave copies each unit's keys and values once,
 // asynchronously, into a ring of LDS stages; the tiles' waves work on the units
@@ -20,27 +20,13 @@
 // maximum follows a row's true one only when that has grown by more than 8 (in
 // units of log 2: weights stay below 2^8), and rows that have not chosen a block
 // are masked on the packed weights.
-//
-// Stage rows hold their 16-byte pieces XOR-swizzled by the row, so that both
-// readers are free of bank conflicts: 16 rows at one piece (the A operand of
-// S^T = K Q^T), and 16 rows' columns (the A operand of O^T = V^T P^T, through
-// the transpose read).
 #include <algorithm>
 
-#include "async_copy.hpp"
-#include "block_device.hpp"
+#include "block_stage.hpp"
 
 namespace msgla {
 
 namespace {
-
-// A stage tile of rows of W pieces: piece p of row r lies at p ^ tile_key(r).
-// Rows r .. r + 3 differ in bits that keep neighbouring pieces together, so the
-// 16 lanes of one transpose read (four rows, two pieces) meet eight different
-// 16-byte units, as do eight consecutive rows at one piece.
-template <int W> __device__ __forceinline__ constexpr int tile_key(int r) {
-  return W == 8 ? (r >> 1 & 1) << 1 | (r >> 2 & 1) << 2 | (r >> 3 & 1) : (r & 3) << 1 | (r >> 2 & 1) << 3 | (r >> 3 & 1);
-}
 
 // One wave's copy of rows key0 .. key0 + KT - 1 (row `last` again behind it: rows
 // there have weight 0 and must hold numbers).  Pieces behind the head's width
@@ -70,53 +56,6 @@ template <int W, int KT> struct RowCopy {
         dma16(base + (int64_t)min(key0 + r, last) * st + (p * 16 < width ? p * 16 : 0), lds + 1024 * i);
       }
     }
-  }
-};
-
-// Column reader: slab s's rows at columns 16 t .. + 15 (layout of blk_column).
-template <typename T, int W> struct Columns;
-template <int W> struct Columns<bf16, W> {
-  int at;
-  __device__ Columns(int lane) {
-    const int a = lane >> 4, e = (lane >> 2) & 3, c = lane & 3, r = 4 * a + e;
-    at = r * W * 16 + (((c >> 1) ^ tile_key<W>(r)) * 16) + 8 * (c & 1);
-  }
-  __device__ __forceinline__ u32x4 read(const char* lds, int s, int t) const {
-    const char* p = lds + (at ^ (32 * t)) + s * 32 * W * 16;
-    const blk_v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((blk_lds_v4s*)p);
-    const blk_v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((blk_lds_v4s*)(p + 16 * W * 16));
-    const u32x2 x = __builtin_bit_cast(u32x2, lo), y = __builtin_bit_cast(u32x2, hi);
-    return u32x4{x[0], x[1], y[0], y[1]};
-  }
-};
-template <int W> struct Columns<float, W> {
-  static_assert(W >= 16, "swizzle of four bits");
-  int at[4];
-  __device__ Columns(int lane) {
-    const int a = lane >> 4, c = lane & 15;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int r = 4 * a + j;
-      at[j] = r * W * 16 + (((c >> 2) ^ tile_key<W>(r)) * 16) + 4 * (c & 3);
-    }
-  }
-  __device__ __forceinline__ u32x4 read(const char* lds, int s, int t) const {
-    u32x4 v;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = *reinterpret_cast<const uint32_t*>(lds + (at[j] ^ (64 * t)) + s * 16 * W * 16);
-    return v;
-  }
-};
-
-// Row reader: slab w of rows 16 kt + l % 16.
-template <int W> struct Rows {
-  int at;
-  __device__ Rows(int lane) {
-    const int c = lane & 15, a = lane >> 4;
-    at = c * W * 16 + ((a ^ tile_key<W>(c)) * 16);
-  }
-  __device__ __forceinline__ u32x4 read(const char* lds, int kt, int w) const {
-    return ld16(lds + (at ^ (64 * w)) + kt * 16 * W * 16);
   }
 };
 
@@ -406,7 +345,7 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
   constexpr int STAGE = KT * (DKP + DVP) * (int)sizeof(T), NT = WAVES;
   const int qn = P.GT > 1 ? NT / P.GT + 2 : NT * P.QT;
   const int rest = (NT + 1) * ((P.nb + 31) / 32 * 4) + qn * (P.n + 1) * 2 + 1024;
-  constexpr int LDS = 160 * 1024;
+  constexpr int LDS = (WAVES == TILE_WAVES_MAX ? 160 : 80) * 1024;  // of one workgroup on a CU, or two
   constexpr int MOST = (NT + 1) * (BLK_TILES_MAX / 8) + NT * BLK_ROWS * (BLK_MAX_SEL + 1) * 2 + 1024;
   static_assert((LDS - MOST) / STAGE >= MIN_STAGES && std::min((LDS - MOST) / STAGE, 8) * STAGE >= NT * BLK_ROWS * BLK_MAX_SEL * 4,
                 "beside the largest maps and lists there is a ring, in which the raw selection fits");
@@ -424,15 +363,21 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
   return hipGetLastError();
 }
 
-// 15 tiles leave 128 registers a wave, 7 leave 256.  Units of 64 keys fit the
+// 15 tiles leave 128 registers a wave, 3 leave 256.  Units of 64 keys fit the
 // first in the forward at d_v up to 128 (227 us at B = 8, L = 2048, 16 / 4 heads
 // of 128, against 233 with 32 keys and 279 with 7 tiles of 64); elsewhere they
 // spill (d_v 256, one sequence of 16384, 8 / 2 heads: 508 us with 32 keys, 1899
 // with 64, 578 with 7 tiles of 64; gradient at B = 2, L = 4096: 246, 284, 289).
+// 15 tiles a workgroup need two workgroups for every CU; below, 3 do better
+// (fp32 gradient of 1200 tiles: 181 us with 15).
 template <typename T, int DKP, int DVP, bool GRAD> hipError_t by_block(const BlkParams& P, hipStream_t st) {
+  const bool many = P.tiles >= 15 * 512;
   if constexpr (sizeof(T) == 4) {
-    return launch_t<T, DKP, DVP, 16, DVP == 256 || (GRAD && DKP == 128) ? 7 : 15, GRAD>(P, st);
+    if (many && DVP < 256 && !(GRAD && DKP == 128))
+      return launch_t<T, DKP, DVP, 16, DVP < 256 && !(GRAD && DKP == 128) ? 15 : 3, GRAD>(P, st);
+    return launch_t<T, DKP, DVP, 16, 3, GRAD>(P, st);
   } else {
+    if (!many) return launch_t<T, DKP, DVP, 32, 3, GRAD>(P, st);
     constexpr int KT = !GRAD && DVP <= 128 ? 64 : 32;
     return P.lgT == 5 ? launch_t<T, DKP, DVP, 32, 15, GRAD>(P, st) : launch_t<T, DKP, DVP, KT, 15, GRAD>(P, st);
   }
