@@ -79,15 +79,15 @@ struct Take {
   }
 };
 
-// Forward: few tiles leave most of the chip idle, so each one's blocks are dealt
-// to as many waves as give about 2048, eight on a CU.
+// Forward: few tiles leave most of the chip idle, so each one's blocks are dealt,
+// 32 keys at a time, to as many waves as give about 2048, eight on a CU.
 struct FwdWs {
   size_t po, pm, total;
   int parts;
 };
 FwdWs fwd_ws(const BlkParams& P, Take take = Take()) {
   FwdWs w{};
-  w.parts = P.tiles >= 1024 ? 1 : std::min<int>(P.n, (int)(2048 / P.tiles));
+  w.parts = P.tiles >= 1024 ? 1 : std::min<int>(P.n << (P.lgT - 5), (int)(2048 / P.tiles));
   if (w.parts > 1) {
     w.po = take((size_t)P.tiles * w.parts * BLK_ROWS * blk_dvp(P.dvw) * 4);
     w.pm = take((size_t)P.tiles * w.parts * BLK_ROWS * 8);
@@ -311,8 +311,7 @@ msgla_status msgla_block_attention_step(const msgla_block_config* cfg, const msg
   P.sel = P.sel_out;
   set_fwd(P, w, workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);
-  HIP_TRY(launch_block_append(P, es == 2, st));
-  HIP_TRY(launch_block_select(P, es == 2, st));
+  HIP_TRY(launch_block_step(P, es == 2, st));
   HIP_TRY(launch_block_forward(P, es == 2, st));
   return MSGLA_OK;
 }

@@ -14,7 +14,7 @@ struct BlkHeads {
 constexpr int BLK_ROWS = 16;     // (query, head) rows of a tile: one MFMA tile
 constexpr int BLK_KEYS = 32;     // keys of a step
 constexpr int BLK_MAX_SEL = 64;  // largest n_select
-constexpr int BLK_PIECE = 512;   // blocks whose scores are in LDS at once
+constexpr int BLK_PIECE = 256;   // blocks whose scores are in LDS at once
 
 struct BlkParams {
   BlkHeads q, k, v, o, dout, dq, dk, dv;
@@ -51,7 +51,8 @@ struct BlkParams {
 
 hipError_t launch_block_means(const BlkParams& P, bool bf16_path, hipStream_t st);
 hipError_t launch_block_select(const BlkParams& P, bool bf16_path, hipStream_t st);
-hipError_t launch_block_append(const BlkParams& P, bool bf16_path, hipStream_t st);
+// the step: puts the token into the caches and selects its blocks
+hipError_t launch_block_step(const BlkParams& P, bool bf16_path, hipStream_t st);
 hipError_t launch_block_forward(const BlkParams& P, bool bf16_path, hipStream_t st);
 // many queries: keys and values shared by a workgroup; nb at most BLK_TILES_MAX
 constexpr int BLK_TILES_MAX = 16384;

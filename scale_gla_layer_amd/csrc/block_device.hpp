@@ -123,14 +123,17 @@ struct BlkTile {
   }
 };
 
-// The lists of a tile's queries in LDS, each ended by BLK_END.
+// The lists of a tile's queries in LDS, each ended by BLK_END: one wave.
 constexpr int BLK_LIST = BLK_MAX_SEL + 1;
-__device__ __forceinline__ void blk_lists(const BlkParams& P, const BlkTile& t, int* lists, int tid) {
-  if (tid < P.QT) {
-    const int i = t.i0 + tid, p = blk_position(P, t.b, i);
-    int* l = lists + tid * BLK_LIST;
-    const int32_t* sel = P.sel + (((int64_t)t.b * P.Hkv + t.h) * P.L + min(i, P.L - 1)) * P.n;
-    l[blk_chosen(P, sel, p, [&](int n, int j) { l[n] = j; })] = BLK_END;
+__device__ __forceinline__ void blk_lists(const BlkParams& P, const BlkTile& t, int* lists, int* raw, int lane) {
+  const int rows = min(P.QT, P.L - t.i0);
+  const int32_t* sel = P.sel + (((int64_t)t.b * P.Hkv + t.h) * P.L + t.i0) * P.n;
+  for (int i = lane; i < rows * P.n; i += 64) raw[i] = sel[i];
+  __syncthreads();
+  if (lane < P.QT) {
+    const int p = blk_position(P, t.b, t.i0 + lane);
+    int* l = lists + lane * BLK_LIST;
+    l[blk_chosen(P, raw + lane * P.n, p, [&](int n, int j) { l[n] = j; })] = BLK_END;
   }
 }
 

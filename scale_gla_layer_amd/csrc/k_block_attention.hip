@@ -28,107 +28,150 @@ __device__ __forceinline__ char* out_at(const BlkHeads& t, int64_t b, int64_t i,
   return t.p + b * t.sb + i * t.st + h * t.sh;
 }
 
+// What a wave holds of its tile of rows, and one step of 32 keys.
+template <typename T, int DKP, int DVP> struct FwdTile {
+  Qfrag<T, DKP> q;
+  float m = -__builtin_inff(), l = 0.f;  // running maximum (in units of log 2) and sum
+  f32x4 acc[DVP / 16];
+
+  __device__ FwdTile() {
+#pragma unroll
+    for (int d = 0; d < DVP / 16; ++d) acc[d] = zero4();
+  }
+  // keys k0 .. k0 + 31 for rows at position p (take: the row attends their block); keys behind
+  // `last` have weight 0 in every row: zeroes stand in, whatever is there
+  __device__ __forceinline__ void step(const BlkParams& P, int b, int h, int k0, int last, int p, bool take, char* vs, int lane) {
+    const int r = lane & 15, a = lane >> 4, vw = P.dvw * (int)sizeof(T), kw = P.dkw * (int)sizeof(T);
+    const float sc = P.scale * BLK_LOG2E;
+    __syncthreads();
+    blk_stage<T, DVP, 64>(vs, BLK_KEYS, vw, lane, [&](int i) { return k0 + i <= last ? at(P.v, b, k0 + i, h) : nullptr; });
+    float w[2][4];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+      const char* kr = at(P.k, b, min(k0 + 16 * kt + r, P.S - 1), h);
+      f32x4 s = zero4();
+#pragma unroll
+      for (int c = 0; c < Qfrag<T, DKP>::N; ++c) s = mma_slab<T>(blk_ld(kr, 64 * c + 16 * a, kw), q.f[c], s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[kt][i] = take && k0 + 16 * kt + 4 * a + i <= p ? s[i] * sc : -__builtin_inff();
+    }
+    float mx = m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(w[0][i], w[1][i]));
+    mx = blk_quad_max(mx);
+    const float ref = mx == -__builtin_inff() ? 0.f : mx;  // nothing to attend yet
+    const float corr = __builtin_amdgcn_exp2f(m - ref);
+    m = mx;
+    l *= corr;
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[kt][i] = __builtin_amdgcn_exp2f(w[kt][i] - ref);
+        l += w[kt][i];
+      }
+#pragma unroll
+    for (int d = 0; d < DVP / 16; ++d) acc[d] *= corr;
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < BLK_KEYS / blk_slab<T>(); ++s) {
+      const u32x4 x = blk_pack<T>(w, s);
+#pragma unroll
+      for (int d = 0; d < DVP / 16; ++d)
+        acc[d] = mma_slab<T>(blk_column<T>(vs, blk_pitch<T, DVP>(), s * blk_slab<T>(), d, lane), x, acc[d]);
+    }
+  }
+  __device__ __forceinline__ void store(const BlkParams& P, const BlkRow& row, int64_t tile, int part, int lane) {
+    const int r = lane & 15, a = lane >> 4;
+    l = blk_quad_sum(l);
+    if (!row.in) return;
+    if (P.parts > 1) {
+      const int64_t pr = (tile * P.parts + part) * BLK_ROWS + r;
+      if (a == 0) {
+        P.pm[2 * pr] = m;
+        P.pm[2 * pr + 1] = l;
+      }
+#pragma unroll
+      for (int d = 0; d < DVP / 16; ++d) {
+        const float v[4] = {acc[d][0], acc[d][1], acc[d][2], acc[d][3]};
+        st16(P.po + pr * DVP + 16 * d + 4 * a, pack16<float>(v));
+      }
+      return;
+    }
+    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // no key: 0; a NaN stays
+    char* o = out_at(P.o, row.b, row.i, row.head);
+#pragma unroll
+    for (int d = 0; d < DVP / 16; ++d) {
+      const int c = 16 * d + 4 * a;
+      const float v[4] = {acc[d][0] * inv, acc[d][1] * inv, acc[d][2] * inv, acc[d][3] * inv};
+      if (c < P.dvw) blk_st4<T>(o + c * sizeof(T), v);
+    }
+    if (P.lse && a == 0)
+      P.lse[((int64_t)row.b * P.Hq + row.head) * P.L + row.i] = l == 0.f ? -__builtin_inff() : m * BLK_LN2 + logf(l);
+  }
+};
+
 template <typename T, int DKP, int DVP>
 __global__ __launch_bounds__(64) void k_block_forward(const BlkParams P) {
-  __shared__ int lists[BLK_ROWS * BLK_LIST];
+  __shared__ int lists[BLK_ROWS * BLK_LIST], raw[BLK_ROWS * BLK_MAX_SEL];
   __shared__ __attribute__((aligned(16))) char vs[BLK_KEYS * blk_pitch<T, DVP>()];
-  const int lane = threadIdx.x, r = lane & 15, a = lane >> 4;
-  const int64_t work = blockIdx.x;
-  const int64_t tile = work / P.parts;
-  const int part = (int)(work - tile * P.parts);
+  const int lane = threadIdx.x, r = lane & 15;
+  const int64_t tile = (int64_t)blockIdx.x / P.parts;
+  const int part = (int)((int64_t)blockIdx.x - tile * P.parts);
   const BlkTile t(P, tile);
   const BlkRow row = t.row(P, r);
-  blk_lists(P, t, lists, lane);
-  Qfrag<T, DKP> q;
-  q.load(at(P.q, row.b, row.in ? row.i : 0, row.in ? row.head : 0), P.dkw * sizeof(T), lane, row.in);
+  blk_lists(P, t, lists, raw, lane);
+  FwdTile<T, DKP, DVP> f;
+  f.q.load(at(P.q, row.b, row.in ? row.i : 0, row.in ? row.head : 0), P.dkw * sizeof(T), lane, row.in);
   __syncthreads();
   const int* mine = lists + (row.i - t.i0) * BLK_LIST;
   int cur = row.in && row.p >= 0 ? *mine : BLK_END, seen = 0;
   int last = row.p;  // the tile's last position
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) last = max(last, __shfl_xor(last, o));
-  float m = -__builtin_inff(), l = 0.f;
-  f32x4 acc[DVP / 16];
-#pragma unroll
-  for (int d = 0; d < DVP / 16; ++d) acc[d] = zero4();
-  const float sc = P.scale * BLK_LOG2E;
-  const int vw = P.dvw * (int)sizeof(T), kw = P.dkw * (int)sizeof(T);
   for (;;) {
     const int j = blk_row_min(cur);
     if (j == BLK_END) break;
     const bool member = cur == j;
     if (member) cur = *++mine;
-    if (seen++ % P.parts != part) continue;
     const int first = j << P.lgT;
     for (int k0 = first; k0 < first + (1 << P.lgT) && k0 <= last; k0 += BLK_KEYS) {
-      __syncthreads();
-      // rows behind the tile's last position have weight 0 in every row: zeroes, whatever is there
-      blk_stage<T, DVP, 64>(vs, BLK_KEYS, vw, lane, [&](int i) {
-        return k0 + i <= last ? at(P.v, t.b, k0 + i, t.h) : nullptr;
-      });
-      float p[2][4];
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt) {
-        const char* kr = at(P.k, t.b, min(k0 + 16 * kt + r, P.S - 1), t.h);
-        f32x4 s = zero4();
-#pragma unroll
-        for (int w = 0; w < Qfrag<T, DKP>::N; ++w) s = mma_slab<T>(blk_ld(kr, 64 * w + 16 * a, kw), q.f[w], s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[kt][i] = member && k0 + 16 * kt + 4 * a + i <= row.p ? s[i] * sc : -__builtin_inff();
+      if (P.parts > 1 && seen++ % P.parts != part) continue;
+      f.step(P, t.b, t.h, k0, last, row.p, member, vs, lane);
+    }
+  }
+  f.store(P, row, tile, part, lane);
+}
+
+// One query a sequence (L = 1), its rows the heads of a group: unit u of 32 keys
+// of its list goes to part u mod parts, found by scalar steps.
+template <typename T, int DKP, int DVP>
+__global__ __launch_bounds__(64) void k_block_decode(const BlkParams P) {
+  __shared__ __attribute__((aligned(16))) char vs[BLK_KEYS * blk_pitch<T, DVP>()];
+  const int lane = threadIdx.x;
+  const int64_t tile = (int64_t)blockIdx.x / P.parts;
+  const int part = (int)((int64_t)blockIdx.x - tile * P.parts);
+  const BlkTile t(P, tile);
+  const int mine = lane < P.n ? P.sel[((int64_t)t.b * P.Hkv + t.h) * P.n + lane] : -1;
+  const BlkRow row = t.row(P, lane & 15);
+  FwdTile<T, DKP, DVP> f;
+  f.q.load(at(P.q, row.b, 0, row.in ? row.head : 0), P.dkw * sizeof(T), lane, row.in);
+  const int last = __builtin_amdgcn_readfirstlane(blk_position(P, t.b, 0));  // the query's position
+  if (last >= 0) {
+    const int own = last >> P.lgT, lg_units = P.lgT - 5;
+    int before = -1, chosen = 0;  // the rule of blk_chosen
+    for (int e = 0; e < P.n; ++e) {
+      const int j = __builtin_amdgcn_readlane(mine, e);
+      if (j <= before || j > own) continue;
+      before = j;
+      for (int s = 0; s < 1 << lg_units; ++s) {
+        const int k0 = (j << P.lgT) + BLK_KEYS * s;
+        if (((chosen << lg_units) + s) % P.parts == part && k0 <= last) f.step(P, t.b, t.h, k0, last, row.p, true, vs, lane);
       }
-      float mx = m;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx = fmaxf(mx, fmaxf(p[0][i], p[1][i]));
-      mx = blk_quad_max(mx);
-      const float ref = mx == -__builtin_inff() ? 0.f : mx;  // nothing to attend yet
-      const float corr = __builtin_amdgcn_exp2f(m - ref);
-      m = mx;
-      l *= corr;
-#pragma unroll
-      for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          p[kt][i] = __builtin_amdgcn_exp2f(p[kt][i] - ref);
-          l += p[kt][i];
-        }
-#pragma unroll
-      for (int d = 0; d < DVP / 16; ++d) acc[d] *= corr;
-      __syncthreads();
-#pragma unroll
-      for (int s = 0; s < BLK_KEYS / blk_slab<T>(); ++s) {
-        const u32x4 w = blk_pack<T>(p, s);
-#pragma unroll
-        for (int d = 0; d < DVP / 16; ++d)
-          acc[d] = mma_slab<T>(blk_column<T>(vs, blk_pitch<T, DVP>(), s * blk_slab<T>(), d, lane), w, acc[d]);
-      }
+      ++chosen;
     }
   }
-  l = blk_quad_sum(l);
-  if (P.parts > 1) {
-    const int64_t pr = (tile * P.parts + part) * BLK_ROWS + r;
-    if (a == 0) {
-      P.pm[2 * pr] = m;
-      P.pm[2 * pr + 1] = l;
-    }
-#pragma unroll
-    for (int d = 0; d < DVP / 16; ++d) {
-      const float v[4] = {acc[d][0], acc[d][1], acc[d][2], acc[d][3]};
-      st16(P.po + pr * DVP + 16 * d + 4 * a, pack16<float>(v));
-    }
-    return;
-  }
-  if (!row.in) return;
-  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // no key: 0; a NaN stays
-  char* o = out_at(P.o, row.b, row.i, row.head);
-#pragma unroll
-  for (int d = 0; d < DVP / 16; ++d) {
-    const int c = 16 * d + 4 * a;
-    const float v[4] = {acc[d][0] * inv, acc[d][1] * inv, acc[d][2] * inv, acc[d][3] * inv};
-    if (c < P.dvw) blk_st4<T>(o + c * sizeof(T), v);
-  }
-  if (P.lse && a == 0)
-    P.lse[((int64_t)row.b * P.Hq + row.head) * P.L + row.i] = l == 0.f ? -__builtin_inff() : m * BLK_LN2 + logf(l);
+  f.store(P, row, tile, part, lane);
 }
 
 // Joins a row's partial outputs.
@@ -139,10 +182,12 @@ template <typename T, int DVP> __global__ __launch_bounds__(64) void k_block_joi
   if (!row.in) return;
   const int64_t pr = tile * P.parts * BLK_ROWS + r;
   float m = -__builtin_inff(), l = 0.f, o[DVP / 64];
+#pragma unroll 4
   for (int k = 0; k < P.parts; ++k) m = fmaxf(m, P.pm[2 * (pr + k * BLK_ROWS)]);
   const float ref = m == -__builtin_inff() ? 0.f : m;
 #pragma unroll
   for (int d = 0; d < DVP / 64; ++d) o[d] = 0.f;
+#pragma unroll 4
   for (int k = 0; k < P.parts; ++k) {
     const int64_t at = pr + k * BLK_ROWS;
     const float w = __builtin_amdgcn_exp2f(P.pm[2 * at] - ref);
@@ -183,12 +228,12 @@ template <typename T> __global__ __launch_bounds__(256) void k_block_delta(const
 
 // dq = scale sum_j p_j (do . v_j - delta) k_j, the tiles and steps of the forward.
 template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_block_dq(const BlkParams P) {
-  __shared__ int lists[BLK_ROWS * BLK_LIST];
+  __shared__ int lists[BLK_ROWS * BLK_LIST], raw[BLK_ROWS * BLK_MAX_SEL];
   __shared__ __attribute__((aligned(16))) char ks[BLK_KEYS * blk_pitch<T, DKP>()];
   const int lane = threadIdx.x, r = lane & 15, a = lane >> 4;
   const BlkTile t(P, blockIdx.x);
   const BlkRow row = t.row(P, r);
-  blk_lists(P, t, lists, lane);
+  blk_lists(P, t, lists, raw, lane);
   Qfrag<T, DKP> q;
   Qfrag<T, DVP> g;
   const int vw = P.dvw * (int)sizeof(T), kw = P.dkw * (int)sizeof(T);
@@ -256,7 +301,9 @@ template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_
 
 template <typename T, int DKP, int DVP> struct Run {
   static void forward(const BlkParams& P, hipStream_t st) {
-    hipLaunchKernelGGL((k_block_forward<T, DKP, DVP>), dim3((unsigned)(P.tiles * P.parts)), dim3(64), 0, st, P);
+    const dim3 grid((unsigned)(P.tiles * P.parts));
+    if (P.L == 1) hipLaunchKernelGGL((k_block_decode<T, DKP, DVP>), grid, dim3(64), 0, st, P);
+    else hipLaunchKernelGGL((k_block_forward<T, DKP, DVP>), grid, dim3(64), 0, st, P);
     if (P.parts > 1)
       hipLaunchKernelGGL((k_block_join<T, DVP>), dim3((unsigned)(P.tiles * BLK_ROWS)), dim3(64), 0, st, P);
   }

@@ -5,9 +5,11 @@
 // with c_j the block's mean key.  Sums are in 64 bits, where products of the
 // inputs are all but exact: the choice is the inputs', not the summation
 // order's.  The scores of 16 queries against 16 blocks are a chain of 64-bit
-// MFMAs; their ordered bit patterns go to LDS, where one wave finds a row's
-// n-th largest by bisection on the bits (a handful of steps: it stops once the
-// count is right) and writes the chosen blocks in ascending order.
+// MFMAs; their ordered bit patterns go to LDS.  There 16 lanes take a row, four
+// rows a wave, and find its n-th largest key by bisection on the upper 32 bits
+// (about 20 steps: each lane counts its own keys, four lane exchanges add up; a
+// row is done once its count is right), going on to the lower ones only where
+// that leaves a tie, and write the chosen blocks in ascending order.
 #include "block_device.hpp"
 
 namespace msgla {
@@ -57,25 +59,6 @@ template <typename T> __global__ __launch_bounds__(64) void k_block_means(const 
   block_mean<T>(P.lgT, P.dkw * (int)sizeof(T), out, threadIdx.x, [&](int i) { return base + i * P.k.st; });
 }
 
-// One token's key and value into the caches, and the mean of the block it completes.
-template <typename T> __global__ __launch_bounds__(64) void k_block_append(const BlkParams P) {
-  const int b = blockIdx.x / P.Hkv, h = blockIdx.x % P.Hkv, lane = threadIdx.x;
-  const int p = P.start[b];
-  if (p < 0 || p >= P.S) return;
-  const char* nk = P.kt.p + b * P.kt.sb + h * P.kt.sh;
-  const char* nv = P.vt.p + b * P.vt.sb + h * P.vt.sh;
-  char* kr = P.k.p + b * P.k.sb + (int64_t)p * P.k.st + h * P.k.sh;
-  char* vr = P.v.p + b * P.v.sb + (int64_t)p * P.v.st + h * P.v.sh;
-  for (int c = 16 * lane; c < P.dkw * (int)sizeof(T); c += 1024) st16(kr + c, ld16(nk + c));
-  for (int c = 16 * lane; c < P.dvw * (int)sizeof(T); c += 1024) st16(vr + c, ld16(nv + c));
-  const int last = (1 << P.lgT) - 1;
-  if ((p & last) != last) return;
-  const int j = p >> P.lgT;
-  const char* base = P.k.p + b * P.k.sb + ((int64_t)j << P.lgT) * P.k.st + h * P.k.sh;
-  block_mean<T>(P.lgT, P.dkw * (int)sizeof(T), P.means + (((int64_t)b * P.Hkv + h) * P.nb + j) * P.dkw, lane,
-                [&](int i) { return i == last ? nk : base + i * P.k.st; });
-}
-
 // Bits whose order as whole numbers is the scores' (a NaN ranks as minus infinity).
 __device__ __forceinline__ uint64_t score_key(double s) {
   if (s != s) s = -__builtin_inf();
@@ -86,44 +69,88 @@ __device__ __forceinline__ uint64_t score_key(double s) {
 constexpr uint64_t FORCED = ~0ull;
 constexpr int SEL_WAVES = 4, SEL_ROWS = 16;
 
+// Sum over the 16 lanes of a row group (DPP rotations within 16 lanes).
+__device__ __forceinline__ int row16_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x121, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x122, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x124, 0xf, 0xf, false);
+  return v + __builtin_amdgcn_update_dpp(0, v, 0x128, 0xf, 0xf, false);
+}
+// the 16 bits of a wave's ballot that belong to the lane's row group
+__device__ __forceinline__ uint32_t row16_ballot(bool v, int lane) {
+  const uint64_t m = __ballot(v);
+  return ((lane & 32 ? (uint32_t)(m >> 32) : (uint32_t)m) >> (lane & 16)) & 0xffffu;
+}
+
+// The largest T that at least n of a row's values reach, found bit by bit;
+// count(T) is the number of values >= T.  exact: just n do.
+template <class Count> __device__ __forceinline__ uint32_t bisect(int n, bool active, bool& exact, Count count) {
+  uint32_t t = 0;
+  exact = false;
+  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+    const uint32_t want = t | bit;
+    const int c = count(want);
+    if (!exact && c >= n) {
+      t = want;
+      exact = c == n;
+    }
+    if (__all(exact || !active)) break;
+  }
+  return t;
+}
+
 template <typename T, int DKP, int PIECE> __global__ __launch_bounds__(64 * SEL_WAVES) void k_block_select(const BlkParams P) {
+  constexpr bool MULTI = PIECE == BLK_PIECE;  // more blocks than one piece holds, perhaps
+  constexpr int CARRY = MULTI ? BLK_MAX_SEL : 1, CS = MULTI ? BLK_MAX_SEL / 16 : 0, SLOTS = CS + PIECE / 16;
+  constexpr int QP = DKP + 2, PER = DKP / 16;  // row pitch of the query sums; elements a thread sums
+  __shared__ double qsum[SEL_ROWS][QP];
   __shared__ uint64_t key[SEL_ROWS][PIECE];
-  __shared__ uint64_t ckey[SEL_ROWS][BLK_MAX_SEL];  // chosen so far, while pieces remain
-  __shared__ int cblk[SEL_ROWS][BLK_MAX_SEL];
+  __shared__ uint64_t ckey[SEL_ROWS][CARRY];  // chosen so far, while pieces remain
+  __shared__ int cblk[SEL_ROWS][CARRY];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c16 = lane & 15, a = lane >> 4;
   const int per = (P.L + SEL_ROWS - 1) / SEL_ROWS;
   const int64_t bh = blockIdx.x / per;
   const int i0 = (int)(blockIdx.x - bh * per) * SEL_ROWS, b = (int)(bh / P.Hkv), h = (int)(bh - (int64_t)b * P.Hkv);
   int32_t* out = P.sel_out + (bh * P.L + i0) * P.n;
-  // a positions' own blocks: row l % 16 for every lane, and the greatest
+  // the positions' own blocks: row l % 16 for every lane, and the greatest
   const int mypos = blk_position(P, b, i0 + c16);
   const int myown = mypos < 0 ? -1 : mypos >> P.lgT;
   int top = myown;
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor(top, o));
-  // the group's query sums, elements 16 g + 4 a .. + 3 of row l % 16
-  double q[DKP / 16][4];
   {
-    const char* qr = P.q.p + b * P.q.sb + (int64_t)min(i0 + c16, P.L - 1) * P.q.st + (int64_t)h * P.G * P.q.sh;
+    // the group's query sums, PER elements of a row each thread
+    const int r = threadIdx.x >> 4, e0 = c16 * PER;
+    double q[PER];
 #pragma unroll
-    for (int g = 0; g < DKP / 16; ++g) {
-      const int e0 = 16 * g + 4 * a;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) q[g][e] = 0.0;
-      if (e0 < P.dkw && mypos >= 0)
-        for (int u = 0; u < P.G; ++u) {
-          const T* p = reinterpret_cast<const T*>(qr + u * P.q.sh) + e0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) q[g][e] += (double)to_f32(p[e]);
+    for (int e = 0; e < PER; ++e) q[e] = 0.0;
+    if (e0 < P.dkw && blk_position(P, b, i0 + r) >= 0) {
+      const char* qr = P.q.p + b * P.q.sb + (int64_t)(i0 + r) * P.q.st + (int64_t)h * P.G * P.q.sh + e0 * sizeof(T);
+      for (int u = 0; u < P.G; ++u) {
+        const char* p = qr + u * P.q.sh;  // d_k is a multiple of 8
+        float f[8];
+        if constexpr (PER * sizeof(T) == 8) {
+          const u32x2 w = ld8(p);
+          unpack16<T>(u32x4{w[0], w[1], 0u, 0u}, f);
+        } else {
+          unpack16<T>(ld16(p), f);
+          if constexpr (PER * sizeof(T) == 32) unpack16<T>(ld16(p + 16), f + 4);
         }
+#pragma unroll
+        for (int e = 0; e < PER; ++e) q[e] += (double)f[e];
+      }
     }
+#pragma unroll
+    for (int e = 0; e < PER; ++e) qsum[r][e0 + e] = q[e];
   }
   const float* means = P.means + bh * P.nb * P.dkw;
-  for (int i = threadIdx.x; i < SEL_ROWS * BLK_MAX_SEL; i += 64 * SEL_WAVES) ckey[i / BLK_MAX_SEL][i % BLK_MAX_SEL] = 0;
-  int carried[SEL_ROWS / SEL_WAVES];
+  __syncthreads();
+  double q[DKP / 16][4];  // elements 16 g + 4 a .. + 3 of row l % 16
 #pragma unroll
-  for (int k = 0; k < SEL_ROWS / SEL_WAVES; ++k) carried[k] = 0;
-  int piece = 0;
+  for (int g = 0; g < DKP / 16; ++g)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) q[g][e] = qsum[c16][16 * g + 4 * a + e];
+  int carried = 0, piece = 0;
   do {
     const int stop = min(piece + PIECE, top + 1);  // blocks [piece, stop)
     for (int j0 = piece + 16 * wave; j0 < stop; j0 += 16 * SEL_WAVES) {
@@ -132,10 +159,10 @@ template <typename T, int DKP, int PIECE> __global__ __launch_bounds__(64 * SEL_
 #pragma unroll
       for (int g = 0; g < DKP / 16; ++g) {
         const int e0 = 16 * g + 4 * a;
-        const bool in = e0 < P.dkw;
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (e0 < P.dkw) unpack16<float>(ld16(m + e0), f);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          s = __builtin_amdgcn_mfma_f64_16x16x4f64(q[g][e], in ? (double)m[e0 + e] : 0.0, s, 0, 0, 0);
+        for (int e = 0; e < 4; ++e) s = __builtin_amdgcn_mfma_f64_16x16x4f64(q[g][e], (double)f[e], s, 0, 0, 0);
       }
       // element i: row l / 16 + 4 i, block l % 16
 #pragma unroll
@@ -149,74 +176,222 @@ template <typename T, int DKP, int PIECE> __global__ __launch_bounds__(64 * SEL_
     }
     __syncthreads();
     const bool more = stop <= top;
-    constexpr int SLOTS = PIECE / 64 + 1;
+    const int r = 4 * wave + a, slots = (stop - piece + 15) >> 4;  // the lane's row; its keys c16, c16 + 16, ..
+    uint32_t k[SLOTS];
 #pragma unroll
-    for (int rr = 0; rr < SEL_ROWS / SEL_WAVES; ++rr) {
-      const int r = wave * (SEL_ROWS / SEL_WAVES) + rr;
-      if (i0 + r >= P.L) break;
-      uint64_t k[SLOTS];
-      const int cb = cblk[r][lane];
-      k[0] = lane < carried[rr] ? ckey[r][lane] : 0;
+    for (int e = 0; e < CS; ++e) k[e] = 16 * e + c16 < carried ? (uint32_t)(ckey[r][16 * e + c16] >> 32) : 0;
 #pragma unroll
-      for (int e = 1; e < SLOTS; ++e) {
-        const int j = piece + 64 * (e - 1) + lane;
-        k[e] = j < stop ? key[r][j - piece] : 0;
+    for (int e = CS; e < SLOTS; ++e) k[e] = e - CS < slots ? (uint32_t)(key[r][16 * (e - CS) + c16] >> 32) : 0;
+    auto low = [&](int e) -> uint32_t {  // of a key whose upper half is not 0
+      return e < CS ? (uint32_t)ckey[r][16 * e + c16] : (uint32_t)key[r][16 * (e - CS) + c16];
+    };
+    auto count = [&](uint32_t t) {
+      int c = 0;
+#pragma unroll
+      for (int e = 0; e < SLOTS; ++e)
+        if (e < CS || e - CS < slots) c += k[e] >= t ? 1 : 0;
+      return row16_sum(c);
+    };
+    // Every score's upper half is above 0 (minus infinity's is 0x000fffff).  With
+    // n of them or fewer all are taken.
+    uint32_t hi = 1, lo = 0;
+    bool all_hi = true, all_lo = true;  // every key with that upper half is taken; every one that reaches (hi, lo)
+    int ties = 0;
+    const int total = count(1);
+    if (__any(total > P.n)) {
+      const bool cut = total > P.n;
+      bool exact;
+      const uint32_t t = bisect(P.n, cut, exact, count);
+      if (cut) hi = t, all_hi = exact;
+      if (!__all(all_hi)) {
+        const int above = hi == ~0u ? 0 : count(hi + 1), want = P.n - above;
+        auto count_low = [&](uint32_t t2) {
+          int c = 0;
+          for (int e = 0; e < SLOTS; ++e)
+            if ((e < CS || e - CS < slots) && k[e] == hi) c += low(e) >= t2 ? 1 : 0;
+          return row16_sum(c);
+        };
+        const uint32_t t2 = bisect(want, !all_hi, exact, count_low);
+        lo = t2;
+        all_lo = exact;
+        ties = want - (t2 == ~0u ? 0 : count_low(t2 + 1));
       }
-      auto count = [&](uint64_t t) {
-        int c = 0;
-#pragma unroll
-        for (int e = 0; e < SLOTS; ++e) c += __popcll(__ballot(k[e] >= t));
-        return c;
-      };
-      // the largest threshold that at least n keys reach (1, if there are no more than n)
-      uint64_t t = 1;
-      bool exact = true;
-      if (count(1) > P.n) {
-        t = 0;
-        exact = false;
-        for (int bit = 63; bit >= 0; --bit) {
-          const uint64_t want = t | (1ull << bit);
-          const int c = count(want);
-          if (c >= P.n) {
-            t = want;
-            if (c == P.n) {
-              exact = true;
-              break;
-            }
-          }
-        }
-      }
-      int ties = exact ? 65536 : P.n - count(t + 1);  // of the keys equal to t, the first so many
-      int base = 0;
-#pragma unroll
-      for (int e = 0; e < SLOTS; ++e) {
-        const uint64_t eq = __ballot(k[e] == t), below = (1ull << lane) - 1;
-        const bool take = k[e] > t || (k[e] == t && (exact || (int)__popcll(eq & below) < ties));
-        if (!exact) ties -= min(ties, (int)__popcll(eq));
-        const uint64_t took = __ballot(take);
-        if (take) {
-          const int at = base + (int)__popcll(took & below);
-          const int j = e == 0 ? cb : piece + 64 * (e - 1) + lane;
-          if (more) {
-            ckey[r][at] = k[e];
-            cblk[r][at] = j;
-          } else {
-            out[(int64_t)r * P.n + at] = j;
-          }
-        }
-        base += (int)__popcll(took);
-      }
-      carried[rr] = base;
-      if (!more && lane >= base && lane < P.n) out[(int64_t)r * P.n + lane] = -1;
     }
+    int base = 0;
+#pragma unroll
+    for (int e = 0; e < SLOTS; ++e) {
+      if (e >= CS && e - CS >= slots) continue;
+      bool take = k[e] > hi || (k[e] == hi && all_hi);
+      if (!__all(all_hi)) {
+        const uint32_t l = k[e] == hi ? low(e) : 0;
+        const bool equal = !all_hi && k[e] == hi && l == lo;
+        const uint32_t eq = row16_ballot(equal, lane);
+        const int before = __popc(eq & ((1u << c16) - 1));
+        take = take || (!all_hi && k[e] == hi && l > lo) || (equal && (all_lo || before < ties));
+        ties -= min(ties, (int)__popc(eq));
+      }
+      const uint32_t took = row16_ballot(take, lane);
+      if (take) {
+        const int at = base + (int)__popc(took & ((1u << c16) - 1));
+        const int j = e < CS ? cblk[r][16 * e + c16] : piece + 16 * (e - CS) + c16;
+        if (more) {
+          // lists only shrink: entry `at` of the next list was read with this slot or before
+          ckey[r][at] = e < CS ? ckey[r][16 * e + c16] : key[r][16 * (e - CS) + c16];
+          cblk[r][at] = j;
+        } else if (i0 + r < P.L) {
+          out[(int64_t)r * P.n + at] = j;
+        }
+      }
+      base += (int)__popc(took);
+    }
+    carried = base;
+    if (!more && i0 + r < P.L)
+      for (int e = base + c16; e < P.n; e += 16) out[(int64_t)r * P.n + e] = -1;
     __syncthreads();
     piece += PIECE;
   } while (piece <= top);
 }
 
+// The streaming step's first half, one workgroup a sequence and key-value head:
+// the last wave puts the token's key and value into the caches and renews the
+// mean of the block that this completes (which is the query's own: it is not
+// scored); all waves score the blocks before, four lanes a block; the first one
+// finds the best of up to STEP_PIECE at a time, 64 lanes on the one row.
+constexpr int STEP_WAVES = 16, STEP_PIECE = 512;
+
+template <typename T, int DKP> __global__ __launch_bounds__(64 * STEP_WAVES) void k_block_step(const BlkParams P) {
+  constexpr int PER = DKP / 4, SLOTS = STEP_PIECE / 64 + 1;
+  __shared__ uint64_t key[STEP_PIECE];
+  __shared__ uint64_t ckey[64];
+  __shared__ int cblk[64];
+  const int b = blockIdx.x / P.Hkv, h = blockIdx.x % P.Hkv, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int p = P.start[b];
+  int32_t* out = P.sel_out + (int64_t)blockIdx.x * P.n;
+  if (p < 0 || p >= P.S) {
+    if (tid < P.n) out[tid] = -1;
+    return;
+  }
+  const int own = p >> P.lgT;
+  float* means = P.means + (int64_t)blockIdx.x * P.nb * P.dkw;
+  if (wave == STEP_WAVES - 1) {
+    const char* nk = P.kt.p + b * P.kt.sb + h * P.kt.sh;
+    const char* nv = P.vt.p + b * P.vt.sb + h * P.vt.sh;
+    char* kr = P.k.p + b * P.k.sb + (int64_t)p * P.k.st + h * P.k.sh;
+    char* vr = P.v.p + b * P.v.sb + (int64_t)p * P.v.st + h * P.v.sh;
+    for (int c = 16 * lane; c < P.dkw * (int)sizeof(T); c += 1024) st16(kr + c, ld16(nk + c));
+    for (int c = 16 * lane; c < P.dvw * (int)sizeof(T); c += 1024) st16(vr + c, ld16(nv + c));
+    const int last = (1 << P.lgT) - 1;
+    if ((p & last) == last) {
+      const char* base = P.k.p + b * P.k.sb + ((int64_t)own << P.lgT) * P.k.st + h * P.k.sh;
+      block_mean<T>(P.lgT, P.dkw * (int)sizeof(T), means + (int64_t)own * P.dkw, lane,
+                    [&](int i) { return i == last ? nk : base + i * P.k.st; });
+    }
+  }
+  // the group's query sums, elements PER (l % 4) .. of each four lanes
+  const int e0 = (lane & 3) * PER;
+  double q[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) q[e] = 0.0;
+#pragma unroll 4
+  for (int u = 0; u < P.G; ++u) {
+    const char* qr = P.q.p + b * P.q.sb + (int64_t)(h * P.G + u) * P.q.sh;
+#pragma unroll
+    for (int c = 0; c < PER; c += per16<T>()) {
+      float f[per16<T>()];
+      if (e0 + c < P.dkw) {
+        unpack16<T>(ld16(qr + (e0 + c) * sizeof(T)), f);
+#pragma unroll
+        for (int e = 0; e < per16<T>(); ++e) q[c + e] += (double)f[e];
+      }
+    }
+  }
+  int carried = 0, piece = 0;
+  do {
+    const int stop = min(piece + STEP_PIECE, own + 1);
+    for (int j0 = piece + (tid >> 2); j0 - (lane >> 2) < stop; j0 += 16 * STEP_WAVES) {
+      const int j = min(j0, own);
+      double s = 0.0;
+#pragma unroll
+      for (int c = 0; c < PER; c += 4)
+        if (e0 + c < P.dkw) {
+          float f[4];
+          unpack16<float>(ld16(means + (int64_t)j * P.dkw + e0 + c), f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s += q[c + e] * (double)f[e];
+        }
+      s += __shfl_xor(s, 1);
+      s += __shfl_xor(s, 2);
+      if ((lane & 3) == 0 && j0 < stop)
+        key[j0 - piece] = j0 < P.n_first || j0 > own - P.n_recent ? FORCED : score_key(s);
+    }
+    __syncthreads();
+    if (wave == 0) {
+      const bool more = stop <= own;
+      uint64_t k[SLOTS];
+      const int cb = cblk[lane];
+      k[0] = lane < carried ? ckey[lane] : 0;
+#pragma unroll
+      for (int e = 1; e < SLOTS; ++e) k[e] = 64 * (e - 1) + lane < stop - piece ? key[64 * (e - 1) + lane] : 0;
+      // as in k_block_select, the row's values in all lanes: the upper halves first,
+      // the lower ones where those tie
+      auto count = [&](auto reach) {
+        int c = 0;
+#pragma unroll
+        for (int e = 0; e < SLOTS; ++e) c += (int)__popcll(__ballot(reach((uint32_t)(k[e] >> 32), (uint32_t)k[e])));
+        return c;
+      };
+      auto largest = [&](int n, bool& exact, auto reach) {
+        uint32_t t = 0;
+        exact = false;
+        for (uint32_t bit = 1u << 31; bit && !exact; bit >>= 1) {
+          const int c = count([&](uint32_t u, uint32_t v) { return reach(u, v, t | bit); });
+          if (c >= n) t |= bit, exact = c == n;
+        }
+        return t;
+      };
+      uint32_t hi = 1, lo = 0;
+      bool all_hi = true, all_lo = true;
+      int ties = 0;
+      if (count([](uint32_t u, uint32_t) { return u != 0; }) > P.n) {
+        hi = largest(P.n, all_hi, [](uint32_t u, uint32_t, uint32_t t) { return u >= t; });
+        if (!all_hi) {
+          const int want = P.n - count([&](uint32_t u, uint32_t) { return u > hi; });
+          lo = largest(want, all_lo, [&](uint32_t u, uint32_t v, uint32_t t) { return u == hi && v >= t; });
+          ties = want - count([&](uint32_t u, uint32_t v) { return u == hi && v > lo; });
+        }
+      }
+      int base = 0;
+      const uint64_t below = (1ull << lane) - 1, cut = (uint64_t)hi << 32 | lo;
+#pragma unroll
+      for (int e = 0; e < SLOTS; ++e) {
+        const uint32_t u = (uint32_t)(k[e] >> 32);
+        const uint64_t eq = __ballot(!all_hi && k[e] == cut);
+        const bool take = all_hi ? u >= hi : k[e] > cut || (k[e] == cut && (all_lo || (int)__popcll(eq & below) < ties));
+        ties -= min(ties, (int)__popcll(eq));
+        const uint64_t took = __ballot(take);
+        if (take) {
+          const int at = base + (int)__popcll(took & below), j = e == 0 ? cb : piece + 64 * (e - 1) + lane;
+          if (more) {
+            ckey[at] = k[e];
+            cblk[at] = j;
+          } else {
+            out[at] = j;
+          }
+        }
+        base += (int)__popcll(took);
+      }
+      carried = base;
+      if (!more && lane >= base && lane < P.n) out[lane] = -1;
+    }
+    __syncthreads();
+    piece += STEP_PIECE;
+  } while (piece <= own);
+}
+
 template <typename T, int DKP> void select_t(const BlkParams& P, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)P.B * P.Hkv * ((P.L + SEL_ROWS - 1) / SEL_ROWS))), block(64 * SEL_WAVES);
-  // the smaller score buffer lets five workgroups share a CU's LDS instead of two
+  // the smaller score buffer lets five workgroups share a CU's LDS instead of one
   if (P.nb <= 128) hipLaunchKernelGGL((k_block_select<T, DKP, 128>), grid, block, 0, st, P);
   else hipLaunchKernelGGL((k_block_select<T, DKP, BLK_PIECE>), grid, block, 0, st, P);
 }
@@ -230,10 +405,13 @@ hipError_t launch_block_means(const BlkParams& P, bool bf16_path, hipStream_t st
   return hipGetLastError();
 }
 
-hipError_t launch_block_append(const BlkParams& P, bool bf16_path, hipStream_t st) {
-  const dim3 grid((unsigned)(P.B * P.Hkv));
-  if (bf16_path) hipLaunchKernelGGL(k_block_append<bf16>, grid, dim3(64), 0, st, P);
-  else hipLaunchKernelGGL(k_block_append<float>, grid, dim3(64), 0, st, P);
+hipError_t launch_block_step(const BlkParams& P, bool bf16_path, hipStream_t st) {
+  const dim3 grid((unsigned)(P.B * P.Hkv)), block(64 * STEP_WAVES);
+  const bool k64 = blk_dkp(P.dkw) == 64;
+  if (bf16_path && k64) hipLaunchKernelGGL((k_block_step<bf16, 64>), grid, block, 0, st, P);
+  else if (bf16_path) hipLaunchKernelGGL((k_block_step<bf16, 128>), grid, block, 0, st, P);
+  else if (k64) hipLaunchKernelGGL((k_block_step<float, 64>), grid, block, 0, st, P);
+  else hipLaunchKernelGGL((k_block_step<float, 128>), grid, block, 0, st, P);
   return hipGetLastError();
 }
 
