@@ -347,44 +347,81 @@ def msgla_forward_noalloc(cfg: MsglaConfig, packed, x, B: int, L: int, out, stat
 # Tensors are checked here against what the C entry points assume of the
 # pointers they get; a ValueError names the argument.
 
+_TORCH = None
+
+
+def _t():
+    """torch, imported at the first call."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
+
+
 def _storage(cfg):
-    import torch
-    return torch.bfloat16 if cfg.dtype == BF16 else torch.float32
+    return _t().bfloat16 if cfg.dtype == BF16 else _t().float32
 
 
-def _tensor(name: str, t, shape, dtype, device, contiguous=False):
-    """t itself, on `device` (given as a tensor's), of this shape and type, its last dimension dense."""
-    if t.device != device or t.device.type != "cuda":
+def _raw_stream(stream) -> int:
+    """The current stream of the current device, unless one is given."""
+    if stream is not None:
+        return _stream(stream)
+    raw = getattr(_t()._C, "_cuda_getCurrentRawStream", None)  # without making a Stream object
+    return _stream(None) if raw is None else raw(_t().cuda.current_device())
+
+
+def _tensor(name: str, t, shape, dtype, device) -> tuple:
+    """The strides of t, which has to have this shape (a tuple) and type on `device` (a ROCm device's)
+    and dense rows in its last dimension."""
+    strides = t.stride()
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and \
+            (strides[-1] == 1 or shape[-1] == 1):
+        return strides
+    if t.device != device or not t.is_cuda:
         raise ValueError(f"{name} must be on {device}, a ROCm device: it is on {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}: it is {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}: it has {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}: it has {tuple(t.shape)}")
+    raise ValueError(f"the last dimension of {name} must be dense")
+
+
+def _dense(name: str, t, shape, dtype, device):
+    """The address of a contiguous t, or None for None."""
+    if t is None:
+        return None
+    _tensor(name, t, shape, dtype, device)
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be dense")
-    return t
+    return t.data_ptr()
 
 
 def _f32(name: str, t, shape, device):
-    import torch
-    return None if t is None else _tensor(name, t, shape, torch.float32, device, contiguous=True)
+    return _dense(name, t, shape, _t().float32, device)
 
 
 def _apart(name: str, t):
     """An output whose rows do not overlap (no broadcast dimension of more than one entry)."""
+    if t.is_contiguous():
+        return
     size = 1
     for n, s in sorted(((n, s) for n, s in zip(t.shape, t.stride()) if n > 1), key=lambda p: p[1]):
         if s < size:
             raise ValueError(f"the rows of {name} overlap")
         size = s * (n - 1) + size
-    return t
 
 
-def _rows(t) -> CRows:
+def _rows(name: str, t, shape, dtype, device) -> CRows:
     """[B, L, width], or [B, width] as rows of one position."""
-    return CRows(t.data_ptr(), t.stride(0), t.stride(1) if t.dim() == 3 else 0)
+    st = _tensor(name, t, shape, dtype, device)
+    return CRows(t.data_ptr(), st[0], st[1] if len(st) == 3 else 0)
+
+
+def _rows_out(name: str, t, shape, dtype, device) -> CRows:
+    rows = _rows(name, t, shape, dtype, device)
+    _apart(name, t)
+    return rows
 
 
 _REC_CACHE: dict = {}
@@ -407,73 +444,72 @@ def msgla_recurrence_backward_workspace_bytes(cfg: RecurrenceConfig, B: int, L: 
 
 
 def _recurrence_inputs(cfg, x, z, bias, mask, h_in, dims):
-    import torch
+    """(shape, type, device, the C arguments of x, z, bias, mask and h_in)"""
     if x.dim() != dims:
         raise ValueError(f"x must have {dims} dimensions: it has {x.dim()}")
-    shape = (*x.shape[:-1], cfg.width)
-    _tensor("x", x, shape, _storage(cfg), x.device)
-    _tensor("z", z, shape, _storage(cfg), x.device)
-    _f32("bias", bias, (cfg.width,), x.device)
-    _f32("h_in", h_in, (shape[0], cfg.width), x.device)
-    if mask is not None:
-        _tensor("mask", mask, shape[:-1], torch.uint8, x.device, contiguous=True)
-    return shape
+    shape, dt, dev = (*x.shape[:-1], cfg.width), _storage(cfg), x.device
+    return shape, dt, dev, (_rows("x", x, shape, dt, dev), _rows("z", z, shape, dt, dev),
+                            _f32("bias", bias, (cfg.width,), dev),
+                            _dense("mask", mask, shape[:-1], _t().uint8, dev),
+                            _f32("h_in", h_in, (shape[0], cfg.width), dev))
+
+
+def _bytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def msgla_recurrence_forward(cfg: RecurrenceConfig, x, z, y, workspace, bias=None, mask=None, h_in=None, h_out=None,
                              stream=None):
     """x, z, y: [B, L, width] (any strides with a dense last dimension); bias [width], h_in and h_out
     [B, width] fp32; mask: [B, L] uint8."""
-    shape = _recurrence_inputs(cfg, x, z, bias, mask, h_in, 3)
-    _apart("y", _tensor("y", y, shape, _storage(cfg), x.device))
-    _f32("h_out", h_out, (shape[0], cfg.width), x.device)
+    shape, dt, dev, args = _recurrence_inputs(cfg, x, z, bias, mask, h_in, 3)
     st = load_library().msgla_recurrence_forward(
-        ctypes.byref(c_recurrence_config(cfg)), _rows(x), _rows(z), _ptr(bias), _ptr(mask), _ptr(h_in), shape[0],
-        shape[1], _rows(y), _ptr(h_out), _ptr(workspace), 0 if workspace is None else workspace.numel() *
-        workspace.element_size(), _stream(stream))
+        c_recurrence_config(cfg), *args, shape[0], shape[1], _rows_out("y", y, shape, dt, dev),
+        _f32("h_out", h_out, (shape[0], cfg.width), dev), _ptr(workspace), _bytes(workspace), _raw_stream(stream))
     _check("msgla_recurrence_forward", st)
 
 
 def msgla_recurrence_backward(cfg: RecurrenceConfig, x, z, dy, dx, dz, workspace, bias=None, mask=None, h_in=None,
                               dh_out=None, dbias=None, dh_in=None, stream=None):
     """dy (or None for 0), dx, dz: as x; dh_out, dh_in: [B, width] fp32; dbias: [width] fp32."""
-    shape = _recurrence_inputs(cfg, x, z, bias, mask, h_in, 3)
-    if dy is not None:
-        _tensor("dy", dy, shape, _storage(cfg), x.device)
-    for name, t in (("dx", dx), ("dz", dz)):
-        _apart(name, _tensor(name, t, shape, _storage(cfg), x.device))
-    _f32("dh_out", dh_out, (shape[0], cfg.width), x.device)
-    _f32("dh_in", dh_in, (shape[0], cfg.width), x.device)
-    _f32("dbias", dbias, (cfg.width,), x.device)
+    shape, dt, dev, args = _recurrence_inputs(cfg, x, z, bias, mask, h_in, 3)
+    state = (shape[0], cfg.width)
     st = load_library().msgla_recurrence_backward(
-        ctypes.byref(c_recurrence_config(cfg)), _rows(x), _rows(z), _ptr(bias), _ptr(mask), _ptr(h_in),
-        None if dy is None else _rows(dy), _ptr(dh_out), shape[0], shape[1], _rows(dx), _rows(dz), _ptr(dbias),
-        _ptr(dh_in), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        c_recurrence_config(cfg), *args, None if dy is None else _rows("dy", dy, shape, dt, dev),
+        _f32("dh_out", dh_out, state, dev), shape[0], shape[1], _rows_out("dx", dx, shape, dt, dev),
+        _rows_out("dz", dz, shape, dt, dev), _f32("dbias", dbias, (cfg.width,), dev), _f32("dh_in", dh_in, state, dev),
+        _ptr(workspace), _bytes(workspace), _raw_stream(stream))
     _check("msgla_recurrence_backward", st)
 
 
 def msgla_recurrence_step(cfg: RecurrenceConfig, x_t, z_t, y_t, h_in, h_out, bias=None, mask=None, stream=None):
     """x_t, z_t, y_t: [B, width]; h_in, h_out: [B, width] fp32 (may be one tensor); mask: [B] uint8."""
-    shape = _recurrence_inputs(cfg, x_t, z_t, bias, mask, h_in, 2)
-    _apart("y_t", _tensor("y_t", y_t, shape, _storage(cfg), x_t.device))
-    _f32("h_out", h_out, shape, x_t.device)
+    shape, dt, dev, args = _recurrence_inputs(cfg, x_t, z_t, bias, mask, h_in, 2)
     st = load_library().msgla_recurrence_step(
-        ctypes.byref(c_recurrence_config(cfg)), _rows(x_t), _rows(z_t), _ptr(bias), _ptr(mask), _ptr(h_in), shape[0],
-        _rows(y_t), _ptr(h_out), _stream(stream))
+        c_recurrence_config(cfg), *args, shape[0], _rows_out("y_t", y_t, shape, dt, dev),
+        _f32("h_out", h_out, shape, dev), _raw_stream(stream))
     _check("msgla_recurrence_step", st)
 
 
-def _heads(name: str, t) -> CHeads:
+def _heads(name: str, t, shape, dtype, device) -> CHeads:
     """[B, L, heads, width], or [B, heads, width] as rows of one position."""
-    strides = [0 if n == 1 else s for n, s in zip(t.shape[:-1], t.stride()[:-1])]
-    if t.data_ptr() % 16 or any(s * t.element_size() % 16 for s in strides):
-        raise ValueError(f"rows of {name} must start at multiples of 16 bytes")
-    return CHeads(t.data_ptr(), strides[0], strides[1] if t.dim() == 4 else 0, strides[-1])
+    st = _tensor(name, t, shape, dtype, device)
+    ptr, unit = t.data_ptr(), 16 // t.element_size()
+    if (ptr % 16) or ((st[0] | st[1] | st[-2]) % unit):
+        st = [0 if n == 1 else s for n, s in zip(shape, st)]
+        if ptr % 16 or (st[0] | st[1] | st[-2]) % unit:
+            raise ValueError(f"rows of {name} must start at multiples of 16 bytes")
+    return CHeads(ptr, st[0], st[1] if len(st) == 4 else 0, st[-2])
+
+
+def _heads_out(name: str, t, shape, dtype, device) -> CHeads:
+    heads = _heads(name, t, shape, dtype, device)
+    _apart(name, t)
+    return heads
 
 
 def _i32(name: str, t, shape, device):
-    import torch
-    return None if t is None else _tensor(name, t, shape, torch.int32, device, contiguous=True)
+    return _dense(name, t, shape, _t().int32, device)
 
 
 _BLOCK_CACHE: dict = {}
@@ -511,67 +547,57 @@ def _dims(name: str, t, n: int):
 
 def msgla_block_means(cfg: BlockAttentionConfig, k, means, lens=None, start_from=None, stream=None):
     """k [B, S, heads_kv, d_k] -> means [B, heads_kv, blocks, d_k] fp32; lens, start_from: [B] int32."""
-    B, S = _dims("k", k, 4).shape[:2]
-    _tensor("k", k, (B, S, cfg.heads_kv, cfg.d_k), _storage(cfg), k.device)
-    _f32("means", means, (B, cfg.heads_kv, block_count(cfg, S), cfg.d_k), k.device)
-    _i32("lens", lens, (B,), k.device)
-    _i32("start_from", start_from, (B,), k.device)
-    st = load_library().msgla_block_means(ctypes.byref(c_block_config(cfg)), _heads("k", k), _ptr(lens),
-                                          _ptr(start_from), B, S, _ptr(means), _stream(stream))
+    B, S, dev = *_dims("k", k, 4).shape[:2], k.device
+    st = load_library().msgla_block_means(
+        c_block_config(cfg), _heads("k", k, (B, S, cfg.heads_kv, cfg.d_k), _storage(cfg), dev),
+        _i32("lens", lens, (B,), dev), _i32("start_from", start_from, (B,), dev), B, S,
+        _f32("means", means, (B, cfg.heads_kv, block_count(cfg, S), cfg.d_k), dev), _raw_stream(stream))
     _check("msgla_block_means", st)
 
 
 def msgla_block_select(cfg: BlockAttentionConfig, q, means, S: int, sel, start=None, lens=None, stream=None):
     """q [B, L, heads_q, d_k] -> sel [B, heads_kv, L, n_select] int32."""
-    B, L = _dims("q", q, 4).shape[:2]
-    _tensor("q", q, (B, L, cfg.heads_q, cfg.d_k), _storage(cfg), q.device)
-    _f32("means", means, (B, cfg.heads_kv, block_count(cfg, S), cfg.d_k), q.device)
-    _i32("sel", sel, (B, cfg.heads_kv, L, cfg.n_select), q.device)
-    _i32("start", start, (B,), q.device)
-    _i32("lens", lens, (B,), q.device)
-    st = load_library().msgla_block_select(ctypes.byref(c_block_config(cfg)), _heads("q", q), _ptr(means), _ptr(start),
-                                           _ptr(lens), B, L, S, _ptr(sel), _stream(stream))
+    B, L, dev = *_dims("q", q, 4).shape[:2], q.device
+    st = load_library().msgla_block_select(
+        c_block_config(cfg), _heads("q", q, (B, L, cfg.heads_q, cfg.d_k), _storage(cfg), dev),
+        _f32("means", means, (B, cfg.heads_kv, block_count(cfg, S), cfg.d_k), dev), _i32("start", start, (B,), dev),
+        _i32("lens", lens, (B,), dev), B, L, S, _i32("sel", sel, (B, cfg.heads_kv, L, cfg.n_select), dev),
+        _raw_stream(stream))
     _check("msgla_block_select", st)
 
 
 def _block_inputs(cfg, q, k, v, sel, start, lens):
+    """(B, L, S, type, device, the C arguments of the six)"""
     B, L = _dims("q", q, 4).shape[:2]
     S, dt, dev = _dims("k", k, 4).shape[1], _storage(cfg), q.device
-    _tensor("q", q, (B, L, cfg.heads_q, cfg.d_k), dt, dev)
-    _tensor("k", k, (B, S, cfg.heads_kv, cfg.d_k), dt, dev)
-    _tensor("v", v, (B, S, cfg.heads_kv, cfg.d_v), dt, dev)
-    _i32("sel", sel, (B, cfg.heads_kv, L, cfg.n_select), dev)
-    _i32("start", start, (B,), dev)
-    _i32("lens", lens, (B,), dev)
-    return B, L, S
+    if sel is None:
+        raise ValueError("sel is missing")
+    return B, L, S, dt, dev, (
+        _heads("q", q, (B, L, cfg.heads_q, cfg.d_k), dt, dev), _heads("k", k, (B, S, cfg.heads_kv, cfg.d_k), dt, dev),
+        _heads("v", v, (B, S, cfg.heads_kv, cfg.d_v), dt, dev), _i32("sel", sel, (B, cfg.heads_kv, L, cfg.n_select), dev),
+        _i32("start", start, (B,), dev), _i32("lens", lens, (B,), dev))
 
 
 def msgla_block_attention(cfg: BlockAttentionConfig, q, k, v, sel, out, lse, workspace, start=None, lens=None,
                           stream=None):
     """q [B, L, heads_q, d_k], k [B, S, heads_kv, d_k], v [B, S, heads_kv, d_v] -> out [B, L, heads_q, d_v] and
     lse [B, heads_q, L] fp32 (or None)."""
-    B, L, S = _block_inputs(cfg, q, k, v, sel, start, lens)
-    _apart("out", _tensor("out", out, (B, L, cfg.heads_q, cfg.d_v), _storage(cfg), q.device))
-    _f32("lse", lse, (B, cfg.heads_q, L), q.device)
+    B, L, S, dt, dev, args = _block_inputs(cfg, q, k, v, sel, start, lens)
     st = load_library().msgla_block_attention(
-        ctypes.byref(c_block_config(cfg)), _heads("q", q), _heads("k", k), _heads("v", v), _ptr(sel), _ptr(start),
-        _ptr(lens), B, L, S, _heads("out", out), _ptr(lse), _ptr(workspace),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _stream(stream))
+        c_block_config(cfg), *args, B, L, S, _heads_out("out", out, (B, L, cfg.heads_q, cfg.d_v), dt, dev),
+        _f32("lse", lse, (B, cfg.heads_q, L), dev), _ptr(workspace), _bytes(workspace), _raw_stream(stream))
     _check("msgla_block_attention", st)
 
 
 def msgla_block_attention_backward(cfg: BlockAttentionConfig, q, k, v, sel, out, lse, dout, dq, dk, dv, workspace,
                                    start=None, lens=None, stream=None):
-    B, L, S = _block_inputs(cfg, q, k, v, sel, start, lens)
-    for name, t in (("out", out), ("dout", dout)):
-        _tensor(name, t, (B, L, cfg.heads_q, cfg.d_v), _storage(cfg), q.device)
-    _f32("lse", lse, (B, cfg.heads_q, L), q.device)
-    for name, t, like in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        _apart(name, _tensor(name, t, like.shape, like.dtype, q.device))
+    B, L, S, dt, dev, args = _block_inputs(cfg, q, k, v, sel, start, lens)
+    shape = (B, L, cfg.heads_q, cfg.d_v)
     st = load_library().msgla_block_attention_backward(
-        ctypes.byref(c_block_config(cfg)), _heads("q", q), _heads("k", k), _heads("v", v), _ptr(sel), _ptr(start),
-        _ptr(lens), _heads("out", out), _ptr(lse), _heads("dout", dout), B, L, S, _heads("dq", dq), _heads("dk", dk),
-        _heads("dv", dv), _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        c_block_config(cfg), *args, _heads("out", out, shape, dt, dev), _f32("lse", lse, (B, cfg.heads_q, L), dev),
+        _heads("dout", dout, shape, dt, dev), B, L, S, _heads_out("dq", dq, tuple(q.shape), dt, dev),
+        _heads_out("dk", dk, tuple(k.shape), dt, dev), _heads_out("dv", dv, tuple(v.shape), dt, dev), _ptr(workspace),
+        _bytes(workspace), _raw_stream(stream))
     _check("msgla_block_attention_backward", st)
 
 
@@ -580,16 +606,11 @@ def msgla_block_attention_step(cfg: BlockAttentionConfig, q_t, k_t, v_t, k, v, m
     """q_t [B, heads_q, d_k], k_t [B, heads_kv, d_k], v_t [B, heads_kv, d_v], caches k [B, S, heads_kv, d_k] and
     v [B, S, heads_kv, d_v], means [B, heads_kv, blocks, d_k] fp32, pos [B] int32 -> out_t [B, heads_q, d_v]."""
     B, S, dt, dev = q_t.shape[0], _dims("k", k, 4).shape[1], _storage(cfg), q_t.device
-    _tensor("q_t", q_t, (B, cfg.heads_q, cfg.d_k), dt, dev)
-    _tensor("k_t", k_t, (B, cfg.heads_kv, cfg.d_k), dt, dev)
-    _tensor("v_t", v_t, (B, cfg.heads_kv, cfg.d_v), dt, dev)
-    _apart("k", _tensor("k", k, (B, S, cfg.heads_kv, cfg.d_k), dt, dev))
-    _apart("v", _tensor("v", v, (B, S, cfg.heads_kv, cfg.d_v), dt, dev))
-    _f32("means", means, (B, cfg.heads_kv, block_count(cfg, S), cfg.d_k), dev)
-    _i32("pos", pos, (B,), dev)
-    _apart("out_t", _tensor("out_t", out_t, (B, cfg.heads_q, cfg.d_v), dt, dev))
+    hq, hkv, dk, dv = cfg.heads_q, cfg.heads_kv, cfg.d_k, cfg.d_v
     st = load_library().msgla_block_attention_step(
-        ctypes.byref(c_block_config(cfg)), _heads("q_t", q_t), _heads("k_t", k_t), _heads("v_t", v_t), _ptr(pos), B, S,
-        _heads("k", k), _heads("v", v), _ptr(means), _heads("out_t", out_t), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        c_block_config(cfg), _heads("q_t", q_t, (B, hq, dk), dt, dev), _heads("k_t", k_t, (B, hkv, dk), dt, dev),
+        _heads("v_t", v_t, (B, hkv, dv), dt, dev), _i32("pos", pos, (B,), dev), B, S,
+        _heads_out("k", k, (B, S, hkv, dk), dt, dev), _heads_out("v", v, (B, S, hkv, dv), dt, dev),
+        _f32("means", means, (B, hkv, block_count(cfg, S), dk), dev), _heads_out("out_t", out_t, (B, hq, dv), dt, dev),
+        _ptr(workspace), _bytes(workspace), _raw_stream(stream))
     _check("msgla_block_attention_step", st)

@@ -3,7 +3,6 @@ weights with torch, packs the weights once, owns the workspace, and calls the
 binding.  No arithmetic of the layer happens here."""
 from __future__ import annotations
 
-import contextlib
 from typing import Optional
 
 import numpy as np
@@ -200,17 +199,21 @@ class DecodeGraph:
         return self.out
 
 
-@contextlib.contextmanager
-def _launching_on(t):
-    """Makes t's device the current one, on which the library launches; yields that device's current stream."""
+def _elsewhere(t):
+    """None if t's device is the current one, on which the library launches; else a context that makes it so."""
     torch = _torch()
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"tensors must be on a ROCm device: got one on {t.device}")
-    if t.device.index == torch.cuda.current_device():
-        yield torch.cuda.current_stream().cuda_stream
-        return
-    with torch.cuda.device(t.device):
-        yield torch.cuda.current_stream().cuda_stream
+    return None if t.device.index == torch.cuda.current_device() else torch.cuda.device(t.device)
+
+
+def _on(t, method, *args):
+    """method(*args) with t's device current; the library takes its current stream."""
+    there = _elsewhere(t)
+    if there is None:
+        return method(*args)
+    with there:
+        return method(*args)
 
 
 def _workspace(n: int, device):
@@ -226,7 +229,7 @@ class DeviceRecurrence:
     def __init__(self, cfg: RecurrenceConfig):
         self.cfg = cfg
 
-    def _sizes(self, x, query):
+    def _room(self, x, query):
         if x.dim() != 3:
             raise ValueError(f"x must be [B, L, width]: it has {x.dim()} dimensions")
         n = query(self.cfg, x.shape[0], x.shape[1])
@@ -236,37 +239,40 @@ class DeviceRecurrence:
 
     def forward(self, x, z, bias=None, mask=None, h_in=None, y=None, h_out=None):
         """x, z [B, L, width] -> (y [B, L, width], state after the last position [B, width] fp32)."""
+        return _on(x, self._forward, x, z, bias, mask, h_in, y, h_out)
+
+    def _forward(self, x, z, bias, mask, h_in, y, h_out):
         torch = _torch()
-        with _launching_on(x) as stream:
-            ws = self._sizes(x, binding.msgla_recurrence_workspace_bytes)
-            y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
-            if h_out is None:
-                h_out = torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)
-            binding.msgla_recurrence_forward(self.cfg, x, z, y, ws, bias, mask, h_in, h_out, stream)
+        ws = self._room(x, binding.msgla_recurrence_workspace_bytes)
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+        if h_out is None:
+            h_out = torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)
+        binding.msgla_recurrence_forward(self.cfg, x, z, y, ws, bias, mask, h_in, h_out)
         return y, h_out
 
     def backward(self, x, z, dy, bias=None, mask=None, h_in=None, dh_out=None, dx=None, dz=None):
         """(dx, dz, dbias, dh_in) from dy [B, L, width] (or None for 0) and dh_out [B, width] (or None):
         dbias is None without a bias, dh_in without h_in."""
+        return _on(x, self._backward, x, z, dy, bias, mask, h_in, dh_out, dx, dz)
+
+    def _backward(self, x, z, dy, bias, mask, h_in, dh_out, dx, dz):
         torch = _torch()
-        with _launching_on(x) as stream:
-            ws = self._sizes(x, binding.msgla_recurrence_backward_workspace_bytes)
-            dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
-            dz = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dz is None else dz
-            dbias = None if bias is None else torch.empty_like(bias)
-            dh_in = None if h_in is None else torch.empty_like(h_in)
-            binding.msgla_recurrence_backward(self.cfg, x, z, dy, dx, dz, ws, bias, mask, h_in, dh_out, dbias, dh_in,
-                                              stream)
+        ws = self._room(x, binding.msgla_recurrence_backward_workspace_bytes)
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
+        dz = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dz is None else dz
+        dbias = None if bias is None else torch.empty_like(bias)
+        dh_in = None if h_in is None else torch.empty_like(h_in)
+        binding.msgla_recurrence_backward(self.cfg, x, z, dy, dx, dz, ws, bias, mask, h_in, dh_out, dbias, dh_in)
         return dx, dz, dbias, dh_in
 
     def step(self, x_t, z_t, h, bias=None, mask=None, y_t=None, h_out=None):
         """One token of every sequence: x_t, z_t [B, width], h [B, width] fp32 -> (y_t, state).
         The state is renewed in place unless h_out is given."""
-        torch = _torch()
-        h_out = h if h_out is None else h_out
-        with _launching_on(x_t) as stream:
-            y_t = torch.empty(x_t.shape, dtype=x_t.dtype, device=x_t.device) if y_t is None else y_t
-            binding.msgla_recurrence_step(self.cfg, x_t, z_t, y_t, h, h_out, bias, mask, stream)
+        return _on(x_t, self._step, x_t, z_t, h, bias, mask, y_t, h if h_out is None else h_out)
+
+    def _step(self, x_t, z_t, h, bias, mask, y_t, h_out):
+        y_t = _torch().empty(x_t.shape, dtype=x_t.dtype, device=x_t.device) if y_t is None else y_t
+        binding.msgla_recurrence_step(self.cfg, x_t, z_t, y_t, h, h_out, bias, mask)
         return y_t, h_out
 
 
@@ -287,60 +293,69 @@ class DeviceBlockAttention:
     def means(self, k, lens=None, start_from=None, means=None):
         """Mean keys of the whole blocks of k [B, S, heads_kv, d_k]: [B, heads_kv, blocks, d_k] fp32.
         start_from [B] int32 (with a means of earlier calls): blocks that end at or before it are kept."""
-        torch = _torch()
         if start_from is not None and means is None:
             raise ValueError("start_from keeps rows of a means that must be given")
-        with _launching_on(k) as stream:
-            if means is None:
-                means = torch.empty((k.shape[0], self.cfg.heads_kv, binding.block_count(self.cfg, k.shape[1]),
-                                     self.cfg.d_k), dtype=torch.float32, device=k.device)
-            binding.msgla_block_means(self.cfg, k, means, lens, start_from, stream)
+        return _on(k, self._means, k, lens, start_from, means)
+
+    def _means(self, k, lens, start_from, means):
+        torch = _torch()
+        if means is None:
+            means = torch.empty((k.shape[0], self.cfg.heads_kv, binding.block_count(self.cfg, k.shape[1]),
+                                 self.cfg.d_k), dtype=torch.float32, device=k.device)
+        binding.msgla_block_means(self.cfg, k, means, lens, start_from)
         return means
 
     def select(self, q, means, start=None, lens=None, sel=None):
         """The blocks of every query of q [B, L, heads_q, d_k]: [B, heads_kv, L, n_select] int32."""
+        return _on(q, self._select, q, means, start, lens, sel)
+
+    def _select(self, q, means, start, lens, sel):
         torch = _torch()
-        with _launching_on(q) as stream:
-            if sel is None:
-                sel = torch.empty((q.shape[0], self.cfg.heads_kv, q.shape[1], self.cfg.n_select), dtype=torch.int32,
-                                  device=q.device)
-            binding.msgla_block_select(self.cfg, q, means, means.shape[2] * self.cfg.block, sel, start, lens, stream)
+        if sel is None:
+            sel = torch.empty((q.shape[0], self.cfg.heads_kv, q.shape[1], self.cfg.n_select), dtype=torch.int32,
+                              device=q.device)
+        binding.msgla_block_select(self.cfg, q, means, means.shape[2] * self.cfg.block, sel, start, lens)
         return sel
 
     def forward(self, q, k, v, sel, start=None, lens=None, out=None, lse=None):
         """(out [B, L, heads_q, d_v], lse [B, heads_q, L] fp32)."""
+        return _on(q, self._forward, q, k, v, sel, start, lens, out, lse)
+
+    def _forward(self, q, k, v, sel, start, lens, out, lse):
         torch = _torch()
-        with _launching_on(q) as stream:
-            B, L = q.shape[:2]
-            ws = self._room(binding.msgla_block_attention_workspace_bytes, q.device, B, L, k.shape[1])
-            if out is None:
-                out = torch.empty((B, L, self.cfg.heads_q, self.cfg.d_v), dtype=q.dtype, device=q.device)
-            if lse is None:
-                lse = torch.empty((B, self.cfg.heads_q, L), dtype=torch.float32, device=q.device)
-            binding.msgla_block_attention(self.cfg, q, k, v, sel, out, lse, ws, start, lens, stream)
+        B, L = q.shape[:2]
+        ws = self._room(binding.msgla_block_attention_workspace_bytes, q.device, B, L, k.shape[1])
+        if out is None:
+            out = torch.empty((B, L, self.cfg.heads_q, self.cfg.d_v), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, self.cfg.heads_q, L), dtype=torch.float32, device=q.device)
+        binding.msgla_block_attention(self.cfg, q, k, v, sel, out, lse, ws, start, lens)
         return out, lse
 
     def backward(self, q, k, v, sel, out, lse, dout, start=None, lens=None, dq=None, dk=None, dv=None):
         """(dq, dk, dv) for the forward's inputs, out and lse."""
+        return _on(q, self._backward, q, k, v, sel, out, lse, dout, start, lens, dq, dk, dv)
+
+    def _backward(self, q, k, v, sel, out, lse, dout, start, lens, dq, dk, dv):
         torch = _torch()
-        with _launching_on(q) as stream:
-            ws = self._room(binding.msgla_block_attention_backward_workspace_bytes, q.device, q.shape[0], q.shape[1],
-                            k.shape[1])
-            dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if d is None else d
-                          for t, d in ((q, dq), (k, dk), (v, dv)))
-            binding.msgla_block_attention_backward(self.cfg, q, k, v, sel, out, lse, dout, dq, dk, dv, ws, start, lens,
-                                                   stream)
+        ws = self._room(binding.msgla_block_attention_backward_workspace_bytes, q.device, q.shape[0], q.shape[1],
+                        k.shape[1])
+        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if d is None else d
+                      for t, d in ((q, dq), (k, dk), (v, dv)))
+        binding.msgla_block_attention_backward(self.cfg, q, k, v, sel, out, lse, dout, dq, dk, dv, ws, start, lens)
         return dq, dk, dv
 
     def step(self, q_t, k_t, v_t, k, v, means, pos, out_t=None):
         """One token of every sequence: puts k_t, v_t at pos [B] int32 of the caches, renews the means, selects
         and attends: out_t [B, heads_q, d_v].  The caller advances pos."""
+        return _on(q_t, self._step, q_t, k_t, v_t, k, v, means, pos, out_t)
+
+    def _step(self, q_t, k_t, v_t, k, v, means, pos, out_t):
         torch = _torch()
-        with _launching_on(q_t) as stream:
-            ws = self._room(binding.msgla_block_attention_step_workspace_bytes, q_t.device, q_t.shape[0], k.shape[1])
-            if out_t is None:
-                out_t = torch.empty((q_t.shape[0], self.cfg.heads_q, self.cfg.d_v), dtype=q_t.dtype, device=q_t.device)
-            binding.msgla_block_attention_step(self.cfg, q_t, k_t, v_t, k, v, means, pos, out_t, ws, stream)
+        ws = self._room(binding.msgla_block_attention_step_workspace_bytes, q_t.device, q_t.shape[0], k.shape[1])
+        if out_t is None:
+            out_t = torch.empty((q_t.shape[0], self.cfg.heads_q, self.cfg.d_v), dtype=q_t.dtype, device=q_t.device)
+        binding.msgla_block_attention_step(self.cfg, q_t, k_t, v_t, k, v, means, pos, out_t, ws)
         return out_t
 
 
