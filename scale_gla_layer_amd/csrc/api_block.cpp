@@ -68,7 +68,13 @@ BlkParams blk_params(const msgla_block_config* c, int64_t B, int64_t L, int64_t 
 
 int es_of(const msgla_block_config* c) { return c->dtype == MSGLA_BF16 ? 2 : 4; }
 
-bool use_tiles(const BlkParams& P) { return P.tiles >= 1024 && P.nb <= BLK_TILES_MAX; }
+// Enough tiles for workgroups of 15 to fill the chip; below, a tile is a wave's,
+// and its blocks are dealt, 32 keys at a time, to as many waves (parts) as give
+// about 4096, sixteen on a CU.
+bool use_tiles(const BlkParams& P) { return P.tiles >= 4096 && P.nb <= BLK_TILES_MAX; }
+int parts_of(const BlkParams& P) {
+  return P.tiles >= 4096 ? 1 : std::min<int>(P.n << (P.lgT - 5), (int)(4096 / P.tiles));
+}
 
 struct Take {
   size_t cur = 0;
@@ -79,15 +85,13 @@ struct Take {
   }
 };
 
-// Forward: few tiles leave most of the chip idle, so each one's blocks are dealt,
-// 32 keys at a time, to as many waves as give about 2048, eight on a CU.
 struct FwdWs {
   size_t po, pm, total;
   int parts;
 };
 FwdWs fwd_ws(const BlkParams& P, Take take = Take()) {
   FwdWs w{};
-  w.parts = P.tiles >= 1024 ? 1 : std::min<int>(P.n << (P.lgT - 5), (int)(2048 / P.tiles));
+  w.parts = parts_of(P);
   if (w.parts > 1) {
     w.po = take((size_t)P.tiles * w.parts * BLK_ROWS * blk_dvp(P.dvw) * 4);
     w.pm = take((size_t)P.tiles * w.parts * BLK_ROWS * 8);
@@ -104,8 +108,8 @@ void set_fwd(BlkParams& P, const FwdWs& w, void* ws) {
 }
 
 struct BwdWs {
-  size_t delta, bits, cnt, off, slot, list, items, n_items, part, total;
-  int seg, W, max_items, max_parts;
+  size_t delta, bits, cnt, off, slot, list, items, n_items, part, po, pm, total;
+  int parts, seg, W, max_items, max_parts;
 };
 BwdWs bwd_ws(const BlkParams& P) {
   BwdWs w{};
@@ -127,6 +131,11 @@ BwdWs bwd_ws(const BlkParams& P) {
   w.items = take(bh * w.max_items * 8);
   w.n_items = take(bh * 4);
   w.part = take(((bh * w.max_parts) << P.lgT) * (size_t)(blk_dkp(P.dkw) + blk_dvp(P.dvw)) * 4);
+  w.parts = parts_of(P);
+  if (w.parts > 1) {  // partial gradients of the queries
+    w.po = take((size_t)P.tiles * w.parts * BLK_ROWS * 2 * blk_dkp(P.dkw) * 4);
+    w.pm = take((size_t)P.tiles * w.parts * BLK_ROWS * 4);
+  }
   w.total = take.cur;
   return w;
 }
@@ -245,7 +254,7 @@ msgla_status msgla_block_attention_backward(const msgla_block_config* cfg, const
   BlkParams P = blk_params(cfg, B, L, S);
   const BwdWs w = bwd_ws(P);
   if (workspace_bytes < w.total) return MSGLA_ERR_WORKSPACE;
-  if (!fwd_grid_ok(P, 1) || !bwd_grid_ok(P, w)) return MSGLA_ERR_UNSUPPORTED;
+  if (!fwd_grid_ok(P, w.parts) || !bwd_grid_ok(P, w)) return MSGLA_ERR_UNSUPPORTED;
   P.q = heads_of(q, es);
   P.k = heads_of(k, es);
   P.v = heads_of(v, es);
@@ -258,7 +267,11 @@ msgla_status msgla_block_attention_backward(const msgla_block_config* cfg, const
   P.start = start;
   P.lens = lens;
   P.lse_in = lse;
-  P.parts = 1;
+  P.parts = w.parts;
+  if (w.parts > 1) {
+    P.po = at<float>(workspace, w.po);
+    P.pm = at<float>(workspace, w.pm);
+  }
   P.delta = at<float>(workspace, w.delta);
   P.bits = at<uint64_t>(workspace, w.bits);
   P.cnt = at<int32_t>(workspace, w.cnt);

@@ -35,8 +35,8 @@ struct BlkParams {
   int QT, GT, tiles_per_seq;
   int64_t tiles;
   int parts;     // workgroups a tile's blocks are dealt to
-  float* po;     // [tile][part][16][DVP] partial outputs
-  float* pm;     // [tile][part][16][2] their maxima (in units of log 2) and sums
+  float* po;     // [tile][part][16][DVP] partial outputs; backward [..][2][DKP] partial sums for dq
+  float* pm;     // [tile][part][16][2] their maxima (in units of log 2) and sums; backward [..] delta's errors
   // queries of each block
   int seg, W, max_items, max_parts;  // queries of a work item, 64-query words, bounds per (sequence, head)
   uint64_t* bits;   // [B Hkv][W][nb]

@@ -226,12 +226,19 @@ template <typename T> __global__ __launch_bounds__(256) void k_block_delta(const
   if (c == 0) P.delta[i] = s;
 }
 
-// dq = scale sum_j p_j (do . v_j - delta) k_j, the tiles and steps of the forward.
+// dq = scale sum_j p_j (do . v_j - delta) k_j, by the tiles, steps and parts of
+// the forward.  For bf16 the weights' gradients go through the product as a sum
+// of two bf16 values, and delta, which comes from the rounded output, is put
+// right: with e = sum_j p_j (do . v_j - delta), its error (the weights sum to 1),
+// dq loses scale e sum_j p_j k_j, and delta + e is what dk and dv then use.
 template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_block_dq(const BlkParams P) {
+  constexpr bool EXACT = sizeof(T) == 2;
   __shared__ int lists[BLK_ROWS * BLK_LIST], raw[BLK_ROWS * BLK_MAX_SEL];
   __shared__ __attribute__((aligned(16))) char ks[BLK_KEYS * blk_pitch<T, DKP>()];
   const int lane = threadIdx.x, r = lane & 15, a = lane >> 4;
-  const BlkTile t(P, blockIdx.x);
+  const int64_t tile = (int64_t)blockIdx.x / P.parts;
+  const int part = (int)((int64_t)blockIdx.x - tile * P.parts);
+  const BlkTile t(P, tile);
   const BlkRow row = t.row(P, r);
   blk_lists(P, t, lists, raw, lane);
   Qfrag<T, DKP> q;
@@ -242,15 +249,18 @@ template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_
   g.load(at(P.dout, row.b, live ? row.i : 0, live ? row.head : 0), vw, lane, live);
   __syncthreads();
   const int* mine = lists + (row.i - t.i0) * BLK_LIST;
-  int cur = live ? *mine : BLK_END;
+  int cur = live ? *mine : BLK_END, seen = 0;
   int last = row.p;
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) last = max(last, __shfl_xor(last, o));
   const int64_t lr = ((int64_t)row.b * P.Hq + row.head) * P.L + row.i;
   const float lse = live ? P.lse_in[lr] * BLK_LOG2E : 0.f, delta = live ? P.delta[lr] : 0.f;
-  f32x4 acc[DKP / 16];
+  f32x4 acc[DKP / 16], mean[EXACT ? DKP / 16 : 1];  // mean: sum_j p_j k_j
 #pragma unroll
   for (int d = 0; d < DKP / 16; ++d) acc[d] = zero4();
+#pragma unroll
+  for (int d = 0; d < (EXACT ? DKP / 16 : 1); ++d) mean[d] = zero4();
+  float off = 0.f;
   const float sc = P.scale * BLK_LOG2E;
   for (;;) {
     const int j = blk_row_min(cur);
@@ -259,44 +269,102 @@ template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_
     if (member) cur = *++mine;
     const int first = j << P.lgT;
     for (int k0 = first; k0 < first + (1 << P.lgT) && k0 <= last; k0 += BLK_KEYS) {
+      if (P.parts > 1 && seen++ % P.parts != part) continue;
       __syncthreads();
       blk_stage<T, DKP, 64>(ks, BLK_KEYS, kw, lane, [&](int i) {
         return k0 + i <= last ? at(P.k, t.b, k0 + i, t.h) : nullptr;
       });
       __syncthreads();
-      float ds[2][4];
+      float w[2][4], ds[2][4];
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt) {
         const char* kr = ks + (16 * kt + r) * blk_pitch<T, DKP>();
         const char* vr = at(P.v, t.b, min(k0 + 16 * kt + r, P.S - 1), t.h);
         f32x4 s = zero4(), dp = zero4();
 #pragma unroll
-        for (int w = 0; w < Qfrag<T, DKP>::N; ++w) s = mma_slab<T>(ld16(kr + 64 * w + 16 * a), q.f[w], s);
+        for (int c = 0; c < Qfrag<T, DKP>::N; ++c) s = mma_slab<T>(ld16(kr + 64 * c + 16 * a), q.f[c], s);
 #pragma unroll
-        for (int w = 0; w < Qfrag<T, DVP>::N; ++w) dp = mma_slab<T>(blk_ld(vr, 64 * w + 16 * a, vw), g.f[w], dp);
+        for (int c = 0; c < Qfrag<T, DVP>::N; ++c) dp = mma_slab<T>(blk_ld(vr, 64 * c + 16 * a, vw), g.f[c], dp);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float p = __builtin_amdgcn_exp2f(s[i] * sc - lse);
-          ds[kt][i] = member && k0 + 16 * kt + 4 * a + i <= row.p ? p * (dp[i] - delta) * P.scale : 0.f;
+          const bool on = member && k0 + 16 * kt + 4 * a + i <= row.p;
+          w[kt][i] = on ? __builtin_amdgcn_exp2f(s[i] * sc - lse) : 0.f;
+          ds[kt][i] = on ? w[kt][i] * (dp[i] - delta) : 0.f;
+          off += ds[kt][i];
         }
       }
 #pragma unroll
       for (int s = 0; s < BLK_KEYS / blk_slab<T>(); ++s) {
-        const u32x4 w = blk_pack<T>(ds, s);
+        u32x4 x, lo = zero16(), y = zero16();
+        if constexpr (EXACT) {
+          const float v[8] = {ds[0][0], ds[0][1], ds[0][2], ds[0][3], ds[1][0], ds[1][1], ds[1][2], ds[1][3]};
+          split_bf16(v, x, lo);
+          y = blk_pack<T>(w, s);
+        } else {
+          x = blk_pack<T>(ds, s);
+        }
 #pragma unroll
-        for (int d = 0; d < DKP / 16; ++d)
-          acc[d] = mma_slab<T>(blk_column<T>(ks, blk_pitch<T, DKP>(), s * blk_slab<T>(), d, lane), w, acc[d]);
+        for (int d = 0; d < DKP / 16; ++d) {
+          const u32x4 f = blk_column<T>(ks, blk_pitch<T, DKP>(), s * blk_slab<T>(), d, lane);
+          acc[d] = mma_slab<T>(f, x, acc[d]);
+          if constexpr (EXACT) {
+            acc[d] = mma_slab<T>(f, lo, acc[d]);
+            mean[d] = mma_slab<T>(f, y, mean[d]);
+          }
+        }
       }
     }
   }
   if (!row.in) return;
+  off = EXACT ? blk_quad_sum(off) : 0.f;
+  if (P.parts > 1) {
+    const int64_t pr = (tile * P.parts + part) * BLK_ROWS + r;
+    if (a == 0) P.pm[pr] = off;
+#pragma unroll
+    for (int d = 0; d < DKP / 16; ++d) {
+      st16(P.po + pr * 2 * DKP + 16 * d + 4 * a, __builtin_bit_cast(u32x4, acc[d]));
+      if constexpr (EXACT) st16(P.po + (pr * 2 + 1) * DKP + 16 * d + 4 * a, __builtin_bit_cast(u32x4, mean[d]));
+    }
+    return;
+  }
+  if (EXACT && live && a == 0) P.delta[lr] = delta + off;
   char* o = out_at(P.dq, row.b, row.i, row.head);
 #pragma unroll
   for (int d = 0; d < DKP / 16; ++d) {
     const int c = 16 * d + 4 * a;
-    const float v[4] = {acc[d][0], acc[d][1], acc[d][2], acc[d][3]};
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = (acc[d][e] - (EXACT ? off * mean[EXACT ? d : 0][e] : 0.f)) * P.scale;
     if (c < P.dkw) blk_st4<T>(o + c * sizeof(T), v);
   }
+}
+
+// Joins a row's partial gradients.
+template <typename T, int DKP> __global__ __launch_bounds__(64) void k_block_dq_join(const BlkParams P) {
+  constexpr bool EXACT = sizeof(T) == 2;
+  const int64_t tile = blockIdx.x / BLK_ROWS;
+  const int r = (int)(blockIdx.x % BLK_ROWS), lane = threadIdx.x;
+  const BlkRow row = BlkTile(P, tile).row(P, r);
+  if (!row.in) return;
+  const int64_t pr = tile * P.parts * BLK_ROWS + r;
+  float off = 0.f, g[DKP / 64], m[DKP / 64];
+#pragma unroll
+  for (int d = 0; d < DKP / 64; ++d) g[d] = m[d] = 0.f;
+#pragma unroll 4
+  for (int k = 0; k < P.parts; ++k) {
+    const int64_t at = pr + k * BLK_ROWS;
+    off += P.pm[at];
+#pragma unroll
+    for (int d = 0; d < DKP / 64; ++d) {
+      g[d] += P.po[at * 2 * DKP + 64 * d + lane];
+      if (EXACT) m[d] += P.po[(at * 2 + 1) * DKP + 64 * d + lane];
+    }
+  }
+  if (EXACT && row.p >= 0 && lane == 0) P.delta[((int64_t)row.b * P.Hq + row.head) * P.L + row.i] += off;
+  T* out = reinterpret_cast<T*>(out_at(P.dq, row.b, row.i, row.head));
+#pragma unroll
+  for (int d = 0; d < DKP / 64; ++d)
+    if (64 * d + lane < P.dkw) out[64 * d + lane] = from_f32<T>((g[d] - off * m[d]) * P.scale);
 }
 
 template <typename T, int DKP, int DVP> struct Run {
@@ -308,7 +376,9 @@ template <typename T, int DKP, int DVP> struct Run {
       hipLaunchKernelGGL((k_block_join<T, DVP>), dim3((unsigned)(P.tiles * BLK_ROWS)), dim3(64), 0, st, P);
   }
   static void dq(const BlkParams& P, hipStream_t st) {
-    hipLaunchKernelGGL((k_block_dq<T, DKP, DVP>), dim3((unsigned)P.tiles), dim3(64), 0, st, P);
+    hipLaunchKernelGGL((k_block_dq<T, DKP, DVP>), dim3((unsigned)(P.tiles * P.parts)), dim3(64), 0, st, P);
+    if (P.parts > 1)
+      hipLaunchKernelGGL((k_block_dq_join<T, DKP>), dim3((unsigned)(P.tiles * BLK_ROWS)), dim3(64), 0, st, P);
   }
 };
 

@@ -368,16 +368,11 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
 // of 128, against 233 with 32 keys and 279 with 7 tiles of 64); elsewhere they
 // spill (d_v 256, one sequence of 16384, 8 / 2 heads: 508 us with 32 keys, 1899
 // with 64, 578 with 7 tiles of 64; gradient at B = 2, L = 4096: 246, 284, 289).
-// 15 tiles a workgroup need two workgroups for every CU; below, 3 do better
-// (fp32 gradient of 1200 tiles: 181 us with 15).
+// fp32 with wide heads takes 3 tiles for their registers.
 template <typename T, int DKP, int DVP, bool GRAD> hipError_t by_block(const BlkParams& P, hipStream_t st) {
-  const bool many = P.tiles >= 15 * 512;
   if constexpr (sizeof(T) == 4) {
-    if (many && DVP < 256 && !(GRAD && DKP == 128))
-      return launch_t<T, DKP, DVP, 16, DVP < 256 && !(GRAD && DKP == 128) ? 15 : 3, GRAD>(P, st);
-    return launch_t<T, DKP, DVP, 16, 3, GRAD>(P, st);
+    return launch_t<T, DKP, DVP, 16, DVP == 256 || (GRAD && DKP == 128) ? 3 : 15, GRAD>(P, st);
   } else {
-    if (!many) return launch_t<T, DKP, DVP, 32, 3, GRAD>(P, st);
     constexpr int KT = !GRAD && DVP <= 128 ? 64 : 32;
     return P.lgT == 5 ? launch_t<T, DKP, DVP, 32, 15, GRAD>(P, st) : launch_t<T, DKP, DVP, KT, 15, GRAD>(P, st);
   }

@@ -97,12 +97,51 @@ def test_training(hq, hkv, dk, dv, block, n, L, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,dk,dv,block,n,B,L,lens", [
+    (8, 8, 64, 64, 32, 4, 26, 330, True), (16, 4, 128, 128, 64, 4, 16, 270, False), (24, 8, 80, 96, 32, 6, 16, 171, True),
+    (64, 4, 128, 256, 64, 4, 7, 150, False), (40, 2, 64, 128, 128, 3, 4, 277, True), (32, 8, 128, 64, 128, 2, 10, 210, True),
+    (16, 1, 32, 256, 64, 20, 3, 1400, False)])
+def test_enough_queries_to_share_keys(hq, hkv, dk, dv, block, n, B, L, lens, dtype):
+    """At least 4096 tiles: workgroups of 15 (or 3) tiles share keys and values."""
+    cfg = _cfg(hq, hkv, dk, dv, block, n, min(1, n - 2), 2, dtype)
+    rng = np.random.default_rng(L)
+    if lens:
+        start = rng.integers(0, 60, B)
+        _case(cfg, B, L, S=L + 77, start=start, lens=np.minimum(start + rng.integers(0, 2 * L, B), L + 60), seed=L)
+    else:
+        _case(cfg, B, L, seed=L)
+
+
+def test_enough_queries_with_any_selection():
+    cfg = _cfg(16, 16, 64, 64, 32, 8)
+    rng = np.random.default_rng(14)
+    B, L = 16, 260
+    sel = rng.integers(-2, 10, (B, 16, L, 8))
+    sel[rng.random(sel.shape) < 0.1] = 2 ** 31 - 1
+    sel[rng.random(sel.shape) < 0.1] = -2 ** 31
+    sel[0, 0, :100] = -1
+    sel[0, 1, :100] = sel[0, 1, :100, :1]
+    _case(cfg, B, L, sel=sel.astype(np.int32), seed=9)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_any_selection_of_single_queries(dtype):
+    cfg = _cfg(12, 3, 64, 80, 32, 8, dtype=dtype)
+    rng = np.random.default_rng(15)
+    B, S = 5, 300
+    sel = rng.integers(-2, 12, (B, 3, 1, 8))
+    sel[0, 0], sel[1, 1, 0, 3:] = -1, sel[1, 1, 0, 2]
+    sel[2, 2, 0, 1], sel[3, 0, 0, 0] = 2 ** 31 - 1, -2 ** 31
+    _case(cfg, B, 1, S=S, start=[299, 150, 64, 0, -1], lens=[300, 151, 300, 1, 300], sel=sel.astype(np.int32), seed=16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("hq,hkv,dk,dv,block,n,B,L", [
     (4, 4, 64, 64, 32, 4, 8, 520), (8, 4, 128, 128, 64, 4, 8, 300), (12, 4, 80, 96, 32, 6, 8, 171),
     (64, 4, 128, 256, 64, 4, 2, 150), (40, 2, 64, 128, 128, 3, 1, 277), (16, 4, 128, 64, 128, 2, 4, 290),
     (8, 2, 32, 256, 64, 20, 1, 2100)])
 def test_many_queries(hq, hkv, dk, dv, block, n, B, L, dtype):
-    """Enough tiles for a workgroup's waves to share keys and values; padding and chunks among them."""
+    """More than a thousand tiles, a wave each; padding and chunks among them."""
     cfg = _cfg(hq, hkv, dk, dv, block, n, min(1, n - 2), 2, dtype)
     _case(cfg, B, L, seed=L)
     rng = np.random.default_rng(L)
@@ -290,10 +329,10 @@ def test_means_of_a_growing_cache():
     assert torch.equal(means, want)
 
 
-@pytest.mark.parametrize("L", [3, 300])
-def test_captured_calls_share_nothing(L):
+@pytest.mark.parametrize("L,dv", [(3, 64), (300, 64), (2100, 256)])
+def test_captured_calls_share_nothing(L, dv):
     torch = _torch()
-    cfg = _cfg(8, 2, 64, 64, 64, 4)
+    cfg = _cfg(8, 2, 64, dv, 64, 4) if L < 2000 else _cfg(64, 2, 128, dv, 64, 4)
     op = _op(cfg)
     sets = []
     for seed in (20, 21):
