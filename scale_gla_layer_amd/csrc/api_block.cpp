@@ -68,12 +68,16 @@ BlkParams blk_params(const msgla_block_config* c, int64_t B, int64_t L, int64_t 
 
 int es_of(const msgla_block_config* c) { return c->dtype == MSGLA_BF16 ? 2 : 4; }
 
-// Enough tiles for workgroups of 15 to fill the chip; below, a tile is a wave's,
-// and its blocks are dealt, 32 keys at a time, to as many waves (parts) as give
-// about 4096, sixteen on a CU.
-bool use_tiles(const BlkParams& P) { return P.tiles >= 4096 && P.nb <= BLK_TILES_MAX; }
+// Tiles that share keys and values, in workgroups; or, for a few queries over long
+// sequences, a tile a wave with its blocks dealt, 32 keys at a time, to as many
+// waves (parts) as give about 4096, sixteen on a CU.  Forward of 16 / 4 heads of
+// 128, shared against dealt: 256 tiles 9.0 and 33.6 us, 64 (of 16 blocks at 8192
+// positions) 117 and 67; 8 / 2 heads of 128 and 128 in fp32: 256 tiles 30 and 57,
+// 32 (16 / 4 heads) 489 and 85.
+// Single queries have nothing to share.
+bool use_tiles(const BlkParams& P) { return P.L > 1 && P.tiles >= 128 && P.nb <= BLK_TILES_MAX; }
 int parts_of(const BlkParams& P) {
-  return P.tiles >= 4096 ? 1 : std::min<int>(P.n << (P.lgT - 5), (int)(4096 / P.tiles));
+  return use_tiles(P) || P.tiles >= 4096 ? 1 : std::min<int>(P.n << (P.lgT - 5), (int)(4096 / P.tiles));
 }
 
 struct Take {
@@ -286,7 +290,6 @@ msgla_status msgla_block_attention_backward(const msgla_block_config* cfg, const
   P.max_items = w.max_items;
   P.max_parts = w.max_parts;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  HIP_TRY(launch_block_delta(P, es == 2, st));
   if (use_tiles(P)) HIP_TRY(launch_block_tiles(P, true, es == 2, st));
   else HIP_TRY(launch_block_dq(P, es == 2, st));
   HIP_TRY(launch_block_dkdv(P, es == 2, st));

@@ -57,7 +57,6 @@ hipError_t launch_block_forward(const BlkParams& P, bool bf16_path, hipStream_t 
 // many queries: keys and values shared by a workgroup; nb at most BLK_TILES_MAX
 constexpr int BLK_TILES_MAX = 16384;
 hipError_t launch_block_tiles(const BlkParams& P, bool gradient, bool bf16_path, hipStream_t st);
-hipError_t launch_block_delta(const BlkParams& P, bool bf16_path, hipStream_t st);
 hipError_t launch_block_dq(const BlkParams& P, bool bf16_path, hipStream_t st);
 hipError_t launch_block_dkdv(const BlkParams& P, bool bf16_path, hipStream_t st);
 

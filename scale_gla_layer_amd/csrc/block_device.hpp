@@ -157,4 +157,21 @@ template <typename T> __device__ __forceinline__ void blk_st4(char* p, const flo
   else st16(p, pack16<float>(v));
 }
 
+// The backward counts each block's queries; its first kernel clears the counts.
+__device__ __forceinline__ void blk_clear_counts(const BlkParams& P, int tid, int threads) {
+  const int64_t n = (int64_t)P.B * P.Hkv * P.nb;
+  for (int64_t i = (int64_t)blockIdx.x * threads + tid; i < n; i += (int64_t)gridDim.x * threads) P.cnt[i] = 0;
+}
+
+// sum of the products of 16 bytes of elements
+template <typename T> __device__ __forceinline__ float blk_dot(u32x4 x, u32x4 y) {
+  constexpr int N = 16 / sizeof(T);
+  float u[N], v[N], s = 0.f;
+  unpack16<T>(x, u);
+  unpack16<T>(y, v);
+#pragma unroll
+  for (int i = 0; i < N; ++i) s = __builtin_fmaf(u[i], v[i], s);
+  return s;
+}
+
 }  // namespace msgla

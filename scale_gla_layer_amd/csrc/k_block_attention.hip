@@ -204,30 +204,8 @@ template <typename T, int DVP> __global__ __launch_bounds__(64) void k_block_joi
     P.lse[((int64_t)row.b * P.Hq + row.head) * P.L + row.i] = l == 0.f ? -__builtin_inff() : m * BLK_LN2 + logf(l);
 }
 
-// delta = sum_c dout_c out_c of every row: what the softmax's gradient subtracts.
-// 16 lanes take a row.
-template <typename T> __global__ __launch_bounds__(256) void k_block_delta(const BlkParams P) {
-  const int64_t n = (int64_t)P.B * P.Hq * P.L, i = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int c = threadIdx.x & 15;
-  if (i >= n) return;
-  const int64_t bh = i / P.L, t = i - bh * P.L, b = bh / P.Hq, h = bh - b * P.Hq;
-  const char *x = at(P.o, b, t, h), *y = at(P.dout, b, t, h);
-  float s = 0.f;
-  if (blk_position(P, (int)b, (int)t) >= 0)
-    for (int k = 16 * c; k < P.dvw * (int)sizeof(T); k += 256) {
-      float u[per16<T>()], v[per16<T>()];
-      unpack16<T>(ld16(x + k), u);
-      unpack16<T>(ld16(y + k), v);
-#pragma unroll
-      for (int e = 0; e < per16<T>(); ++e) s += u[e] * v[e];
-    }
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) s += __shfl_xor(s, o);
-  if (c == 0) P.delta[i] = s;
-}
-
 // dq = scale sum_j p_j (do . v_j - delta) k_j, by the tiles, steps and parts of
-// the forward.  For bf16 the weights' gradients go through the product as a sum
+// the forward; delta = do . o is the softmax's share.  For bf16 the weights' gradients go through the product as a sum
 // of two bf16 values, and delta, which comes from the rounded output, is put
 // right: with e = sum_j p_j (do . v_j - delta), its error (the weights sum to 1),
 // dq loses scale e sum_j p_j k_j, and delta + e is what dk and dv then use.
@@ -254,7 +232,17 @@ template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_
 #pragma unroll
   for (int o = 1; o < 16; o <<= 1) last = max(last, __shfl_xor(last, o));
   const int64_t lr = ((int64_t)row.b * P.Hq + row.head) * P.L + row.i;
-  const float lse = live ? P.lse_in[lr] * BLK_LOG2E : 0.f, delta = live ? P.delta[lr] : 0.f;
+  const float lse = live ? P.lse_in[lr] * BLK_LOG2E : 0.f;
+  float delta = 0.f;
+  {
+    Qfrag<T, DVP> o;
+    o.load(at(P.o, row.b, live ? row.i : 0, live ? row.head : 0), vw, lane, live);
+#pragma unroll
+    for (int c = 0; c < Qfrag<T, DVP>::N; ++c) delta += blk_dot<T>(g.f[c], o.f[c]);
+    delta = blk_quad_sum(delta);
+  }
+  if (live && a == 0 && part == 0) P.delta[lr] = delta;
+  blk_clear_counts(P, lane, 64);
   f32x4 acc[DKP / 16], mean[EXACT ? DKP / 16 : 1];  // mean: sum_j p_j k_j
 #pragma unroll
   for (int d = 0; d < DKP / 16; ++d) acc[d] = zero4();
@@ -397,13 +385,6 @@ template <class F> void dispatch(const BlkParams& P, bool bf16_path, F f) {
 
 hipError_t launch_block_forward(const BlkParams& P, bool bf16_path, hipStream_t st) {
   dispatch(P, bf16_path, [&](auto r) { r.forward(P, st); });
-  return hipGetLastError();
-}
-
-hipError_t launch_block_delta(const BlkParams& P, bool bf16_path, hipStream_t st) {
-  const dim3 grid((unsigned)(((int64_t)P.B * P.Hq * P.L + 15) / 16));
-  if (bf16_path) hipLaunchKernelGGL(k_block_delta<bf16>, grid, dim3(256), 0, st, P);
-  else hipLaunchKernelGGL(k_block_delta<float>, grid, dim3(256), 0, st, P);
   return hipGetLastError();
 }
 

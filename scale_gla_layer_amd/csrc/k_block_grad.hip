@@ -20,7 +20,7 @@ namespace {
 
 constexpr int INV_PIECE = 2048;  // blocks of one workgroup's bit words
 
-// bit i of word (w, j): query 64 w + i chose block j
+// Bit i of word (w, j): query 64 w + i chose block j; and the number of queries of every block.
 __global__ __launch_bounds__(256) void k_block_bits(const BlkParams P) {
   __shared__ unsigned long long word[INV_PIECE];
   const int tid = threadIdx.x, w = blockIdx.x % P.W, j0 = blockIdx.y * INV_PIECE;
@@ -37,64 +37,41 @@ __global__ __launch_bounds__(256) void k_block_bits(const BlkParams P) {
   }
   __syncthreads();
   uint64_t* out = P.bits + (bh * P.W + w) * P.nb + j0;
-  for (int j = tid; j < n; j += 256) out[j] = word[j];
-}
-
-__global__ __launch_bounds__(64) void k_block_count(const BlkParams P) {
-  const int64_t bh = blockIdx.y;
-  const int j = blockIdx.x * 64 + threadIdx.x;
-  if (j >= P.nb) return;
-  const uint64_t* bits = P.bits + bh * P.W * P.nb + j;
-  int c = 0, w = 0;
-  for (; w + 8 <= P.W; w += 8) {
-    uint64_t m[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) m[k] = bits[(int64_t)(w + k) * P.nb];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) c += __popcll(m[k]);
+  for (int j = tid; j < n; j += 256) {
+    out[j] = word[j];
+    if (word[j]) atomicAdd(P.cnt + bh * P.nb + j0 + j, __popcll(word[j]));  // whole numbers: in any order
   }
-  for (; w < P.W; ++w) c += __popcll(bits[(int64_t)w * P.nb]);
-  P.cnt[bh * P.nb + j] = c;
 }
 
-// Running sums over the blocks: where each one's list, work items and partials begin.
-__global__ __launch_bounds__(1024) void k_block_plan(const BlkParams P) {
-  __shared__ int sum[3][1024];
-  const int64_t bh = blockIdx.x;
-  const int tid = threadIdx.x;
-  int before[3] = {0, 0, 0};
-  for (int j0 = 0; j0 < P.nb; j0 += 1024) {
-    const int j = j0 + tid, c = j < P.nb ? P.cnt[bh * P.nb + j] : 0;
-    const int ni = j < P.nb ? max(1, (c + P.seg - 1) / P.seg) : 0;
-    const int v[3] = {c, ni, ni > 1 ? ni : 0};
-    for (int k = 0; k < 3; ++k) sum[k][tid] = v[k];
-    __syncthreads();
-    for (int o = 1; o < 1024; o <<= 1) {
-      int add[3] = {0, 0, 0};
-      if (tid >= o)
-        for (int k = 0; k < 3; ++k) add[k] = sum[k][tid - o];
-      __syncthreads();
-      for (int k = 0; k < 3; ++k) sum[k][tid] += add[k];
-      __syncthreads();
-    }
-    if (j < P.nb) {
-      P.off[bh * P.nb + j] = before[0] + sum[0][tid] - c;
-      P.slot[bh * P.nb + j] = ni > 1 ? before[2] + sum[2][tid] - ni : -1;
-      for (int s = 0; s < ni; ++s)
-        P.items[bh * P.max_items + before[1] + sum[1][tid] - ni + s] = make_int2(j, s * P.seg);
-    }
-    for (int k = 0; k < 3; ++k) before[k] += sum[k][1023];
-    __syncthreads();
-  }
-  if (tid == 0) P.n_items[bh] = before[1];
-}
-
-// A wave writes one block's queries in order.
+// A wave writes one block's queries in order, and where its list, its work items
+// and its partials begin: sums over the blocks before it.
 __global__ __launch_bounds__(64) void k_block_fill(const BlkParams P) {
   const int64_t bh = blockIdx.x / P.nb;
   const int j = (int)(blockIdx.x - bh * P.nb), lane = threadIdx.x;
+  const int32_t* cnt = P.cnt + bh * P.nb;
+  auto items_of = [&](int c) { return max(1, (c + P.seg - 1) / P.seg); };
+  int off = 0, first = 0, slot = 0;
+  for (int i = lane; i < j; i += 64) {
+    const int c = cnt[i], n = items_of(c);
+    off += c;
+    first += n;
+    slot += n > 1 ? n : 0;
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    off += __shfl_xor(off, o);
+    first += __shfl_xor(first, o);
+    slot += __shfl_xor(slot, o);
+  }
+  const int items = items_of(cnt[j]);
+  for (int s = lane; s < items; s += 64) P.items[bh * P.max_items + first + s] = make_int2(j, s * P.seg);
+  if (lane == 0) {
+    P.off[bh * P.nb + j] = off;
+    P.slot[bh * P.nb + j] = items > 1 ? slot : -1;
+    if (j == P.nb - 1) P.n_items[bh] = first + items;
+  }
   const uint64_t* bits = P.bits + bh * P.W * P.nb + j;
-  int32_t* list = P.list + bh * P.L * P.n + P.off[bh * P.nb + j];
+  int32_t* list = P.list + bh * P.L * P.n + off;
   int base = 0;
   for (int w0 = 0; w0 < P.W; w0 += 64) {
     uint64_t m = w0 + lane < P.W ? bits[(int64_t)(w0 + lane) * P.nb] : 0;
@@ -131,7 +108,7 @@ __device__ __forceinline__ void gather_rows(char* lds, int width, int wave, int 
 }
 
 template <typename T, int DKP, int DVP, int KTW, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 2 && KTW == 1 && DKP + DVP <= 256 ? 3 : 2) void k_block_dkdv(const BlkParams P) {
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DKP + DVP > 256 ? 1 : sizeof(T) == 2 && KTW == 1 && DKP + DVP <= 256 ? 3 : 2) void k_block_dkdv(const BlkParams P) {
   constexpr int ES = sizeof(T), WK = DKP * ES / 16, WV = DVP * ES / 16, NK = DKP * ES / 64, NV = DVP * ES / 64;
   constexpr int KEYS = WAVES >= 4 ? 64 : 32, KG = KEYS / 16 / KTW, RG = WAVES / KG, ROWS = 32 * RG;
   constexpr int QB = ROWS * WK * 16, STAGE = QB + ROWS * WV * 16, SLABS = 32 / blk_slab<T>();
@@ -398,8 +375,6 @@ template <typename T, int DKP, int DVP, int KTW, int WAVES> hipError_t dkdv_t(co
 template <typename T, int DKP, int DVP> hipError_t grad_t(const BlkParams& P, hipStream_t st) {
   const int64_t bh = (int64_t)P.B * P.Hkv;
   hipLaunchKernelGGL(k_block_bits, dim3((unsigned)(bh * P.W), (P.nb + INV_PIECE - 1) / INV_PIECE), dim3(256), 0, st, P);
-  hipLaunchKernelGGL(k_block_count, dim3((P.nb + 63) / 64, (unsigned)bh), dim3(64), 0, st, P);
-  hipLaunchKernelGGL(k_block_plan, dim3((unsigned)bh), dim3(1024), 0, st, P);
   hipLaunchKernelGGL(k_block_fill, dim3((unsigned)(bh * P.nb)), dim3(64), 0, st, P);
   const int64_t work = bh * P.max_items;
   // two key tiles a wave where their gradients fit the registers

@@ -131,6 +131,7 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) 
   constexpr int NK = DKP * ES / 64, NV = DVP * ES / 64, KEY_T = KT / 16, SLABS = KT / blk_slab<T>();
   constexpr int KB = KT * WK * 16, STAGE = KB + KT * WV * 16, NT = WAVES, THREADS = 64 * (WAVES + 1);
   constexpr int OUT = GRAD ? DKP : DVP;  // width of the accumulated rows
+  constexpr bool EXACT = GRAD && ES == 2 && WAVES < TILE_WAVES_MAX;  // delta put right (15 tiles leave no registers for it)
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int words = (P.nb + 31) / 32, pitch = P.n + 1;
   __shared__ int slast;
@@ -150,6 +151,7 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) 
     rank = blockIdx.x / heads;
     bh = blockIdx.x - rank * heads;
   }
+  if constexpr (GRAD) blk_clear_counts(P, tid, THREADS);
   if (rank >= groups) return;
   const int t0 = (groups - 1 - rank) * NT;
   const int b = bh / P.Hkv, h = bh - b * P.Hkv;
@@ -207,7 +209,14 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) 
       for (int s = 0; s < NV; ++s) g[s] = live ? blk_ld(gr, 64 * s + 16 * a, vw) : zero16();
       const int64_t lr = ((int64_t)b * P.Hq + hd) * P.L + li;
       nref = live ? -P.lse_in[lr] * BLK_LOG2E : 0.f;
-      l = live ? P.delta[lr] : 0.f;
+      const char* orow = P.o.p + b * P.o.sb + li * P.o.st + hd * P.o.sh;
+      u32x4 ov[NV];
+#pragma unroll
+      for (int s = 0; s < NV; ++s) ov[s] = live ? blk_ld(orow, 64 * s + 16 * a, vw) : zero16();
+#pragma unroll
+      for (int s = 0; s < NV; ++s) l += blk_dot<T>(g[s], ov[s]);
+      l = blk_quad_sum(l);
+      if (!EXACT && live && a == 0) P.delta[lr] = l;
     }
   }
   const uint16_t* at = lists + (live ? row.i - q0 : 0) * pitch;
@@ -215,6 +224,10 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) 
   f32x4 acc[OUT / 16];
 #pragma unroll
   for (int d = 0; d < OUT / 16; ++d) acc[d] = zero4();
+  f32x4 mean[EXACT ? OUT / 16 : 1];  // sum_j p_j k_j
+#pragma unroll
+  for (int d = 0; d < (EXACT ? OUT / 16 : 1); ++d) mean[d] = zero4();
+  float off = 0.f;
   const float sc = P.scale * BLK_LOG2E, per_sc = 1.f / sc;
   float grown = -__builtin_inff();  // a score above this moves the reference
   const Rows<WK> krow(lane);
@@ -259,7 +272,7 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) 
           for (int i = 0; i < 4; ++i)
             if (k0 + 16 * kt + 4 * a + i > row.p) s[kt][i] = -__builtin_inff();
       }
-      float p[KEY_T][4];
+      float p[KEY_T][4], pw[EXACT ? KEY_T : 1][4];
       if constexpr (!GRAD) {
         float mx = s[0][0];
 #pragma unroll
@@ -294,16 +307,24 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) 
 #pragma unroll
           for (int w = 0; w < NV; ++w) dp = mma_slab<T>(vrow.read(vs, kt, w), g[w], dp);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p[kt][i] = __builtin_amdgcn_exp2f(s[kt][i] * sc + nref) * (dp[i] - l);
+          for (int i = 0; i < 4; ++i) {
+            const float w = __builtin_amdgcn_exp2f(s[kt][i] * sc + nref);
+            p[kt][i] = w * (dp[i] - l);
+            if constexpr (EXACT) {
+              pw[kt][i] = w;
+              off += take ? p[kt][i] : 0.f;
+            }
+          }
         }
       }
 #pragma unroll
       for (int sl = 0; sl < SLABS; ++sl) {
-        u32x4 w, lo = zero16();
+        u32x4 w, lo = zero16(), y = zero16();
         if constexpr (GRAD && ES == 2) {  // what the rounding to bf16 leaves goes through the product as well
           const float v[8] = {p[2 * sl][0], p[2 * sl][1], p[2 * sl][2], p[2 * sl][3],
                               p[2 * sl + 1][0], p[2 * sl + 1][1], p[2 * sl + 1][2], p[2 * sl + 1][3]};
           split_bf16(v, w, lo);
+          if constexpr (EXACT) y = blk_pack<T>(pw, sl);
         } else {
           w = blk_pack<T>(p, sl);
         }
@@ -311,12 +332,14 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) 
         for (int i = 0; i < 4; ++i) {  // rows that have not chosen the block
           w[i] = take ? w[i] : 0u;
           lo[i] = take ? lo[i] : 0u;
+          if constexpr (EXACT) y[i] = take ? y[i] : 0u;
         }
 #pragma unroll
         for (int d = 0; d < OUT / 16; ++d) {
           const u32x4 f = col.read(GRAD ? ks : vs, sl, d);
           acc[d] = mma_slab<T>(f, w, acc[d]);
           if constexpr (GRAD && ES == 2) acc[d] = mma_slab<T>(f, lo, acc[d]);
+          if constexpr (EXACT) mean[d] = mma_slab<T>(f, y, mean[d]);
           // without this all reads move ahead of the products, and registers spill
           if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
         }
@@ -326,6 +349,12 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) 
   }
   if (lane == 0) ring_put(&ring.done[wave], 0x7fffffff);
   if constexpr (!GRAD) l = blk_quad_sum(l);
+  if constexpr (EXACT) {
+    off = blk_quad_sum(off);
+    if (live && a == 0) P.delta[((int64_t)row.b * P.Hq + row.head) * P.L + row.i] = l + off;
+#pragma unroll
+    for (int d = 0; d < OUT / 16; ++d) acc[d] -= mean[d] * off;
+  }
   if (!row.in) return;
   const BlkHeads& o = GRAD ? P.dq : P.o;
   const int width = GRAD ? P.dkw : P.dvw;
@@ -370,6 +399,7 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
 // with 64, 578 with 7 tiles of 64; gradient at B = 2, L = 4096: 246, 284, 289).
 // fp32 with wide heads takes 3 tiles for their registers.
 template <typename T, int DKP, int DVP, bool GRAD> hipError_t by_block(const BlkParams& P, hipStream_t st) {
+  if (P.tiles < 4096) return launch_t<T, DKP, DVP, sizeof(T) == 4 ? 16 : 32, 3, GRAD>(P, st);
   if constexpr (sizeof(T) == 4) {
     return launch_t<T, DKP, DVP, 16, DVP == 256 || (GRAD && DKP == 128) ? 3 : 15, GRAD>(P, st);
   } else {

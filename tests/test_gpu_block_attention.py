@@ -102,7 +102,7 @@ def test_training(hq, hkv, dk, dv, block, n, L, dtype):
     (64, 4, 128, 256, 64, 4, 7, 150, False), (40, 2, 64, 128, 128, 3, 4, 277, True), (32, 8, 128, 64, 128, 2, 10, 210, True),
     (16, 1, 32, 256, 64, 20, 3, 1400, False)])
 def test_enough_queries_to_share_keys(hq, hkv, dk, dv, block, n, B, L, lens, dtype):
-    """At least 4096 tiles: workgroups of 15 (or 3) tiles share keys and values."""
+    """At least 4096 tiles: workgroups of 15 tiles (of 3 for wide fp32 heads) share keys and values."""
     cfg = _cfg(hq, hkv, dk, dv, block, n, min(1, n - 2), 2, dtype)
     rng = np.random.default_rng(L)
     if lens:
@@ -141,7 +141,7 @@ def test_any_selection_of_single_queries(dtype):
     (64, 4, 128, 256, 64, 4, 2, 150), (40, 2, 64, 128, 128, 3, 1, 277), (16, 4, 128, 64, 128, 2, 4, 290),
     (8, 2, 32, 256, 64, 20, 1, 2100)])
 def test_many_queries(hq, hkv, dk, dv, block, n, B, L, dtype):
-    """More than a thousand tiles, a wave each; padding and chunks among them."""
+    """Some thousand tiles, three a workgroup; padding and chunks among them."""
     cfg = _cfg(hq, hkv, dk, dv, block, n, min(1, n - 2), 2, dtype)
     _case(cfg, B, L, seed=L)
     rng = np.random.default_rng(L)
