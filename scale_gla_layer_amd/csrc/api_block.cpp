@@ -111,6 +111,19 @@ void set_fwd(BlkParams& P, const FwdWs& w, void* ws) {
   }
 }
 
+struct StepWs {
+  size_t sel, key;
+  FwdWs fwd;
+};
+StepWs step_ws(const BlkParams& P) {
+  StepWs w{};
+  Take take;
+  w.sel = take((size_t)P.B * P.Hkv * P.n * 4);
+  w.key = take(blk_step_spread(P) ? (size_t)P.B * P.Hkv * P.nb * 8 : 0);
+  w.fwd = fwd_ws(P, take);
+  return w;
+}
+
 struct BwdWs {
   size_t delta, bits, cnt, off, slot, list, items, n_items, part, po, pm, total;
   int parts, seg, W, max_items, max_parts;
@@ -171,9 +184,7 @@ size_t msgla_block_attention_backward_workspace_bytes(const msgla_block_config* 
 
 size_t msgla_block_attention_step_workspace_bytes(const msgla_block_config* cfg, int64_t B, int64_t S) {
   if (!blk_config_ok(cfg) || !blk_sizes_ok(B, 1, S)) return BAD;
-  Take take;
-  take((size_t)B * cfg->heads_kv * cfg->n_select * 4);
-  return fwd_ws(blk_params(cfg, B, 1, S), take).total;
+  return step_ws(blk_params(cfg, B, 1, S)).fwd.total;
 }
 
 msgla_status msgla_block_means(const msgla_block_config* cfg, const msgla_heads* k,
@@ -310,9 +321,8 @@ msgla_status msgla_block_attention_step(const msgla_block_config* cfg, const msg
       !aligned16(workspace))
     return MSGLA_ERR_INVALID_ARG;
   BlkParams P = blk_params(cfg, B, 1, S);
-  Take take;
-  const size_t sel = take((size_t)B * P.Hkv * P.n * 4);
-  const FwdWs w = fwd_ws(P, take);
+  const StepWs s = step_ws(P);
+  const FwdWs& w = s.fwd;
   if (workspace_bytes < w.total) return MSGLA_ERR_WORKSPACE;
   if (!fwd_grid_ok(P, w.parts) || !select_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   P.q = heads_of(q_t, es);
@@ -323,7 +333,8 @@ msgla_status msgla_block_attention_step(const msgla_block_config* cfg, const msg
   P.o = heads_of(out_t, es);
   P.means = means;
   P.start = pos;
-  P.sel_out = at<int32_t>(workspace, sel);
+  P.sel_out = at<int32_t>(workspace, s.sel);
+  P.bits = at<uint64_t>(workspace, s.key);
   P.sel = P.sel_out;
   set_fwd(P, w, workspace);
   hipStream_t st = static_cast<hipStream_t>(stream);

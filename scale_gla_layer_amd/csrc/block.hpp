@@ -39,7 +39,7 @@ struct BlkParams {
   float* pm;     // [tile][part][16][2] their maxima (in units of log 2) and sums; backward [..] delta's errors
   // queries of each block
   int seg, W, max_items, max_parts;  // queries of a work item, 64-query words, bounds per (sequence, head)
-  uint64_t* bits;   // [B Hkv][W][nb]
+  uint64_t* bits;   // [B Hkv][W][nb]; a step's scores [B Hkv][nb]
   int32_t* cnt;     // [B Hkv][nb]
   int32_t* off;     // [B Hkv][nb]
   int32_t* slot;    // [B Hkv][nb] first partial of a block of several items
@@ -52,6 +52,9 @@ struct BlkParams {
 hipError_t launch_block_means(const BlkParams& P, bool bf16_path, hipStream_t st);
 hipError_t launch_block_select(const BlkParams& P, bool bf16_path, hipStream_t st);
 // the step: puts the token into the caches and selects its blocks
+// Caches of more blocks have their scores spread over workgroups (and in memory: `bits`).
+constexpr int BLK_STEP_ONE = 128;
+inline bool blk_step_spread(const BlkParams& P) { return P.nb > BLK_STEP_ONE; }
 hipError_t launch_block_step(const BlkParams& P, bool bf16_path, hipStream_t st);
 hipError_t launch_block_forward(const BlkParams& P, bool bf16_path, hipStream_t st);
 // many queries: keys and values shared by a workgroup; nb at most BLK_TILES_MAX

@@ -10,6 +10,8 @@
 // (about 20 steps: each lane counts its own keys, four lane exchanges add up; a
 // row is done once its count is right), going on to the lower ones only where
 // that leaves a tie, and write the chosen blocks in ascending order.
+#include <algorithm>
+
 #include "block_device.hpp"
 
 namespace msgla {
@@ -27,6 +29,7 @@ __device__ __forceinline__ void block_mean(int lgT, int width, float* out, int l
 #pragma unroll
   for (int e = 0; e < PER; ++e) s[e] = 0.0;
   if (pc * 16 < width)
+#pragma unroll 8
     for (int i = lane / LPR; i < (1 << lgT); i += 64 / LPR) {
       float v[PER];
       unpack16<T>(ld16(row(i) + pc * 16), v);
@@ -252,141 +255,181 @@ template <typename T, int DKP, int PIECE> __global__ __launch_bounds__(64 * SEL_
   } while (piece <= top);
 }
 
-// The streaming step's first half, one workgroup a sequence and key-value head:
-// the last wave puts the token's key and value into the caches and renews the
-// mean of the block that this completes (which is the query's own: it is not
-// scored); all waves score the blocks before, four lanes a block; the first one
-// finds the best of up to STEP_PIECE at a time, 64 lanes on the one row.
-constexpr int STEP_WAVES = 16, STEP_PIECE = 512;
+// The streaming step's first half.  A wave puts the token's key and value into
+// the caches and renews the mean of the block that this completes (which is the
+// query's own: it is not scored); the blocks before are scored, four lanes a
+// block; a wave finds the best of up to STEP_PIECE at a time, 64 lanes on the one
+// row.  Up to BLK_STEP_ONE blocks, one workgroup a sequence and key-value head
+// does it all; of longer caches the scores are spread over more workgroups, and
+// the choice is a launch of its own.
+constexpr int STEP_WAVES = 8, STEP_PIECE = 512;
+static_assert(BLK_STEP_ONE <= STEP_PIECE, "one piece, whose scores fit in LDS");
 
-template <typename T, int DKP> __global__ __launch_bounds__(64 * STEP_WAVES) void k_block_step(const BlkParams P) {
-  constexpr int PER = DKP / 4, SLOTS = STEP_PIECE / 64 + 1;
-  __shared__ uint64_t key[STEP_PIECE];
-  __shared__ uint64_t ckey[64];
+template <typename T> __device__ __forceinline__ void step_append(const BlkParams& P, int b, int h, int p, int lane) {
+  const char* nk = P.kt.p + b * P.kt.sb + h * P.kt.sh;
+  const char* nv = P.vt.p + b * P.vt.sb + h * P.vt.sh;
+  char* kr = P.k.p + b * P.k.sb + (int64_t)p * P.k.st + h * P.k.sh;
+  char* vr = P.v.p + b * P.v.sb + (int64_t)p * P.v.st + h * P.v.sh;
+  for (int c = 16 * lane; c < P.dkw * (int)sizeof(T); c += 1024) st16(kr + c, ld16(nk + c));
+  for (int c = 16 * lane; c < P.dvw * (int)sizeof(T); c += 1024) st16(vr + c, ld16(nv + c));
+  const int last = (1 << P.lgT) - 1, own = p >> P.lgT;
+  if ((p & last) == last) {
+    const char* base = P.k.p + b * P.k.sb + ((int64_t)own << P.lgT) * P.k.st + h * P.k.sh;
+    block_mean<T>(P.lgT, P.dkw * (int)sizeof(T), P.means + (((int64_t)b * P.Hkv + h) * P.nb + own) * P.dkw, lane,
+                  [&](int i) { return i == last ? nk : base + i * P.k.st; });
+  }
+}
+
+// key[j] of the blocks first, first + stride, .. before stop, by four lanes each.
+// The whole workgroup comes here; qsum: DKP doubles of LDS.
+template <typename T, int DKP>
+__device__ __forceinline__ void step_scores(const BlkParams& P, int b, int h, int own, int first, int stride, int stop,
+                                            int tid, double* qsum, uint64_t* key) {
+  constexpr int PER = DKP / 4;
+  const int e0 = (tid & 3) * PER;  // the lane's elements
+  const float* means = P.means + ((int64_t)b * P.Hkv + h) * P.nb * P.dkw;
+  float m[PER];
+  auto load = [&](int j) {
+#pragma unroll
+    for (int c = 0; c < PER; c += 4)
+      if (e0 + c < P.dkw) unpack16<float>(ld16(means + (int64_t)min(j, own) * P.dkw + e0 + c), m + c);
+  };
+  load(first);
+  if (tid < DKP) {  // the group's query sums
+    double q = 0.0;
+    if (tid < P.dkw) {
+      const char* qr = P.q.p + b * P.q.sb + (int64_t)h * P.G * P.q.sh + tid * sizeof(T);
+#pragma unroll 8
+      for (int u = 0; u < P.G; ++u) q += (double)to_f32(*reinterpret_cast<const T*>(qr + u * P.q.sh));
+    }
+    qsum[tid] = q;
+  }
+  __syncthreads();
+  for (int j = first; j - ((tid & 63) >> 2) < stop; j += stride) {
+    double s = 0.0;
+#pragma unroll
+    for (int c = 0; c < PER; ++c)
+      if (e0 + c < P.dkw) s += qsum[e0 + c] * (double)m[c];
+    if (j + stride - ((tid & 63) >> 2) < stop) load(j + stride);
+    s += __shfl_xor(s, 1);
+    s += __shfl_xor(s, 2);
+    if ((tid & 3) == 0 && j < stop) key[j] = j < P.n_first || j > own - P.n_recent ? FORCED : score_key(s);
+  }
+}
+
+// A wave's choice among the blocks 0 .. own, in ascending order to out.
+__device__ __forceinline__ void step_choose(const BlkParams& P, int own, const uint64_t* key, int32_t* out, int lane) {
+  constexpr int SLOTS = STEP_PIECE / 64 + 1;
+  __shared__ uint64_t ckey[64];  // chosen so far, while pieces remain
   __shared__ int cblk[64];
-  const int b = blockIdx.x / P.Hkv, h = blockIdx.x % P.Hkv, tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int p = P.start[b];
-  int32_t* out = P.sel_out + (int64_t)blockIdx.x * P.n;
-  if (p < 0 || p >= P.S) {
-    if (tid < P.n) out[tid] = -1;
-    return;
-  }
-  const int own = p >> P.lgT;
-  float* means = P.means + (int64_t)blockIdx.x * P.nb * P.dkw;
-  if (wave == STEP_WAVES - 1) {
-    const char* nk = P.kt.p + b * P.kt.sb + h * P.kt.sh;
-    const char* nv = P.vt.p + b * P.vt.sb + h * P.vt.sh;
-    char* kr = P.k.p + b * P.k.sb + (int64_t)p * P.k.st + h * P.k.sh;
-    char* vr = P.v.p + b * P.v.sb + (int64_t)p * P.v.st + h * P.v.sh;
-    for (int c = 16 * lane; c < P.dkw * (int)sizeof(T); c += 1024) st16(kr + c, ld16(nk + c));
-    for (int c = 16 * lane; c < P.dvw * (int)sizeof(T); c += 1024) st16(vr + c, ld16(nv + c));
-    const int last = (1 << P.lgT) - 1;
-    if ((p & last) == last) {
-      const char* base = P.k.p + b * P.k.sb + ((int64_t)own << P.lgT) * P.k.st + h * P.k.sh;
-      block_mean<T>(P.lgT, P.dkw * (int)sizeof(T), means + (int64_t)own * P.dkw, lane,
-                    [&](int i) { return i == last ? nk : base + i * P.k.st; });
-    }
-  }
-  // the group's query sums, elements PER (l % 4) .. of each four lanes
-  const int e0 = (lane & 3) * PER;
-  double q[PER];
-#pragma unroll
-  for (int e = 0; e < PER; ++e) q[e] = 0.0;
-#pragma unroll 4
-  for (int u = 0; u < P.G; ++u) {
-    const char* qr = P.q.p + b * P.q.sb + (int64_t)(h * P.G + u) * P.q.sh;
-#pragma unroll
-    for (int c = 0; c < PER; c += per16<T>()) {
-      float f[per16<T>()];
-      if (e0 + c < P.dkw) {
-        unpack16<T>(ld16(qr + (e0 + c) * sizeof(T)), f);
-#pragma unroll
-        for (int e = 0; e < per16<T>(); ++e) q[c + e] += (double)f[e];
-      }
-    }
-  }
   int carried = 0, piece = 0;
   do {
     const int stop = min(piece + STEP_PIECE, own + 1);
-    for (int j0 = piece + (tid >> 2); j0 - (lane >> 2) < stop; j0 += 16 * STEP_WAVES) {
-      const int j = min(j0, own);
-      double s = 0.0;
+    const bool more = stop <= own;
+    uint64_t k[SLOTS];
+    const int cb = cblk[lane];
+    k[0] = lane < carried ? ckey[lane] : 0;
 #pragma unroll
-      for (int c = 0; c < PER; c += 4)
-        if (e0 + c < P.dkw) {
-          float f[4];
-          unpack16<float>(ld16(means + (int64_t)j * P.dkw + e0 + c), f);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s += q[c + e] * (double)f[e];
-        }
-      s += __shfl_xor(s, 1);
-      s += __shfl_xor(s, 2);
-      if ((lane & 3) == 0 && j0 < stop)
-        key[j0 - piece] = j0 < P.n_first || j0 > own - P.n_recent ? FORCED : score_key(s);
+    for (int e = 1; e < SLOTS; ++e) {
+      const int j = piece + 64 * (e - 1) + lane;
+      k[e] = j < stop ? key[j] : 0;
     }
-    __syncthreads();
-    if (wave == 0) {
-      const bool more = stop <= own;
-      uint64_t k[SLOTS];
-      const int cb = cblk[lane];
-      k[0] = lane < carried ? ckey[lane] : 0;
+    // as in k_block_select, the row's values in all lanes: the upper halves first,
+    // the lower ones where those tie
+    auto count = [&](auto reach) {
+      int c = 0;
 #pragma unroll
-      for (int e = 1; e < SLOTS; ++e) k[e] = 64 * (e - 1) + lane < stop - piece ? key[64 * (e - 1) + lane] : 0;
-      // as in k_block_select, the row's values in all lanes: the upper halves first,
-      // the lower ones where those tie
-      auto count = [&](auto reach) {
-        int c = 0;
+      for (int e = 0; e < SLOTS; ++e) c += (int)__popcll(__ballot(reach((uint32_t)(k[e] >> 32), (uint32_t)k[e])));
+      return c;
+    };
+    auto largest = [&](int n, bool& exact, auto reach) {
+      uint32_t t = 0;
+      exact = false;
+      for (uint32_t bit = 1u << 31; bit && !exact; bit >>= 1) {
+        const int c = count([&](uint32_t u, uint32_t v) { return reach(u, v, t | bit); });
+        if (c >= n) t |= bit, exact = c == n;
+      }
+      return t;
+    };
+    uint32_t hi = 1, lo = 0;
+    bool all_hi = true, all_lo = true;
+    int ties = 0;
+    if (count([](uint32_t u, uint32_t) { return u != 0; }) > P.n) {
+      hi = largest(P.n, all_hi, [](uint32_t u, uint32_t, uint32_t t) { return u >= t; });
+      if (!all_hi) {
+        const int want = P.n - count([&](uint32_t u, uint32_t) { return u > hi; });
+        lo = largest(want, all_lo, [&](uint32_t u, uint32_t v, uint32_t t) { return u == hi && v >= t; });
+        ties = want - count([&](uint32_t u, uint32_t v) { return u == hi && v > lo; });
+      }
+    }
+    int base = 0;
+    const uint64_t below = (1ull << lane) - 1, cut = (uint64_t)hi << 32 | lo;
 #pragma unroll
-        for (int e = 0; e < SLOTS; ++e) c += (int)__popcll(__ballot(reach((uint32_t)(k[e] >> 32), (uint32_t)k[e])));
-        return c;
-      };
-      auto largest = [&](int n, bool& exact, auto reach) {
-        uint32_t t = 0;
-        exact = false;
-        for (uint32_t bit = 1u << 31; bit && !exact; bit >>= 1) {
-          const int c = count([&](uint32_t u, uint32_t v) { return reach(u, v, t | bit); });
-          if (c >= n) t |= bit, exact = c == n;
-        }
-        return t;
-      };
-      uint32_t hi = 1, lo = 0;
-      bool all_hi = true, all_lo = true;
-      int ties = 0;
-      if (count([](uint32_t u, uint32_t) { return u != 0; }) > P.n) {
-        hi = largest(P.n, all_hi, [](uint32_t u, uint32_t, uint32_t t) { return u >= t; });
-        if (!all_hi) {
-          const int want = P.n - count([&](uint32_t u, uint32_t) { return u > hi; });
-          lo = largest(want, all_lo, [&](uint32_t u, uint32_t v, uint32_t t) { return u == hi && v >= t; });
-          ties = want - count([&](uint32_t u, uint32_t v) { return u == hi && v > lo; });
+    for (int e = 0; e < SLOTS; ++e) {
+      const uint32_t u = (uint32_t)(k[e] >> 32);
+      const uint64_t eq = __ballot(!all_hi && k[e] == cut);
+      const bool take = all_hi ? u >= hi : k[e] > cut || (k[e] == cut && (all_lo || (int)__popcll(eq & below) < ties));
+      ties -= min(ties, (int)__popcll(eq));
+      const uint64_t took = __ballot(take);
+      if (take) {
+        const int at = base + (int)__popcll(took & below), j = e == 0 ? cb : piece + 64 * (e - 1) + lane;
+        if (more) {
+          ckey[at] = k[e];
+          cblk[at] = j;
+        } else {
+          out[at] = j;
         }
       }
-      int base = 0;
-      const uint64_t below = (1ull << lane) - 1, cut = (uint64_t)hi << 32 | lo;
-#pragma unroll
-      for (int e = 0; e < SLOTS; ++e) {
-        const uint32_t u = (uint32_t)(k[e] >> 32);
-        const uint64_t eq = __ballot(!all_hi && k[e] == cut);
-        const bool take = all_hi ? u >= hi : k[e] > cut || (k[e] == cut && (all_lo || (int)__popcll(eq & below) < ties));
-        ties -= min(ties, (int)__popcll(eq));
-        const uint64_t took = __ballot(take);
-        if (take) {
-          const int at = base + (int)__popcll(took & below), j = e == 0 ? cb : piece + 64 * (e - 1) + lane;
-          if (more) {
-            ckey[at] = k[e];
-            cblk[at] = j;
-          } else {
-            out[at] = j;
-          }
-        }
-        base += (int)__popcll(took);
-      }
-      carried = base;
-      if (!more && lane >= base && lane < P.n) out[lane] = -1;
+      base += (int)__popcll(took);
     }
-    __syncthreads();
+    carried = base;
+    asm volatile("" ::: "memory");  // the wave's own LDS writes, before the next piece's reads
+    if (!more && lane >= base && lane < P.n) out[lane] = -1;
     piece += STEP_PIECE;
   } while (piece <= own);
+}
+
+// One workgroup a sequence and head: everything (SPREAD false); or gridDim.y - 1
+// that score and one that appends, with the choice to come.
+template <typename T, int DKP, bool SPREAD> __global__ __launch_bounds__(64 * STEP_WAVES) void k_block_step(const BlkParams P) {
+  __shared__ uint64_t lds[SPREAD ? 1 : BLK_STEP_ONE];
+  __shared__ double qsum[DKP];
+  const int b = blockIdx.x / P.Hkv, h = blockIdx.x % P.Hkv, tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int p = P.start[b], own = p >> P.lgT;
+  int32_t* out = P.sel_out + (int64_t)blockIdx.x * P.n;
+  if (p < 0 || p >= P.S) {
+    if (!SPREAD && tid < P.n) out[tid] = -1;
+    return;
+  }
+  const int scorers = SPREAD ? (int)gridDim.y - 1 : 1;
+  if (!SPREAD || (int)blockIdx.y < scorers) {
+    uint64_t* key = SPREAD ? P.bits + (int64_t)blockIdx.x * P.nb : lds;
+    step_scores<T, DKP>(P, b, h, own, (int)blockIdx.y * 16 * STEP_WAVES + (tid >> 2), scorers * 16 * STEP_WAVES,
+                        own + 1, tid, qsum, key);
+    if constexpr (SPREAD) return;
+    __syncthreads();
+    if (wave == 0) step_choose(P, own, key, out, lane);
+  }
+  if (wave == STEP_WAVES - 1) step_append<T>(P, b, h, p, lane);
+}
+
+__global__ __launch_bounds__(64) void k_block_choose(const BlkParams P) {
+  const int p = P.start[blockIdx.x / P.Hkv], lane = threadIdx.x;
+  int32_t* out = P.sel_out + (int64_t)blockIdx.x * P.n;
+  if (p >= 0 && p < P.S) step_choose(P, p >> P.lgT, P.bits + (int64_t)blockIdx.x * P.nb, out, lane);
+  else if (lane < P.n) out[lane] = -1;
+}
+
+template <typename T, int DKP> void step_t(const BlkParams& P, hipStream_t st) {
+  const unsigned bh = (unsigned)(P.B * P.Hkv);
+  if (blk_step_spread(P)) {
+    const dim3 grid(bh, (unsigned)std::min((P.nb + 16 * STEP_WAVES - 1) / (16 * STEP_WAVES) + 1, 65535));
+    hipLaunchKernelGGL((k_block_step<T, DKP, true>), grid, dim3(64 * STEP_WAVES), 0, st, P);
+    hipLaunchKernelGGL(k_block_choose, dim3(bh), dim3(64), 0, st, P);
+  } else {
+    hipLaunchKernelGGL((k_block_step<T, DKP, false>), dim3(bh), dim3(64 * STEP_WAVES), 0, st, P);
+  }
 }
 
 template <typename T, int DKP> void select_t(const BlkParams& P, hipStream_t st) {
@@ -406,12 +449,9 @@ hipError_t launch_block_means(const BlkParams& P, bool bf16_path, hipStream_t st
 }
 
 hipError_t launch_block_step(const BlkParams& P, bool bf16_path, hipStream_t st) {
-  const dim3 grid((unsigned)(P.B * P.Hkv)), block(64 * STEP_WAVES);
   const bool k64 = blk_dkp(P.dkw) == 64;
-  if (bf16_path && k64) hipLaunchKernelGGL((k_block_step<bf16, 64>), grid, block, 0, st, P);
-  else if (bf16_path) hipLaunchKernelGGL((k_block_step<bf16, 128>), grid, block, 0, st, P);
-  else if (k64) hipLaunchKernelGGL((k_block_step<float, 64>), grid, block, 0, st, P);
-  else hipLaunchKernelGGL((k_block_step<float, 128>), grid, block, 0, st, P);
+  if (bf16_path) k64 ? step_t<bf16, 64>(P, st) : step_t<bf16, 128>(P, st);
+  else k64 ? step_t<float, 64>(P, st) : step_t<float, 128>(P, st);
   return hipGetLastError();
 }
 

@@ -244,9 +244,9 @@ class DeviceRecurrence:
     def _forward(self, x, z, bias, mask, h_in, y, h_out):
         torch = _torch()
         ws = self._room(x, binding.msgla_recurrence_workspace_bytes)
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device) if y is None else y
+        y = x.new_empty(x.shape) if y is None else y
         if h_out is None:
-            h_out = torch.empty((x.shape[0], x.shape[2]), dtype=torch.float32, device=x.device)
+            h_out = x.new_empty((x.shape[0], x.shape[2]), dtype=torch.float32)
         binding.msgla_recurrence_forward(self.cfg, x, z, y, ws, bias, mask, h_in, h_out)
         return y, h_out
 
@@ -258,8 +258,8 @@ class DeviceRecurrence:
     def _backward(self, x, z, dy, bias, mask, h_in, dh_out, dx, dz):
         torch = _torch()
         ws = self._room(x, binding.msgla_recurrence_backward_workspace_bytes)
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dx is None else dx
-        dz = torch.empty(x.shape, dtype=x.dtype, device=x.device) if dz is None else dz
+        dx = x.new_empty(x.shape) if dx is None else dx
+        dz = x.new_empty(x.shape) if dz is None else dz
         dbias = None if bias is None else torch.empty_like(bias)
         dh_in = None if h_in is None else torch.empty_like(h_in)
         binding.msgla_recurrence_backward(self.cfg, x, z, dy, dx, dz, ws, bias, mask, h_in, dh_out, dbias, dh_in)
@@ -271,7 +271,7 @@ class DeviceRecurrence:
         return _on(x_t, self._step, x_t, z_t, h, bias, mask, y_t, h if h_out is None else h_out)
 
     def _step(self, x_t, z_t, h, bias, mask, y_t, h_out):
-        y_t = _torch().empty(x_t.shape, dtype=x_t.dtype, device=x_t.device) if y_t is None else y_t
+        y_t = x_t.new_empty(x_t.shape) if y_t is None else y_t
         binding.msgla_recurrence_step(self.cfg, x_t, z_t, y_t, h, h_out, bias, mask)
         return y_t, h_out
 
@@ -300,8 +300,8 @@ class DeviceBlockAttention:
     def _means(self, k, lens, start_from, means):
         torch = _torch()
         if means is None:
-            means = torch.empty((k.shape[0], self.cfg.heads_kv, binding.block_count(self.cfg, k.shape[1]),
-                                 self.cfg.d_k), dtype=torch.float32, device=k.device)
+            means = k.new_empty((k.shape[0], self.cfg.heads_kv, binding.block_count(self.cfg, k.shape[1]),
+                                 self.cfg.d_k), dtype=torch.float32)
         binding.msgla_block_means(self.cfg, k, means, lens, start_from)
         return means
 
@@ -312,8 +312,7 @@ class DeviceBlockAttention:
     def _select(self, q, means, start, lens, sel):
         torch = _torch()
         if sel is None:
-            sel = torch.empty((q.shape[0], self.cfg.heads_kv, q.shape[1], self.cfg.n_select), dtype=torch.int32,
-                              device=q.device)
+            sel = q.new_empty((q.shape[0], self.cfg.heads_kv, q.shape[1], self.cfg.n_select), dtype=torch.int32)
         binding.msgla_block_select(self.cfg, q, means, means.shape[2] * self.cfg.block, sel, start, lens)
         return sel
 
@@ -326,9 +325,9 @@ class DeviceBlockAttention:
         B, L = q.shape[:2]
         ws = self._room(binding.msgla_block_attention_workspace_bytes, q.device, B, L, k.shape[1])
         if out is None:
-            out = torch.empty((B, L, self.cfg.heads_q, self.cfg.d_v), dtype=q.dtype, device=q.device)
+            out = q.new_empty((B, L, self.cfg.heads_q, self.cfg.d_v))
         if lse is None:
-            lse = torch.empty((B, self.cfg.heads_q, L), dtype=torch.float32, device=q.device)
+            lse = q.new_empty((B, self.cfg.heads_q, L), dtype=torch.float32)
         binding.msgla_block_attention(self.cfg, q, k, v, sel, out, lse, ws, start, lens)
         return out, lse
 
@@ -337,10 +336,9 @@ class DeviceBlockAttention:
         return _on(q, self._backward, q, k, v, sel, out, lse, dout, start, lens, dq, dk, dv)
 
     def _backward(self, q, k, v, sel, out, lse, dout, start, lens, dq, dk, dv):
-        torch = _torch()
         ws = self._room(binding.msgla_block_attention_backward_workspace_bytes, q.device, q.shape[0], q.shape[1],
                         k.shape[1])
-        dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) if d is None else d
+        dq, dk, dv = (t.new_empty(t.shape) if d is None else d
                       for t, d in ((q, dq), (k, dk), (v, dv)))
         binding.msgla_block_attention_backward(self.cfg, q, k, v, sel, out, lse, dout, dq, dk, dv, ws, start, lens)
         return dq, dk, dv
@@ -351,10 +349,9 @@ class DeviceBlockAttention:
         return _on(q_t, self._step, q_t, k_t, v_t, k, v, means, pos, out_t)
 
     def _step(self, q_t, k_t, v_t, k, v, means, pos, out_t):
-        torch = _torch()
         ws = self._room(binding.msgla_block_attention_step_workspace_bytes, q_t.device, q_t.shape[0], k.shape[1])
         if out_t is None:
-            out_t = torch.empty((q_t.shape[0], self.cfg.heads_q, self.cfg.d_v), dtype=q_t.dtype, device=q_t.device)
+            out_t = q_t.new_empty((q_t.shape[0], self.cfg.heads_q, self.cfg.d_v))
         binding.msgla_block_attention_step(self.cfg, q_t, k_t, v_t, k, v, means, pos, out_t, ws)
         return out_t
 
