@@ -412,7 +412,7 @@ typedef struct {
  * with the input's scale beta by `input`: 1 (PLAIN), 1 - alpha (CONVEX: h is a
  * weighted mean of the inputs), or sqrt(1 - alpha^2) (NORM: keeps the variance
  * of independent inputs).
- *   width: channels, 1 .. 65536.  dtype: of x, z, y and their gradients; the
+ *   width: channels, 1 .. 65536.  gate_normalizer: 1e-6 .. 1e6.  dtype: of x, z, y and their gradients; the
  *   gate, the state and every sum are fp32, as are bias and the states.
  */
 typedef enum {
@@ -527,7 +527,10 @@ typedef struct {
  *   lens:  keys that sequence b has, at most S; NULL: S
  * A query row at a position below 0 or not below lens[b] is padding: it selects
  * nothing, its output row is 0, its lse minus infinity and its gradient 0.  What
- * k and v hold behind lens[b] is not used.
+ * k and v hold behind lens[b] is not used.  A NaN or infinity of k, v, q or dout
+ * at a position that is used may reach every row of its sequence and key-value
+ * head, not only those that chose its block (unused weights are zeroes in the
+ * products).
  * sel [B][heads_kv][L][n_select] int32 holds each query's blocks in ascending
  * order, then -1.  An entry counts if it names a block at or before the query's
  * own and is greater than every entry that counted before it; other entries

@@ -76,8 +76,8 @@ class RecurrenceConfig:
             raise ValueError("width must be 1 .. 65536")
         if self.input not in RECURRENCE_INPUTS:
             raise ValueError(f"input must be one of {RECURRENCE_INPUTS}")
-        if not 0 < self.gate_normalizer <= 3.0e38:
-            raise ValueError("gate_normalizer must be positive and finite")
+        if not 1e-6 <= self.gate_normalizer <= 1e6:
+            raise ValueError("gate_normalizer must be 1e-6 .. 1e6")
         if self.dtype not in (F32, BF16):
             raise ValueError(f"dtype must be {F32!r} or {BF16!r}")
 

@@ -12,8 +12,8 @@ constexpr size_t BAD = (size_t)-1;
 
 bool rec_config_ok(const msgla_recurrence_config* c) {
   return c && c->width >= 1 && c->width <= 65536 && c->input >= 0 && c->input <= 2 &&
-         (c->dtype == MSGLA_F32 || c->dtype == MSGLA_BF16) && c->gate_normalizer > 0.f &&
-         c->gate_normalizer <= 3.0e38f;
+         (c->dtype == MSGLA_F32 || c->dtype == MSGLA_BF16) && c->gate_normalizer >= 1e-6f &&
+         c->gate_normalizer <= 1e6f;
 }
 
 bool rec_batch_ok(int64_t B, int64_t L) {

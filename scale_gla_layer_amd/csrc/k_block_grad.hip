@@ -44,25 +44,43 @@ __global__ __launch_bounds__(256) void k_block_bits(const BlkParams P) {
 }
 
 // A wave writes one block's queries in order, and where its list, its work items
-// and its partials begin: sums over the blocks before it.
-__global__ __launch_bounds__(64) void k_block_fill(const BlkParams P) {
-  const int64_t bh = blockIdx.x / P.nb;
-  const int j = (int)(blockIdx.x - bh * P.nb), lane = threadIdx.x;
+// and its partials begin: sums over the blocks before it, which FILL_WAVES
+// neighbours form together.
+constexpr int FILL_WAVES = 16;
+
+__global__ __launch_bounds__(64 * FILL_WAVES) void k_block_fill(const BlkParams P) {
+  __shared__ int sums[FILL_WAVES][3];
+  const int groups = (P.nb + FILL_WAVES - 1) / FILL_WAVES;
+  const int64_t bh = blockIdx.x / groups;
+  const int j0 = (int)(blockIdx.x - bh * groups) * FILL_WAVES, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int j = j0 + wave;
   const int32_t* cnt = P.cnt + bh * P.nb;
   auto items_of = [&](int c) { return max(1, (c + P.seg - 1) / P.seg); };
   int off = 0, first = 0, slot = 0;
-  for (int i = lane; i < j; i += 64) {
+  auto add = [&](int i) {
     const int c = cnt[i], n = items_of(c);
     off += c;
     first += n;
     slot += n > 1 ? n : 0;
-  }
+  };
+  auto total = [&] {
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    off += __shfl_xor(off, o);
-    first += __shfl_xor(first, o);
-    slot += __shfl_xor(slot, o);
-  }
+    for (int o = 1; o < 64; o <<= 1) {
+      off += __shfl_xor(off, o);
+      first += __shfl_xor(first, o);
+      slot += __shfl_xor(slot, o);
+    }
+  };
+#pragma unroll 4
+  for (int i = threadIdx.x; i < j0; i += 64 * FILL_WAVES) add(i);
+  total();
+  if (lane == 0) sums[wave][0] = off, sums[wave][1] = first, sums[wave][2] = slot;
+  __syncthreads();
+  if (j >= P.nb) return;
+  off = first = slot = 0;
+  if (lane < FILL_WAVES) off = sums[lane][0], first = sums[lane][1], slot = sums[lane][2];
+  else if (lane - FILL_WAVES < wave) add(j0 + lane - FILL_WAVES);
+  total();
   const int items = items_of(cnt[j]);
   for (int s = lane; s < items; s += 64) P.items[bh * P.max_items + first + s] = make_int2(j, s * P.seg);
   if (lane == 0) {
@@ -375,7 +393,8 @@ template <typename T, int DKP, int DVP, int KTW, int WAVES> hipError_t dkdv_t(co
 template <typename T, int DKP, int DVP> hipError_t grad_t(const BlkParams& P, hipStream_t st) {
   const int64_t bh = (int64_t)P.B * P.Hkv;
   hipLaunchKernelGGL(k_block_bits, dim3((unsigned)(bh * P.W), (P.nb + INV_PIECE - 1) / INV_PIECE), dim3(256), 0, st, P);
-  hipLaunchKernelGGL(k_block_fill, dim3((unsigned)(bh * P.nb)), dim3(64), 0, st, P);
+  hipLaunchKernelGGL(k_block_fill, dim3((unsigned)(bh * ((P.nb + FILL_WAVES - 1) / FILL_WAVES))), dim3(64 * FILL_WAVES), 0,
+                     st, P);
   const int64_t work = bh * P.max_items;
   // two key tiles a wave where their gradients fit the registers
   constexpr int KTW = sizeof(T) == 2 && DKP + DVP <= 128 ? 2 : 1;

@@ -315,6 +315,57 @@ def test_steps(hq, hkv, dk, dv, block, dtype):
     assert bool((out == 0).all()) and torch.equal(k.nan_to_num(), before)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("blocks", [129, 700])
+def test_steps_over_long_caches(blocks, dtype):
+    """More blocks than one workgroup scores, and than one piece of the choice holds; equal blocks, which go to the
+    lower index, and positions outside."""
+    torch = _torch()
+    cfg = _cfg(6, 2, 64, 64, 32, 9, dtype=dtype)
+    B, S = 6, 32 * blocks - 3
+    op, t = _op(cfg), _inputs(cfg, B, 1, S, 22)
+    k, v = t["k"], t["v"]
+    k[2, :] = k[2, :32].repeat(blocks, 1, 1)[:S]  # the same mean in every block
+    k[3, 32 * 64:] = k[3, 32 * 64:32 * 65].repeat(blocks, 1, 1)[:S - 32 * 64]
+    pos = np.array([S - 1, 32 * 128 - 1, S - 2, S - 40, -1, 31])
+    row, at = torch.arange(B, device="cuda"), _i32(np.maximum(pos, 0)).long()
+    q, kt, vt = t["q"][:, 0].contiguous(), k[row, at], v[row, at]
+    means = op.means(k, _i32(np.maximum(pos, 0)))
+    want_means = op.means(k, _i32(pos + 1))
+    sel = ref.select(_host(q)[:, None], _host(want_means), cfg, S, pos)
+    want, bound, _ = ref.forward(_host(q)[:, None], _host(k), _host(v), sel, cfg, pos)
+    k0, v0 = k.clone(), v.clone()
+    out = op.step(q, kt, vt, k, v, means, _i32(pos))
+    _check("out", out, want["out"][:, 0], bound["out"][:, 0])
+    assert bool((out[4] == 0).all()) and torch.equal(k, k0) and torch.equal(v, v0)
+    assert torch.equal(means, want_means)
+
+
+def test_more_blocks_than_shared_tiles_hold():
+    """A cache of so many blocks that tiles do not share them, against its part that the selection names."""
+    torch = _torch()
+    cfg = _cfg(16, 1, 64, 64, 32, 6)
+    B, L, S = 1, 131, 32 * 16385
+    op, t = _op(cfg), _inputs(cfg, B, L, S, 23)
+    rng = np.random.default_rng(24)
+    sel = np.sort(np.stack([rng.permutation(8)[:6] for _ in range(L)]))[None, None]
+    start = _i32([S - L])
+    out, lse = op.forward(t["q"], t["k"], t["v"], _i32(sel), start)
+    grads = op.backward(t["q"], t["k"], t["v"], _i32(sel), out, lse, t["dout"], start)
+    # every query by itself, at the last position of the eight blocks
+    q, do = (_host(t[n])[0][:, None] for n in ("q", "dout"))
+    k, v = (np.repeat(_host(t[n][:, :256]), L, axis=0) for n in "kv")
+    last, rows = np.full(L, 255), np.moveaxis(sel[0], 1, 0)[:, :, None]
+    want, bound, _ = ref.forward(q, k, v, rows, cfg, last)
+    _check("out", out[0][:, None], want["out"], bound["out"])
+    _check("lse", lse[0].t()[:, :, None], want["lse"], bound["lse"])
+    want, bound = ref.backward(q, k, v, rows, do, cfg, last)
+    _check("dq", grads[0][0][:, None], want["dq"], bound["dq"])
+    for name, g in zip(("dk", "dv"), grads[1:]):
+        _check(name, g[0, :256], want[name].sum(0), bound[name].sum(0))
+        assert bool((g[0, 256:] == 0).all())
+
+
 def test_means_of_a_growing_cache():
     torch = _torch()
     cfg = _cfg(4, 2, 64, 64, 32, 4)

@@ -291,6 +291,41 @@ def test_another_stream():
         assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
 
 
+@pytest.mark.parametrize("L,D", [(5, 64), (700, 96), (2000, 130)])
+def test_two_streams_at_once(L, D):
+    """Training passes of different inputs, interleaved on two streams, against each alone."""
+    torch = _torch()
+    op = _handle(RecurrenceConfig(D, "norm", 16.0, "f32"))
+    sets = [{n: t.cuda() for n, t in _inputs(3, L, D, "f32", seed, "holes").items()} for seed in (30, 31)]
+
+    def call(d):
+        y, h = op.forward(d["x"], d["z"], d["bias"], d["mask"], d["h_in"])
+        return [y, h, *op.backward(d["x"], d["z"], d["x"], d["bias"], d["mask"], d["h_in"], h)]
+
+    want = [call(d) for d in sets]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in sets], []
+    for _ in range(5):
+        for s, d, w in zip(streams, sets, want):
+            with torch.cuda.stream(s):
+                got.append((call(d), w))
+    torch.cuda.synchronize()
+    for g, w in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, w))
+
+
+@pytest.mark.parametrize("gamma", [1e-6, 1e6])
+@pytest.mark.parametrize("mode", ["plain", "convex", "norm"])
+def test_the_ends_of_the_normalizers_range(gamma, mode):
+    """Gates that forget all, or nothing: results and gradients are numbers."""
+    torch = _torch()
+    op = _handle(RecurrenceConfig(64, mode, gamma, "f32"))
+    d = {n: t.cuda() for n, t in _inputs(2, 300, 64, "f32", 32, "holes").items()}
+    y, h = op.forward(d["x"], d["z"], d["bias"], d["mask"], d["h_in"])
+    for t in (y, h, *op.backward(d["x"], d["z"], d["x"], d["bias"], d["mask"], d["h_in"], h)):
+        assert bool(t.isfinite().all())
+
+
 def test_refusals():
     torch = _torch()
     op = _handle(RecurrenceConfig(64, "norm", 16.0, "bf16"))

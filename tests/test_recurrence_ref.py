@@ -109,6 +109,17 @@ def test_configuration_class_refuses(kw):
         RecurrenceConfig(**{"width": 64, **kw})
 
 
+@pytest.mark.parametrize("gamma", [9e-7, 1.1e6, 1e-30, 3e38])
+def test_gate_normalizers_out_of_range(gamma):
+    with pytest.raises(ValueError, match="gate_normalizer"):
+        RecurrenceConfig(64, gate_normalizer=gamma)
+    assert binding.load_library().msgla_recurrence_workspace_bytes(ctypes.byref(_raw(gate_normalizer=gamma)), 1, 8) == BAD_SIZE
+    for fine in (1e-6, 1e6):
+        RecurrenceConfig(64, gate_normalizer=fine)
+        assert binding.load_library().msgla_recurrence_workspace_bytes(ctypes.byref(_raw(gate_normalizer=fine)), 1,
+                                                                       8) != BAD_SIZE
+
+
 def test_handle_refuses_host_tensors():
     import torch
     from scale_gla_layer_amd.runner import DeviceRecurrence
