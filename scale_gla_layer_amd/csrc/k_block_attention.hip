@@ -2,10 +2,13 @@
 // the queries.  o = softmax(scale q K^T) V over the keys at or before the query
 // in its blocks, by one pass with a running maximum and sum.
 //
-// One wave takes a tile of 16 rows and walks the union of its queries' blocks,
-// 32 keys a step; a row that has not chosen a block is masked there.  Where
-// there are few tiles (decoding), a tile's blocks are dealt to several waves
-// whose partial outputs a second kernel joins.
+// For single queries, for a few over long sequences, and for more blocks than the
+// kernel of shared tiles holds.  One wave takes a tile of 16 rows and walks the
+// union of its queries' blocks, 32 keys a step; a row that has not chosen a block
+// is masked there.  A tile's blocks are dealt to several waves, whose partial
+// outputs a second kernel joins.  Bound by the latency of a wave's chain of loads,
+// hence the many parts: single queries of 16 sequences, 16 / 4 heads of 128, 16
+// blocks of 64 keys take 15 us for 34 MB, and the join 7.
 #include "block_device.hpp"
 
 namespace msgla {
@@ -205,9 +208,10 @@ template <typename T, int DVP> __global__ __launch_bounds__(64) void k_block_joi
 }
 
 // dq = scale sum_j p_j (do . v_j - delta) k_j, by the tiles, steps and parts of
-// the forward; delta = do . o is the softmax's share.  For bf16 the weights' gradients go through the product as a sum
-// of two bf16 values, and delta, which comes from the rounded output, is put
-// right: with e = sum_j p_j (do . v_j - delta), its error (the weights sum to 1),
+// the forward; delta = do . o is the softmax's share.  For bf16 the weights'
+// gradients go through the product as a sum of two bf16 values, and delta, which
+// comes from the rounded output, is put right (without both, dq is off by 1.6
+// times its own rounding): with e = sum_j p_j (do . v_j - delta), its error (the weights sum to 1),
 // dq loses scale e sum_j p_j k_j, and delta + e is what dk and dv then use.
 template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_block_dq(const BlkParams P) {
   constexpr bool EXACT = sizeof(T) == 2;

@@ -7,11 +7,16 @@
 // one of two LDS stages while the other is worked on, 32 rows for each group of
 // waves that together hold all keys.  With KTW = 2 every row that a wave reads
 // from LDS meets 32 keys, which is what LDS and the matrix cores take equal time
-// for; two groups of waves then take different rows and add up at the end.  The lists of those queries come from a bit
-// matrix (block x query) that is written without regard to order and read in
-// order, so no sum's order varies.  A block that many queries chose (the first
-// one) is cut into work items of `seg` queries, whose partial gradients a last
-// kernel adds in order.
+// for; two groups of waves then take different rows and add up at the end.
+//   The lists of those queries come from a bit matrix (block x query) that is
+// written without regard to order and read in order, so no sum's order varies.  A
+// block that many queries chose (the first one) is cut into work items of `seg`
+// queries, whose partial gradients a last kernel adds in order.
+//   Bound by LDS and matrix instructions in turn, at two or three waves a SIMD
+// (one for fp32 heads of more than 256 elements in sum, which would spill: 3.1 ms
+// against 4.4 at B = 2, L = 4096, 16 / 4 heads of 128 and 256).  At B = 2, L =
+// 4096, 16 / 4 heads of 128 in bf16: 241 us for 117 GFLOP, the lists 14, the
+// joining 24.
 #include "block_stage.hpp"
 
 namespace msgla {
@@ -45,8 +50,10 @@ __global__ __launch_bounds__(256) void k_block_bits(const BlkParams P) {
 
 // A wave writes one block's queries in order, and where its list, its work items
 // and its partials begin: sums over the blocks before it, which FILL_WAVES
-// neighbours form together.
-constexpr int FILL_WAVES = 16;
+// neighbours form together (more would write their lists on one CU: 16 take 21 us
+// at B = 2, L = 4096, 16 / 4 heads, 4 take 10, and by itself each takes 8 but reads
+// four times the counts, which is felt from some ten thousand blocks on).
+constexpr int FILL_WAVES = 4;
 
 __global__ __launch_bounds__(64 * FILL_WAVES) void k_block_fill(const BlkParams P) {
   __shared__ int sums[FILL_WAVES][3];

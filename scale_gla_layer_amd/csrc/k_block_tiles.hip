@@ -392,6 +392,10 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
   return hipGetLastError();
 }
 
+// A workgroup of 15 tiles has a CU to itself, two of 3 share one.  15 share keys
+// among more, but need 4096 tiles to fill the chip (forward of 8 / 2 heads of 64
+// with 3 and 15: 2048 tiles 33 and 36 us, 3500 tiles 66 and 48; of 16 / 4 heads of
+// 128: 1024 tiles 18 and 28, 3500 tiles 70 and 70, 8192 in fp32 1.26 and 1.08 ms).
 // 15 tiles leave 128 registers a wave, 3 leave 256.  Units of 64 keys fit the
 // first in the forward at d_v up to 128 (227 us at B = 8, L = 2048, 16 / 4 heads
 // of 128, against 233 with 32 keys and 279 with 7 tiles of 64); elsewhere they

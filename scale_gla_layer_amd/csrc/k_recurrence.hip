@@ -23,7 +23,9 @@
 // leaves every chunk's entry state, then the chunks from the last to the first.
 // Bound by HBM and, nearly as much, by the gate's arithmetic (about 45 vector
 // instruction slots an element with NORM), which is why it is worth reading and
-// evaluating once.
+// evaluating once.  B = 8, L = 2048, D = 1024 in bf16: forward 36 us (2.8 TB/s; a
+// copy of the bytes takes 20), backward 93 (33); in three passes with the maps
+// joined between them they took 77 and 286.
 #include <type_traits>
 
 #include "device_common.hpp"
