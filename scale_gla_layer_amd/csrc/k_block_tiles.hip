@@ -1,7 +1,7 @@
 // Attention over selected blocks for many queries: forward and the gradient of
 // the queries with keys and values shared by a workgroup.
 //
-// A workgroup takes 15 (or 3) neighbouring tiles of 16 (query, head) rows, one
+// A workgroup takes 15 (or 11, or 3) neighbouring tiles of 16 (query, head) rows, one
 // a wave, and walks the union of all its queries' blocks in ascending order, KT
 // keys a unit.  One more wave copies each unit's keys and values once,
 // asynchronously, into a ring of LDS stages; the tiles' waves work on the units
@@ -126,12 +126,12 @@ __device__ __forceinline__ void fill_ring(const BlkParams& P, Ring* ring, char* 
 }
 
 template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD>
-__global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : 2) void k_block_tiles(const BlkParams P, int stages) {
+__global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : WAVES == 11 ? 3 : 2) void k_block_tiles(const BlkParams P, int stages) {
   constexpr int ES = sizeof(T), WK = DKP * ES / 16, WV = DVP * ES / 16;
   constexpr int NK = DKP * ES / 64, NV = DVP * ES / 64, KEY_T = KT / 16, SLABS = KT / blk_slab<T>();
   constexpr int KB = KT * WK * 16, STAGE = KB + KT * WV * 16, NT = WAVES, THREADS = 64 * (WAVES + 1);
   constexpr int OUT = GRAD ? DKP : DVP;  // width of the accumulated rows
-  constexpr bool EXACT = GRAD && ES == 2 && WAVES < TILE_WAVES_MAX;  // delta put right (15 tiles leave no registers for it)
+  constexpr bool EXACT = GRAD && ES == 2 && WAVES == 3;  // delta put right (more tiles leave no registers for it)
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int words = (P.nb + 31) / 32, pitch = P.n + 1;
   __shared__ int slast;
@@ -374,7 +374,7 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
   constexpr int STAGE = KT * (DKP + DVP) * (int)sizeof(T), NT = WAVES;
   const int qn = P.GT > 1 ? NT / P.GT + 2 : NT * P.QT;
   const int rest = (NT + 1) * ((P.nb + 31) / 32 * 4) + qn * (P.n + 1) * 2 + 1024;
-  constexpr int LDS = (WAVES == TILE_WAVES_MAX ? 160 : 80) * 1024;  // of one workgroup on a CU, or two
+  constexpr int LDS = (WAVES > 3 ? 160 : 80) * 1024;  // of one workgroup on a CU, or two
   constexpr int MOST = (NT + 1) * (BLK_TILES_MAX / 8) + NT * BLK_ROWS * (BLK_MAX_SEL + 1) * 2 + 1024;
   static_assert((LDS - MOST) / STAGE >= MIN_STAGES && std::min((LDS - MOST) / STAGE, 8) * STAGE >= NT * BLK_ROWS * BLK_MAX_SEL * 4,
                 "beside the largest maps and lists there is a ring, in which the raw selection fits");
@@ -395,20 +395,22 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
 // A workgroup of 15 tiles has a CU to itself, two of 3 share one.  15 share keys
 // among more, but need 4096 tiles to fill the chip (forward of 8 / 2 heads of 64
 // with 3 and 15: 2048 tiles 33 and 36 us, 3500 tiles 66 and 48; of 16 / 4 heads of
-// 128: 1024 tiles 18 and 28, 3500 tiles 70 and 70, 8192 in fp32 1.26 and 1.08 ms).
-// 15 tiles leave 128 registers a wave, 3 leave 256.  Units of 64 keys fit the
-// first in the forward at d_v up to 128 (227 us at B = 8, L = 2048, 16 / 4 heads
-// of 128, against 233 with 32 keys and 279 with 7 tiles of 64); elsewhere they
-// spill (d_v 256, one sequence of 16384, 8 / 2 heads: 508 us with 32 keys, 1899
-// with 64, 578 with 7 tiles of 64; gradient at B = 2, L = 4096: 246, 284, 289).
-// fp32 with wide heads takes 3 tiles for their registers.
+// 128: 1024 tiles 18 and 28, 3500 tiles 70 and 70, 8192 in fp32 1.26 and 1.08 ms;
+// gradients at 8192 tiles in bf16 606 and 505 us).
+// 15 tiles leave 128 registers a wave, 11 leave 168, 3 leave 256.  Units of 64
+// keys fit the first in the forward at d_v up to 128 (227 us at B = 8, L = 2048,
+// 16 / 4 heads of 128, against 233 with 32 keys, 234 with 11 tiles and 279 with 7);
+// in the gradient they spill (B = 2, L = 4096: 246 and 284 us), and d_v of 256
+// spills with 15 tiles (one sequence of 16384, 8 / 2 heads: forward 509 us with 15,
+// 501 with 11, backward 1207 and 1115).  fp32 with wide heads takes 3 tiles for
+// their registers.
 template <typename T, int DKP, int DVP, bool GRAD> hipError_t by_block(const BlkParams& P, hipStream_t st) {
   if (P.tiles < 4096) return launch_t<T, DKP, DVP, sizeof(T) == 4 ? 16 : 32, 3, GRAD>(P, st);
   if constexpr (sizeof(T) == 4) {
     return launch_t<T, DKP, DVP, 16, DVP == 256 || (GRAD && DKP == 128) ? 3 : 15, GRAD>(P, st);
   } else {
-    constexpr int KT = !GRAD && DVP <= 128 ? 64 : 32;
-    return P.lgT == 5 ? launch_t<T, DKP, DVP, 32, 15, GRAD>(P, st) : launch_t<T, DKP, DVP, KT, 15, GRAD>(P, st);
+    constexpr int KT = !GRAD && DVP <= 128 ? 64 : 32, TILES = DVP == 256 ? 11 : 15;
+    return P.lgT == 5 ? launch_t<T, DKP, DVP, 32, TILES, GRAD>(P, st) : launch_t<T, DKP, DVP, KT, TILES, GRAD>(P, st);
   }
 }
 template <typename T, int DKP, bool GRAD> hipError_t by_dv(const BlkParams& P, hipStream_t st) {
