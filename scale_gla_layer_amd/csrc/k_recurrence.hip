@@ -360,8 +360,11 @@ __global__ __launch_bounds__(64 * REC_WAVES) void k_rec_forward(const RecParams 
 // ---- backward --------------------------------------------------------------------
 
 // Chunks from the last to the first; P.entry holds their entry states.
+// fp32 with PLAIN would need 18 registers more than two workgroups a CU leave
+// (held to them, B = 8, L = 2048, D = 1024: 130 -> 110 us; bf16 fits by itself, and
+// held to them takes 260 us for 250 at B = 16, L = 4093).
 template <typename T, int VEC, int MODE>
-__global__ __launch_bounds__(64 * REC_BWAVES) void k_rec_backward(const RecParams P) {
+__global__ __launch_bounds__(64 * REC_BWAVES, sizeof(T) == 4 ? 2 : 1) void k_rec_backward(const RecParams P) {
   constexpr int NW = REC_BWAVES, NT = REC_NT;
   __shared__ float sA[NW][64 * VEC], sH[NW][64 * VEC], sR[NW][64 * VEC];
   __shared__ Chain<VEC, NW> chain;
