@@ -124,7 +124,9 @@ template <int MODE> __device__ __forceinline__ Gate gate(float z, float inv_gamm
   if constexpr (MODE == 1) g.beta = neg_expm1(la * LN2, g.alpha);
   if constexpr (MODE == 2) {
     const float b2 = neg_expm1(la * (2.f * LN2), g.alpha * g.alpha);
-    g.rbeta = __builtin_amdgcn_rsqf(b2);
+    // b2 runs out of normal numbers before it is 0 (z + b from 74 to 87 at a gamma of 1e6),
+    // and the hardware's root takes those for 0: scaled by an even power of two
+    g.rbeta = 0x1p12f * __builtin_amdgcn_rsqf(0x1p24f * b2);
     g.beta = b2 == 0.f ? 0.f : b2 * g.rbeta;
   }
   return g;
