@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "block_plan.hpp"
+
 namespace msgla {
 
 struct BlkHeads {
@@ -11,9 +13,7 @@ struct BlkHeads {
   int64_t sb, st, sh;  // a sequence, a position, a head
 };
 
-constexpr int BLK_ROWS = 16;     // (query, head) rows of a tile: one MFMA tile
 constexpr int BLK_KEYS = 32;     // keys of a step
-constexpr int BLK_MAX_SEL = 64;  // largest n_select
 constexpr int BLK_PIECE = 256;   // blocks whose scores are in LDS at once
 
 struct BlkParams {
@@ -58,7 +58,6 @@ inline bool blk_step_spread(const BlkParams& P) { return P.nb > BLK_STEP_ONE; }
 hipError_t launch_block_step(const BlkParams& P, bool bf16_path, hipStream_t st);
 hipError_t launch_block_forward(const BlkParams& P, bool bf16_path, hipStream_t st);
 // many queries: keys and values shared by a workgroup; nb at most BLK_TILES_MAX
-constexpr int BLK_TILES_MAX = 16384;
 hipError_t launch_block_tiles(const BlkParams& P, bool gradient, bool bf16_path, hipStream_t st);
 hipError_t launch_block_dq(const BlkParams& P, bool bf16_path, hipStream_t st);
 hipError_t launch_block_dkdv(const BlkParams& P, bool bf16_path, hipStream_t st);

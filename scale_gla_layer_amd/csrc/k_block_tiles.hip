@@ -136,6 +136,7 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : WAV
   const int words = (P.nb + 31) / 32, pitch = P.n + 1;
   __shared__ int slast;
   __shared__ Ring ring;
+  static_assert(sizeof(Ring) + sizeof(int) <= 128, "in TILE_STATIC, with room to align");
   const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, a = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Work in order of length, the last tiles, which have the most blocks, first;
@@ -371,15 +372,14 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : WAV
 }
 
 template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t launch_t(const BlkParams& P, hipStream_t st) {
-  constexpr int STAGE = KT * (DKP + DVP) * (int)sizeof(T), NT = WAVES;
-  const int qn = P.GT > 1 ? NT / P.GT + 2 : NT * P.QT;
-  const int rest = (NT + 1) * ((P.nb + 31) / 32 * 4) + qn * (P.n + 1) * 2 + 1024;
-  constexpr int LDS = (WAVES > 3 ? 160 : 80) * 1024;  // of one workgroup on a CU, or two
-  constexpr int MOST = (NT + 1) * (BLK_TILES_MAX / 8) + NT * BLK_ROWS * (BLK_MAX_SEL + 1) * 2 + 1024;
-  static_assert((LDS - MOST) / STAGE >= MIN_STAGES && std::min((LDS - MOST) / STAGE, 8) * STAGE >= NT * BLK_ROWS * BLK_MAX_SEL * 4,
+  constexpr int ES = sizeof(T), NT = WAVES, LIMIT = tile_lds_limit(WAVES);
+  constexpr TileShape SHAPE = {KT, WAVES};
+  constexpr int STAGE = tile_stage(SHAPE, ES, DKP, DVP);
+  constexpr int MOST = (NT + 1) * (BLK_TILES_MAX / 8) + NT * BLK_ROWS * (BLK_MAX_SEL + 1) * 2 + TILE_STATIC;
+  static_assert((LIMIT - MOST) / STAGE >= MIN_STAGES && std::min((LIMIT - MOST) / STAGE, 8) * STAGE >= NT * BLK_ROWS * BLK_MAX_SEL * 4,
                 "beside the largest maps and lists there is a ring, in which the raw selection fits");
-  const int stages = std::min((LDS - rest) / STAGE, 8);
-  const int lds = stages * STAGE + rest;
+  const TileLds plan = tile_lds(SHAPE, STAGE, P.nb, P.n, P.QT, P.GT);
+  const int stages = plan.stages, lds = plan.bytes;
   const auto kernel = &k_block_tiles<T, DKP, DVP, KT, WAVES, GRAD>;
   if (lds > 64 * 1024) {
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -392,26 +392,13 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
   return hipGetLastError();
 }
 
-// A workgroup of 15 tiles has a CU to itself, two of 3 share one.  15 share keys
-// among more, but need 4096 tiles to fill the chip (forward of 8 / 2 heads of 64
-// with 3 and 15: 2048 tiles 33 and 36 us, 3500 tiles 66 and 48; of 16 / 4 heads of
-// 128: 1024 tiles 18 and 28, 3500 tiles 70 and 70, 8192 in fp32 1.26 and 1.08 ms;
-// gradients at 8192 tiles in bf16 606 and 505 us).
-// 15 tiles leave 128 registers a wave, 11 leave 168, 3 leave 256.  Units of 64
-// keys fit the first in the forward at d_v up to 128 (227 us at B = 8, L = 2048,
-// 16 / 4 heads of 128, against 233 with 32 keys, 234 with 11 tiles and 279 with 7);
-// in the gradient they spill (B = 2, L = 4096: 246 and 284 us), and d_v of 256
-// spills with 15 tiles (one sequence of 16384, 8 / 2 heads: forward 509 us with 15,
-// 501 with 11, backward 1207 and 1115).  fp32 with wide heads takes 3 tiles for
-// their registers.
 template <typename T, int DKP, int DVP, bool GRAD> hipError_t by_block(const BlkParams& P, hipStream_t st) {
-  if (P.tiles < 4096) return launch_t<T, DKP, DVP, sizeof(T) == 4 ? 16 : 32, 3, GRAD>(P, st);
-  if constexpr (sizeof(T) == 4) {
-    return launch_t<T, DKP, DVP, 16, DVP == 256 || (GRAD && DKP == 128) ? 3 : 15, GRAD>(P, st);
-  } else {
-    constexpr int KT = !GRAD && DVP <= 128 ? 64 : 32, TILES = DVP == 256 ? 11 : 15;
-    return P.lgT == 5 ? launch_t<T, DKP, DVP, 32, TILES, GRAD>(P, st) : launch_t<T, DKP, DVP, KT, TILES, GRAD>(P, st);
-  }
+  constexpr int ES = sizeof(T);
+  constexpr TileShape FEW = tile_shape(ES, DKP, DVP, GRAD, 32, false), SHORT = tile_shape(ES, DKP, DVP, GRAD, 32, true),
+                      LONG = tile_shape(ES, DKP, DVP, GRAD, 64, true);
+  if (P.tiles < BLK_TILES_MANY) return launch_t<T, DKP, DVP, FEW.keys, FEW.tiles, GRAD>(P, st);
+  return P.lgT == 5 ? launch_t<T, DKP, DVP, SHORT.keys, SHORT.tiles, GRAD>(P, st)
+                    : launch_t<T, DKP, DVP, LONG.keys, LONG.tiles, GRAD>(P, st);
 }
 template <typename T, int DKP, bool GRAD> hipError_t by_dv(const BlkParams& P, hipStream_t st) {
   if (blk_dvp(P.dvw) == 64) return by_block<T, DKP, 64, GRAD>(P, st);

@@ -1,0 +1,40 @@
+"""GPU: block selection and attention at the ends of what their launches and documents allow."""
+import numpy as np
+import pytest
+
+from scale_gla_layer_amd.config import BlockAttentionConfig
+from tests import block_ref as ref
+from tests.test_gpu_block_attention import _check, _host, _i32, _inputs, _op
+from tests.gpu_cases import say
+
+pytestmark = pytest.mark.gpu
+
+
+def _torch():
+    import torch
+    return torch
+
+
+@pytest.mark.parametrize("dtype,d,grad", [("bf16", 64, False), ("bf16", 128, True), ("f32", 128, False)])
+def test_the_longest_lists_of_the_largest_workgroups(dtype, d, grad):
+    """A head of queries for each of keys, 64 of 256 blocks chosen, 4096 tiles: maps and lists leave the ring
+    of key stages not a byte more than the compute unit has."""
+    torch = _torch()
+    H, L, T, n = 4, 16384, 64, 64
+    cfg = BlockAttentionConfig(H, H, d, d, T, n, 1, 2, None, dtype)
+    say(f"longest lists {dtype} {d}")
+    op, t = _op(cfg), _inputs(cfg, 1, L, L, 41)
+    sel = op.select(t["q"], op.means(t["k"]))
+    out, lse = op.forward(t["q"], t["k"], t["v"], sel)
+    rows = np.array([0, T - 1, 4097, 9000, L - T, L - 1])  # each as a sequence of one query
+    q, do = (_host(t[x])[0, rows][:, None] for x in ("q", "dout"))
+    k, v = (np.repeat(_host(t[x]), len(rows), axis=0) for x in "kv")
+    chosen = np.moveaxis(sel.cpu().numpy()[0][:, rows], 1, 0)[:, :, None]
+    want, bound, _ = ref.forward(q, k, v, chosen, cfg, rows)
+    _check("out", out[0, rows][:, None], want["out"], bound["out"])
+    _check("lse", lse[0][:, rows].t()[:, :, None], want["lse"], bound["lse"])
+    if grad:
+        dq, dk, dv = op.backward(t["q"], t["k"], t["v"], sel, out, lse, t["dout"])
+        want, bound = ref.backward(q, k, v, chosen, do, cfg, rows)
+        _check("dq", dq[0, rows][:, None], want["dq"], bound["dq"])
+        assert bool(dk.isfinite().all()) and bool(dv.isfinite().all())
