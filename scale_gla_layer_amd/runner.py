@@ -305,15 +305,17 @@ class DeviceBlockAttention:
         binding.msgla_block_means(self.cfg, k, means, lens, start_from)
         return means
 
-    def select(self, q, means, start=None, lens=None, sel=None):
-        """The blocks of every query of q [B, L, heads_q, d_k]: [B, heads_kv, L, n_select] int32."""
-        return _on(q, self._select, q, means, start, lens, sel)
+    def select(self, q, means, start=None, lens=None, sel=None, S=None):
+        """The blocks of every query of q [B, L, heads_q, d_k]: [B, heads_kv, L, n_select] int32.  S: the number of
+        positions that k has, where the last block is not whole (None: all of its positions are)."""
+        return _on(q, self._select, q, means, start, lens, sel, S)
 
-    def _select(self, q, means, start, lens, sel):
+    def _select(self, q, means, start, lens, sel, S):
         torch = _torch()
         if sel is None:
             sel = q.new_empty((q.shape[0], self.cfg.heads_kv, q.shape[1], self.cfg.n_select), dtype=torch.int32)
-        binding.msgla_block_select(self.cfg, q, means, means.shape[2] * self.cfg.block, sel, start, lens)
+        binding.msgla_block_select(self.cfg, q, means, means.shape[2] * self.cfg.block if S is None else S, sel, start,
+                                   lens)
         return sel
 
     def forward(self, q, k, v, sel, start=None, lens=None, out=None, lse=None):

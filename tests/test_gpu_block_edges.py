@@ -38,3 +38,19 @@ def test_the_longest_lists_of_the_largest_workgroups(dtype, d, grad):
         want, bound = ref.backward(q, k, v, chosen, do, cfg, rows)
         _check("dq", dq[0, rows][:, None], want["dq"], bound["dq"])
         assert bool(dk.isfinite().all()) and bool(dv.isfinite().all())
+
+
+def test_a_chunk_that_runs_past_the_cache():
+    """Rows behind a cache whose last block is not whole select nothing, as the attention leaves them out."""
+    cfg = BlockAttentionConfig(8, 2, 64, 64, 64, 4)
+    B, L, S, start = 3, 40, 700, [690, 660, 699]
+    op, t = _op(cfg), _inputs(cfg, B, L, S, 42)
+    means = op.means(t["k"])
+    sel = op.select(t["q"], means, _i32(start), S=S)
+    assert np.array_equal(sel.cpu().numpy(), ref.select(_host(t["q"]), _host(means), cfg, S, start))
+    out, lse = op.forward(t["q"], t["k"], t["v"], sel, _i32(start))
+    behind = _torch().tensor(ref.positions(B, L, S, start) < 0).cuda()
+    assert behind.sum() == 30 + 39 and bool((sel.transpose(1, 2)[behind] == -1).all())
+    assert bool((out[behind] == 0).all()) and bool((lse.transpose(1, 2)[behind] == -float("inf")).all())
+    with pytest.raises(ValueError):
+        op.select(t["q"], means, _i32(start), S=S + 64)
