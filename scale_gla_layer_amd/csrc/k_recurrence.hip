@@ -200,13 +200,20 @@ template <int NT> __device__ __forceinline__ uint32_t tokens(const RecParams& P,
   return (uint32_t)__ballot(in && (!P.mask || P.mask[(int64_t)b * P.L + (in ? t : 0)]));
 }
 
-// What enters the sequence, for the chunks of the first group.  Read before the
-// workgroup publishes its map: the chunk that writes the sequence's result, which
-// may go to the same memory, has waited for all of these.
+// What enters the sequence, for the chunks of the first group.
 template <int VEC> __device__ __forceinline__ void load_begin(const float* p, int64_t at, int step, float* begin) {
 #pragma unroll
   for (int e = 0; e < VEC; ++e) begin[e] = 0.f;
   if (p && step < REC_GROUP) load_f32<VEC>(p + at, begin);
+}
+
+// Before the barrier that a workgroup publishes its map behind: the chunk that writes
+// the sequence's result, which may go to the same memory, waits for the maps of all
+// chunks that read what enters.  The barrier itself does not wait for loads; a use of
+// the values does.
+template <int VEC> __device__ __forceinline__ void have_begin(float* begin) {
+#pragma unroll
+  for (int e = 0; e < VEC; ++e) asm volatile("" : "+v"(begin[e])::"memory");
 }
 
 // The value that enters chunk `step` of the chain: the state at the last group
@@ -293,8 +300,8 @@ __global__ __launch_bounds__(64 * REC_WAVES) void k_rec_forward(const RecParams 
     else walk(std::false_type());
   }
   float state[VEC], begin[VEC];
-  const int64_t seq = (int64_t)at.b * P.D + at.cl;
-  load_begin<VEC>(P.h_in, seq, at.step, begin);
+  load_begin<VEC>(P.h_in, (int64_t)at.b * P.D + at.cl, at.step, begin);
+  have_begin<VEC>(begin);
   uint64_t* maps = P.maps + (int64_t)at.b * P.nch * P.D;
   uint64_t* ends = P.ends + (int64_t)at.b * P.groups * P.D;
 #pragma unroll
@@ -429,6 +436,7 @@ __global__ __launch_bounds__(64 * REC_BWAVES, sizeof(T) == 4 ? 2 : 1) void k_rec
   }
   float carry[VEC], begin[VEC];
   load_begin<VEC>(P.dh_out, seq, at.step, begin);
+  have_begin<VEC>(begin);
   uint64_t* maps = P.rmaps + (int64_t)at.b * P.nchb * P.D;
   uint64_t* ends = P.rends + (int64_t)at.b * P.groupsb * P.D;
   if (P.nchb == 1) {
