@@ -389,7 +389,9 @@ msgla_status msgla_backward_saved(const msgla_config* cfg, const void* packed, c
  * A model of MS-GLA layers needs other mixers of the sequence next to them.
  * Those below keep the layer's conventions (device pointers, caller-owned
  * memory, work enqueued on `stream`, argument errors returned synchronously)
- * and its two storage types; they take no packed weights.
+ * and its two storage types; they take no packed weights.  Sizes within the
+ * limits below whose launch would not fit 2^32 threads (B * L * heads of the
+ * order of 2^28) return MSGLA_ERR_UNSUPPORTED, before anything is enqueued.
  */
 
 /* Rows of a tensor [B][L][width] whose elements are contiguous within a row:

@@ -9,7 +9,6 @@ using namespace msgla::host;
 namespace {
 
 constexpr size_t BAD = (size_t)-1;
-constexpr int64_t MAX_GRID = 0x7fffffff;
 
 bool blk_config_ok(const msgla_block_config* c) {
   if (!c || (c->dtype != MSGLA_F32 && c->dtype != MSGLA_BF16)) return false;
@@ -156,16 +155,19 @@ BwdWs bwd_ws(const BlkParams& P) {
   return w;
 }
 
-bool fwd_grid_ok(const BlkParams& P, int parts) {
-  return P.tiles * BLK_ROWS <= MAX_GRID && P.tiles * parts <= MAX_GRID;
-}
-bool select_grid_ok(const BlkParams& P) {
-  return (int64_t)P.B * P.Hkv * cdiv(P.L, 16) <= MAX_GRID && (int64_t)P.B * P.Hkv * P.nb <= MAX_GRID;
+// The launches of an operator (the step's attention is the forward's).
+bool means_grid_ok(const BlkParams& P) { return launch_ok((int64_t)P.B * P.Hkv * P.nb, 64); }
+bool select_grid_ok(const BlkParams& P) { return launch_ok((int64_t)P.B * P.Hkv * cdiv(P.L, 16), 256); }
+bool step_grid_ok(const BlkParams& P) { return launch_ok((int64_t)P.B * P.Hkv, 512); }
+bool tiles_grid_ok(const BlkParams& P, int es, bool gradient, int parts) {
+  if (!use_tiles(P)) return launch_ok(P.tiles * std::max(parts, parts > 1 ? BLK_ROWS : 1), 64);
+  const TileShape s = tile_shape(es, blk_dkp(P.dkw), blk_dvp(P.dvw), gradient, 1 << P.lgT, P.tiles >= BLK_TILES_MANY);
+  return launch_ok(tile_grid(s.tiles, P.tiles_per_seq, (int64_t)P.B * P.Hkv), 64 * (s.tiles + 1));
 }
 bool bwd_grid_ok(const BlkParams& P, const BwdWs& w) {
   const int64_t bh = (int64_t)P.B * P.Hkv;
-  return bh <= 65535 && bh * P.nb <= MAX_GRID && bh * w.W <= MAX_GRID && (bh * w.max_items) << 1 <= MAX_GRID &&
-         (int64_t)P.B * P.Hq * P.L <= 16 * (MAX_GRID - 1) && P.nb <= 65535 * 64;
+  return bh <= 65535 && launch_ok(bh * P.nb, 256) && launch_ok(bh * w.W, 256) &&
+         launch_ok(bh * w.max_items << (P.lgT > 6 ? 1 : 0), P.lgT == 5 ? 128 : 256);
 }
 
 }  // namespace
@@ -193,7 +195,7 @@ msgla_status msgla_block_means(const msgla_block_config* cfg, const msgla_heads*
   const int es = es_of(cfg);
   if (!heads_ok(k, es) || !means || !aligned16(means) || !i32_ok(lens) || !i32_ok(from)) return MSGLA_ERR_INVALID_ARG;
   BlkParams P = blk_params(cfg, B, 1, S);
-  if (!select_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
+  if (!means_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   P.k = heads_of(k, es);
   P.lens = lens;
   P.from = from;
@@ -234,7 +236,7 @@ msgla_status msgla_block_attention(const msgla_block_config* cfg, const msgla_he
   const FwdWs w = fwd_ws(P);
   if (w.total && (!workspace || !aligned16(workspace))) return MSGLA_ERR_INVALID_ARG;
   if (workspace_bytes < w.total) return MSGLA_ERR_WORKSPACE;
-  if (!fwd_grid_ok(P, w.parts)) return MSGLA_ERR_UNSUPPORTED;
+  if (!tiles_grid_ok(P, es, false, w.parts)) return MSGLA_ERR_UNSUPPORTED;
   P.q = heads_of(q, es);
   P.k = heads_of(k, es);
   P.v = heads_of(v, es);
@@ -268,7 +270,7 @@ msgla_status msgla_block_attention_backward(const msgla_block_config* cfg, const
   BlkParams P = blk_params(cfg, B, L, S);
   const BwdWs w = bwd_ws(P);
   if (workspace_bytes < w.total) return MSGLA_ERR_WORKSPACE;
-  if (!fwd_grid_ok(P, w.parts) || !bwd_grid_ok(P, w)) return MSGLA_ERR_UNSUPPORTED;
+  if (!tiles_grid_ok(P, es, true, w.parts) || !bwd_grid_ok(P, w)) return MSGLA_ERR_UNSUPPORTED;
   P.q = heads_of(q, es);
   P.k = heads_of(k, es);
   P.v = heads_of(v, es);
@@ -323,7 +325,7 @@ msgla_status msgla_block_attention_step(const msgla_block_config* cfg, const msg
   const StepWs s = step_ws(P);
   const FwdWs& w = s.fwd;
   if (workspace_bytes < w.total) return MSGLA_ERR_WORKSPACE;
-  if (!fwd_grid_ok(P, w.parts) || !select_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
+  if (!tiles_grid_ok(P, es, false, w.parts) || !step_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   P.q = heads_of(q_t, es);
   P.kt = heads_of(k_t, es);
   P.vt = heads_of(v_t, es);

@@ -43,6 +43,9 @@ constexpr int GEMM_TILE = 128;
 
 inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether a launch's threads fit the 32 bits that a dispatch counts them in.
+inline bool launch_ok(int64_t groups, int threads) { return groups <= (int64_t)0xffffffff / threads; }
+
 inline int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 // K1's tile schedule: every group's row tiles are split evenly over the eight

@@ -83,8 +83,14 @@ bool rows_vec(const msgla_rows* r, int es) {
 
 bool f32_vec(const void* p) { return reinterpret_cast<uintptr_t>(p) % 8 == 0; }
 
-// One workgroup takes 64 lanes' channels; the grid is one-dimensional.
-bool grid_ok(const RecParams& P) { return (int64_t)P.slabs * std::max(P.nch, P.nchb) * P.B <= 0x7fffffff; }
+// One workgroup takes 64 lanes' channels, and a chunk or (the step) a position.
+bool forward_grid_ok(const RecParams& P) {
+  return launch_ok((int64_t)P.slabs * P.nch * P.B, 64 * REC_WAVES) && launch_ok((P.words / 2 + 255) / 256, 256);
+}
+bool backward_grid_ok(const RecParams& P) {
+  return (P.nchb == 1 || forward_grid_ok(P)) && launch_ok((int64_t)P.slabs * P.nchb * P.B, 64 * REC_BWAVES);
+}
+bool step_grid_ok(const RecParams& P) { return launch_ok((int64_t)P.slabs * P.B, 64); }
 
 }  // namespace
 
@@ -126,7 +132,7 @@ msgla_status msgla_recurrence_forward(const msgla_recurrence_config* cfg, const 
   set_ws(P, w, workspace);
   P.slabs = cdiv(P.D, vec ? 128 : 64);
   P.inv_gamma = 1.0f / cfg->gate_normalizer;
-  if (!grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
+  if (!forward_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   HIP_TRY(launch_recurrence_forward(P, cfg->input, es == 2, vec, static_cast<hipStream_t>(stream)));
   return MSGLA_OK;
 }
@@ -166,7 +172,7 @@ msgla_status msgla_recurrence_backward(const msgla_recurrence_config* cfg, const
   P.D = cfg->width;
   P.slabs = cdiv(P.D, vec ? 128 : 64);
   P.inv_gamma = 1.0f / cfg->gate_normalizer;
-  if (!grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
+  if (!backward_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   HIP_TRY(launch_recurrence_backward(P, cfg->input, es == 2, vec, static_cast<hipStream_t>(stream)));
   return MSGLA_OK;
 }
@@ -199,7 +205,7 @@ msgla_status msgla_recurrence_step(const msgla_recurrence_config* cfg, const msg
   P.nch = 1;
   P.slabs = cdiv(P.D, vec ? 128 : 64);
   P.inv_gamma = 1.0f / cfg->gate_normalizer;
-  if (!grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
+  if (!step_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   HIP_TRY(launch_recurrence_step(P, cfg->input, es == 2, vec, static_cast<hipStream_t>(stream)));
   return MSGLA_OK;
 }

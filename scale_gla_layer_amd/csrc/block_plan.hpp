@@ -31,6 +31,11 @@ constexpr TileShape tile_shape(int es, int dkp, int dvp, bool gradient, int bloc
   return {!gradient && dvp <= 128 && block > 32 ? 64 : 32, dvp == 256 ? 11 : 15};
 }
 
+// Workgroups, for `heads` sequences and key-value heads: XCDs take equal numbers of those.
+constexpr long long tile_grid(int tiles, int tiles_per_seq, long long heads) {
+  return (heads >= 8 ? (heads + 7) / 8 * 8 : heads) * ((tiles_per_seq + tiles - 1) / tiles);
+}
+
 struct TileLds {
   int stages, bytes;  // of the ring; all dynamic LDS
 };

@@ -386,9 +386,8 @@ template <typename T, int DKP, int DVP, int KT, int WAVES, bool GRAD> hipError_t
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
-  const int64_t groups = (P.tiles_per_seq + NT - 1) / NT, heads = (int64_t)P.B * P.Hkv;
-  const int64_t grid = heads >= N_XCD ? (heads + N_XCD - 1) / N_XCD * N_XCD * groups : heads * groups;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * (WAVES + 1)), lds, st, P, stages);
+  static_assert(N_XCD == 8, "tile_grid's");
+  hipLaunchKernelGGL(kernel, dim3((unsigned)tile_grid(NT, P.tiles_per_seq, (int64_t)P.B * P.Hkv)), dim3(64 * (WAVES + 1)), lds, st, P, stages);
   return hipGetLastError();
 }
 
