@@ -166,7 +166,7 @@ bool tiles_grid_ok(const BlkParams& P, int es, bool gradient, int parts) {
 }
 bool bwd_grid_ok(const BlkParams& P, const BwdWs& w) {
   const int64_t bh = (int64_t)P.B * P.Hkv;
-  return bh <= 65535 && launch_ok(bh * P.nb, 256) && launch_ok(bh * w.W, 256) &&
+  return launch_ok(bh * P.nb, 256) && launch_ok(bh * w.W, 256) &&
          launch_ok(bh * w.max_items << (P.lgT > 6 ? 1 : 0), P.lgT == 5 ? 128 : 256);
 }
 

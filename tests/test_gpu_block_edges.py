@@ -54,3 +54,21 @@ def test_a_chunk_that_runs_past_the_cache():
     assert bool((out[behind] == 0).all()) and bool((lse.transpose(1, 2)[behind] == -float("inf")).all())
     with pytest.raises(ValueError):
         op.select(t["q"], means, _i32(start), S=S + 64)
+
+
+def test_gradients_of_many_short_sequences():
+    """More sequences and key-value heads than a grid's second dimension would count."""
+    torch = _torch()
+    cfg = BlockAttentionConfig(2, 2, 8, 16, 32, 1, 0, 1)
+    B, L = 40000, 2
+    op, t = _op(cfg), _inputs(cfg, B, L, L, 43)
+    sel = torch.zeros((B, 2, L, 1), dtype=torch.int32, device="cuda")
+    out, lse = op.forward(t["q"], t["k"], t["v"], sel)
+    h = {n: _host(x) for n, x in t.items()}
+    want, bound, _ = ref.forward(h["q"], h["k"], h["v"], sel.cpu().numpy(), cfg)
+    _check("out", out, want["out"], bound["out"])
+    out, lse = torch.from_numpy(want["out"]).to(out).contiguous(), torch.from_numpy(want["lse"]).to(lse).contiguous()
+    got = op.backward(t["q"], t["k"], t["v"], sel, out, lse, t["dout"])
+    want, bound = ref.backward(h["q"], h["k"], h["v"], sel.cpu().numpy(), h["dout"], cfg)
+    for name, x in zip(("dq", "dk", "dv"), got):
+        _check(name, x, want[name], bound[name])
