@@ -454,8 +454,13 @@ def _recurrence_inputs(cfg, x, z, bias, mask, h_in, dims):
                             _f32("h_in", h_in, (shape[0], cfg.width), dev))
 
 
-def _bytes(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+def _room(t, device) -> tuple:
+    """Address and bytes of a workspace, which may be None."""
+    if t is None:
+        return None, 0
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {device}: it is on {t.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def msgla_recurrence_forward(cfg: RecurrenceConfig, x, z, y, workspace, bias=None, mask=None, h_in=None, h_out=None,
@@ -465,7 +470,7 @@ def msgla_recurrence_forward(cfg: RecurrenceConfig, x, z, y, workspace, bias=Non
     shape, dt, dev, args = _recurrence_inputs(cfg, x, z, bias, mask, h_in, 3)
     st = load_library().msgla_recurrence_forward(
         c_recurrence_config(cfg), *args, shape[0], shape[1], _rows_out("y", y, shape, dt, dev),
-        _f32("h_out", h_out, (shape[0], cfg.width), dev), _ptr(workspace), _bytes(workspace), _raw_stream(stream))
+        _f32("h_out", h_out, (shape[0], cfg.width), dev), *_room(workspace, dev), _raw_stream(stream))
     _check("msgla_recurrence_forward", st)
 
 
@@ -478,7 +483,7 @@ def msgla_recurrence_backward(cfg: RecurrenceConfig, x, z, dy, dx, dz, workspace
         c_recurrence_config(cfg), *args, None if dy is None else _rows("dy", dy, shape, dt, dev),
         _f32("dh_out", dh_out, state, dev), shape[0], shape[1], _rows_out("dx", dx, shape, dt, dev),
         _rows_out("dz", dz, shape, dt, dev), _f32("dbias", dbias, (cfg.width,), dev), _f32("dh_in", dh_in, state, dev),
-        _ptr(workspace), _bytes(workspace), _raw_stream(stream))
+        *_room(workspace, dev), _raw_stream(stream))
     _check("msgla_recurrence_backward", st)
 
 
@@ -585,7 +590,7 @@ def msgla_block_attention(cfg: BlockAttentionConfig, q, k, v, sel, out, lse, wor
     B, L, S, dt, dev, args = _block_inputs(cfg, q, k, v, sel, start, lens)
     st = load_library().msgla_block_attention(
         c_block_config(cfg), *args, B, L, S, _heads_out("out", out, (B, L, cfg.heads_q, cfg.d_v), dt, dev),
-        _f32("lse", lse, (B, cfg.heads_q, L), dev), _ptr(workspace), _bytes(workspace), _raw_stream(stream))
+        _f32("lse", lse, (B, cfg.heads_q, L), dev), *_room(workspace, dev), _raw_stream(stream))
     _check("msgla_block_attention", st)
 
 
@@ -596,8 +601,8 @@ def msgla_block_attention_backward(cfg: BlockAttentionConfig, q, k, v, sel, out,
     st = load_library().msgla_block_attention_backward(
         c_block_config(cfg), *args, _heads("out", out, shape, dt, dev), _f32("lse", lse, (B, cfg.heads_q, L), dev),
         _heads("dout", dout, shape, dt, dev), B, L, S, _heads_out("dq", dq, tuple(q.shape), dt, dev),
-        _heads_out("dk", dk, tuple(k.shape), dt, dev), _heads_out("dv", dv, tuple(v.shape), dt, dev), _ptr(workspace),
-        _bytes(workspace), _raw_stream(stream))
+        _heads_out("dk", dk, tuple(k.shape), dt, dev), _heads_out("dv", dv, tuple(v.shape), dt, dev),
+        *_room(workspace, dev), _raw_stream(stream))
     _check("msgla_block_attention_backward", st)
 
 
@@ -612,5 +617,5 @@ def msgla_block_attention_step(cfg: BlockAttentionConfig, q_t, k_t, v_t, k, v, m
         _heads("v_t", v_t, (B, hkv, dv), dt, dev), _i32("pos", pos, (B,), dev), B, S,
         _heads_out("k", k, (B, S, hkv, dk), dt, dev), _heads_out("v", v, (B, S, hkv, dv), dt, dev),
         _f32("means", means, (B, hkv, block_count(cfg, S), dk), dev), _heads_out("out_t", out_t, (B, hq, dv), dt, dev),
-        _ptr(workspace), _bytes(workspace), _raw_stream(stream))
+        *_room(workspace, dev), _raw_stream(stream))
     _check("msgla_block_attention_step", st)
