@@ -55,6 +55,24 @@ template <typename T> __device__ __forceinline__ u32x4 blk_pack(const float (*p)
   }
 }
 
+// The same as a sum of two operands: with bf16 what the first one's rounding leaves
+// goes through the product as well, so that 16 bits of a weight count (fp32: lo is 0).
+template <typename T> __device__ __forceinline__ void blk_split(const float (*p)[4], int s, u32x4& hi, u32x4& lo) {
+  if constexpr (sizeof(T) == 2) {
+    const float v[8] = {p[2 * s][0], p[2 * s][1], p[2 * s][2], p[2 * s][3],
+                        p[2 * s + 1][0], p[2 * s + 1][1], p[2 * s + 1][2], p[2 * s + 1][3]};
+    split_bf16(v, hi, lo);
+  } else {
+    hi = pack16<float>(p[s]);
+    lo = zero16();
+  }
+}
+template <typename T> __device__ __forceinline__ f32x4 blk_mma_split(u32x4 a, u32x4 hi, u32x4 lo, f32x4 c) {
+  c = mma_slab<T>(a, hi, c);
+  if constexpr (sizeof(T) == 2) c = mma_slab<T>(a, lo, c);
+  return c;
+}
+
 // 16 bytes at byte offset `at` of a row of `width` bytes, zero behind its end
 __device__ __forceinline__ u32x4 blk_ld(const char* row, int at, int width) {
   return at < width ? ld16(row + at) : zero16();

@@ -85,10 +85,11 @@ template <typename T, int DKP, int DVP> struct FwdTile {
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < BLK_KEYS / blk_slab<T>(); ++s) {
-      const u32x4 x = blk_pack<T>(w, s);
+      u32x4 x, lo;
+      blk_split<T>(w, s, x, lo);
 #pragma unroll
       for (int d = 0; d < DVP / 16; ++d)
-        acc[d] = mma_slab<T>(blk_column<T>(vs, blk_pitch<T, DVP>(), s * blk_slab<T>(), d, lane), x, acc[d]);
+        acc[d] = blk_mma_split<T>(blk_column<T>(vs, blk_pitch<T, DVP>(), s * blk_slab<T>(), d, lane), x, lo, acc[d]);
     }
   }
   __device__ __forceinline__ void store(const BlkParams& P, const BlkRow& row, int64_t tile, int part, int lane) {
@@ -296,22 +297,14 @@ template <typename T, int DKP, int DVP> __global__ __launch_bounds__(64) void k_
       }
 #pragma unroll
       for (int s = 0; s < BLK_KEYS / blk_slab<T>(); ++s) {
-        u32x4 x, lo = zero16(), y = zero16();
-        if constexpr (EXACT) {
-          const float v[8] = {ds[0][0], ds[0][1], ds[0][2], ds[0][3], ds[1][0], ds[1][1], ds[1][2], ds[1][3]};
-          split_bf16(v, x, lo);
-          y = blk_pack<T>(w, s);
-        } else {
-          x = blk_pack<T>(ds, s);
-        }
+        u32x4 x, lo, y = zero16();
+        blk_split<T>(ds, s, x, lo);
+        if constexpr (EXACT) y = blk_pack<T>(w, s);
 #pragma unroll
         for (int d = 0; d < DKP / 16; ++d) {
           const u32x4 f = blk_column<T>(ks, blk_pitch<T, DKP>(), s * blk_slab<T>(), d, lane);
-          acc[d] = mma_slab<T>(f, x, acc[d]);
-          if constexpr (EXACT) {
-            acc[d] = mma_slab<T>(f, lo, acc[d]);
-            mean[d] = mma_slab<T>(f, y, mean[d]);
-          }
+          acc[d] = blk_mma_split<T>(f, x, lo, acc[d]);
+          if constexpr (EXACT) mean[d] = mma_slab<T>(f, y, mean[d]);
         }
       }
     }

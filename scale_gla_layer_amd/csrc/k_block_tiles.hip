@@ -320,15 +320,9 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : WAV
       }
 #pragma unroll
       for (int sl = 0; sl < SLABS; ++sl) {
-        u32x4 w, lo = zero16(), y = zero16();
-        if constexpr (GRAD && ES == 2) {  // what the rounding to bf16 leaves goes through the product as well
-          const float v[8] = {p[2 * sl][0], p[2 * sl][1], p[2 * sl][2], p[2 * sl][3],
-                              p[2 * sl + 1][0], p[2 * sl + 1][1], p[2 * sl + 1][2], p[2 * sl + 1][3]};
-          split_bf16(v, w, lo);
-          if constexpr (EXACT) y = blk_pack<T>(pw, sl);
-        } else {
-          w = blk_pack<T>(p, sl);
-        }
+        u32x4 w, lo, y = zero16();
+        blk_split<T>(p, sl, w, lo);
+        if constexpr (EXACT) y = blk_pack<T>(pw, sl);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // rows that have not chosen the block
           w[i] = take ? w[i] : 0u;
@@ -338,8 +332,7 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : WAV
 #pragma unroll
         for (int d = 0; d < OUT / 16; ++d) {
           const u32x4 f = col.read(GRAD ? ks : vs, sl, d);
-          acc[d] = mma_slab<T>(f, w, acc[d]);
-          if constexpr (GRAD && ES == 2) acc[d] = mma_slab<T>(f, lo, acc[d]);
+          acc[d] = blk_mma_split<T>(f, w, lo, acc[d]);
           if constexpr (EXACT) mean[d] = mma_slab<T>(f, y, mean[d]);
           // without this all reads move ahead of the products, and registers spill
           if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
