@@ -500,9 +500,9 @@ msgla_status msgla_recurrence_step(const msgla_recurrence_config* cfg, const msg
  * n_first >= 0, n_recent >= 1, n_first + n_recent <= n_select; scale 1e-30 .. 1e30
  * (1 / sqrt(d_k) as a rule).  dtype: of q, k, v, the output and their
  * gradients; bf16 inputs meet on bf16 matrix cores with fp32 sums (softmax
- * weights enter the output's product with 16 bits, as two bf16 values each, and
- * the gradients' rounded to bf16), fp32 ones on fp32 matrix cores; scores for
- * the selection are fp64 sums.
+ * weights and their gradients enter the products with 16 bits, as two bf16
+ * values each), fp32 ones on fp32 matrix cores; scores for the selection are
+ * fp64 sums.
  */
 typedef struct {
   int32_t heads_q, heads_kv;

@@ -12,11 +12,17 @@
 // written without regard to order and read in order, so no sum's order varies.  A
 // block that many queries chose (the first one) is cut into work items of `seg`
 // queries, whose partial gradients a last kernel adds in order.
-//   Bound by LDS and matrix instructions in turn, at two or three waves a SIMD
-// (one for fp32 heads of more than 256 elements in sum, which would spill: 3.1 ms
-// against 4.4 at B = 2, L = 4096, 16 / 4 heads of 128 and 256).  At B = 2, L =
-// 4096, 16 / 4 heads of 128 in bf16: 241 us for 117 GFLOP, the lists 14, the
-// joining 24.
+//   bf16 weights and their gradients enter the products as two bf16 values each
+// (blk_split): rounded once, they put dv and dk 1.4 times as far off as their own
+// rounding does, and the whole gradient takes 470 us instead of 508 at B = 2,
+// L = 4096, 16 / 4 heads of 128.
+//   Bound by LDS and matrix instructions in turn, at as many waves a SIMD as the
+// registers allow without spills to speak of.  bf16 heads of 192 elements in sum
+// and fewer: three.  Of 256 (gradient at the same size): with two 508 us, with
+// three, which spill 4 registers, 501; at blocks of 32, where three spill 22, 389
+// and 592.  Of 128 and 256: two, which spill 2 and at blocks of 32 10, 1.13 ms at
+// L = 16384 and 8 / 2 heads, one 1.43; at blocks of 32 687 and 667 us.  fp32 heads
+// of more than 256 in sum: one (3.1 ms against 4.4 with two at B = 2, L = 4096).
 #include "block_stage.hpp"
 
 namespace msgla {
@@ -133,7 +139,7 @@ __device__ __forceinline__ void gather_rows(char* lds, int width, int wave, int 
 }
 
 template <typename T, int DKP, int DVP, int KTW, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DKP + DVP > 256 ? 1 : sizeof(T) == 2 && KTW == 1 && DKP + DVP <= 256 ? 3 : 2) void k_block_dkdv(const BlkParams P) {
+__global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DKP + DVP > 256 ? 1 : sizeof(T) == 2 && KTW == 1 && DKP + DVP <= 192 ? 3 : 2) void k_block_dkdv(const BlkParams P) {
   constexpr int ES = sizeof(T), WK = DKP * ES / 16, WV = DVP * ES / 16, NK = DKP * ES / 64, NV = DVP * ES / 64;
   constexpr int KEYS = WAVES >= 4 ? 64 : 32, KG = KEYS / 16 / KTW, RG = WAVES / KG, ROWS = 32 * RG;
   constexpr int QB = ROWS * WK * 16, STAGE = QB + ROWS * WV * 16, SLABS = 32 / blk_slab<T>();
@@ -270,24 +276,23 @@ __global__ __launch_bounds__(64 * WAVES, sizeof(T) == 4 && DKP + DVP > 256 ? 1 :
     }
 #pragma unroll
     for (int s = 0; s < SLABS; ++s) {
-      u32x4 wp[KTW], wd[KTW];
+      u32x4 w[KTW], lo[KTW];
 #pragma unroll
-      for (int kt = 0; kt < KTW; ++kt) {
-        wp[kt] = blk_pack<T>(p[kt], s);
-        wd[kt] = blk_pack<T>(ds[kt], s);
-      }
+      for (int kt = 0; kt < KTW; ++kt) blk_split<T>(p[kt], s, w[kt], lo[kt]);
 #pragma unroll
       for (int d = 0; d < DVP / 16; ++d) {
         const u32x4 f = gcol.read(gs, s, d);
 #pragma unroll
-        for (int kt = 0; kt < KTW; ++kt) dv[kt][d] = mma_slab<T>(f, wp[kt], dv[kt][d]);
+        for (int kt = 0; kt < KTW; ++kt) dv[kt][d] = blk_mma_split<T>(f, w[kt], lo[kt], dv[kt][d]);
         if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int kt = 0; kt < KTW; ++kt) blk_split<T>(ds[kt], s, w[kt], lo[kt]);
 #pragma unroll
       for (int d = 0; d < DKP / 16; ++d) {
         const u32x4 f = qcol.read(qs, s, d);
 #pragma unroll
-        for (int kt = 0; kt < KTW; ++kt) dk[kt][d] = mma_slab<T>(f, wd[kt], dk[kt][d]);
+        for (int kt = 0; kt < KTW; ++kt) dk[kt][d] = blk_mma_split<T>(f, w[kt], lo[kt], dk[kt][d]);
         if (d % 4 == 3) __builtin_amdgcn_sched_barrier(0);
       }
     }

@@ -2,7 +2,10 @@
 gradients lose bits on the way, whatever kernel a size takes.
 
 Bounds.  Those of the 64-bit reference without a rounding of the weights: a weight (or its gradient) enters its
-product as a sum of two bf16 values, whose second one leaves 2^-8 of the first one's 2^-8: h^2."""
+product as a sum of two bf16 values, whose second one leaves 2^-8 of the first one's 2^-8: h^2.  delta, formed
+from the stored output, is corrected by e = sum_j p_j (dp_j - delta); with computed weights that are off by the
+share s of themselves, delta + e differs from sum_j p_j dp_j by s sum p |dp| + s |delta| + sum p edp and the
+sum's n u; the correction of dq takes e from a sum of weights that are rounded once, which adds h |e|."""
 import numpy as np
 import pytest
 
@@ -20,6 +23,28 @@ def _forward_bounds(keep):
     w, v, out = keep["w"], keep["v"], keep["out"]
     eo = (keep["share"] + H * H) * (w @ np.abs(v))
     return ref._heads(eo + H * (np.abs(out) + eo))
+
+
+def _backward_bounds(keep, dout, cfg, val, live):
+    w, s, U, G = keep["w"], keep["share"], ref.U, cfg.heads_q // cfg.heads_kv
+    do = np.where(live[:, None, :, None], ref._heads(dout), 0)
+    B = do.shape[0]
+    dp = do @ keep["v"].swapaxes(2, 3)
+    edp = (cfg.d_v + 4) * U * (np.abs(do) @ np.abs(keep["v"]).swapaxes(2, 3))
+    n = keep["hit"].sum(3, keepdims=True)
+    delta = (do * keep["out"]).sum(3, keepdims=True)
+    e = (H + (cfg.d_v + 4) * U) * np.abs(do * keep["out"]).sum(3, keepdims=True)  # the stored output's error, at most
+    edelta = (w * ((s + n * U) * (np.abs(dp) + np.abs(delta) + e) + edp)).sum(3, keepdims=True) + s * (np.abs(delta) + e)
+    ds = w * (dp - delta) * cfg.scale
+    # before the correction the gradient of a score holds e as well, whose lower half is rounded
+    eds = cfg.scale * w * ((np.abs(dp - delta) + e) * (s + 4 * U + H * H) + edp + edelta)
+    eq = (eds + n * U * np.abs(ds) + cfg.scale * w * e * (H + s)) @ np.abs(keep["k"])
+    fold = lambda t: t.reshape(B, cfg.heads_kv, G, *t.shape[2:]).sum(2)  # noqa: E731
+    rows = np.repeat(fold(keep["hit"].sum(2)[..., None]), G, axis=1)
+    ek = fold((eds.swapaxes(2, 3) + rows * U * np.abs(ds).swapaxes(2, 3)) @ np.abs(keep["q"]))
+    ev = fold((w * (s + H * H)).swapaxes(2, 3) @ np.abs(do) + rows * U * (w.swapaxes(2, 3) @ np.abs(do)))
+    err = {"dq": ref._heads(eq), "dk": ref._heads(ek), "dv": ref._heads(ev)}
+    return {x: err[x] + H * (np.abs(val[x]) + err[x]) for x in err}
 
 
 FEW = [(4, 1, 64, 64, 64, 4, 2, 1),                                        # single queries
@@ -61,3 +86,17 @@ def test_no_bits_are_lost_in_steps(hq, hkv, dk, dv):
     out = op.step(q, kt, vt, t["k"], t["v"], means, _i32(pos))
     want, _, keep = ref.forward(_host(q)[:, None], _host(t["k"]), _host(t["v"]), sel.cpu().numpy(), cfg, pos)
     _check("out", out, want["out"][:, 0], _forward_bounds(keep)[:, 0])
+
+
+@pytest.mark.parametrize("hq,hkv,dk,dv,block,n,B,L", FEW + MANY)
+def test_no_bits_are_lost_in_gradients(hq, hkv, dk, dv, block, n, B, L):
+    import torch
+    cfg, op, t, h, sel, start, want, keep = _case(hq, hkv, dk, dv, block, n, B, L)
+    out = torch.from_numpy(want["out"]).to(t["dout"]).contiguous()
+    lse = torch.from_numpy(want["lse"]).float().cuda().contiguous()
+    got = op.backward(t["q"], t["k"], t["v"], sel, out, lse, t["dout"], _i32(start))
+    val, _ = ref.backward(h["q"], h["k"], h["v"], sel.cpu().numpy(), h["dout"], cfg, start)
+    bound = _backward_bounds(keep, h["dout"], cfg, val, ref.positions(B, L, t["k"].shape[1], start) >= 0)
+    for name, x in zip(("dq", "dk", "dv"), got):
+        if name == "dv" or (hq, hkv, dk, dv, block, n, B, L) in FEW:
+            _check(name, x, val[name], bound[name])
