@@ -14,21 +14,22 @@ struct TileShape {
 
 // A workgroup of 15 tiles has a CU to itself, two of 3 share one.  15 share keys
 // among more, but need 4096 tiles to fill the chip (forward of 8 / 2 heads of 64
-// with 3 and 15: 2048 tiles 33 and 36 us, 3500 tiles 66 and 48; of 16 / 4 heads of
-// 128: 1024 tiles 18 and 28, 3500 tiles 70 and 70, 8192 in fp32 1.26 and 1.08 ms;
-// gradients at 8192 tiles in bf16 606 and 505 us).
-// 15 tiles leave 128 registers a wave, 11 leave 168, 3 leave 256.  Units of 64
-// keys fit the first in the forward at d_v up to 128 (227 us at B = 8, L = 2048,
-// 16 / 4 heads of 128, against 233 with 32 keys, 234 with 11 tiles and 279 with 7);
-// in the gradient they spill (B = 2, L = 4096: 246 and 284 us), and d_v of 256
-// spills with 15 tiles (one sequence of 16384, 8 / 2 heads: forward 509 us with 15,
-// 501 with 11, backward 1207 and 1115).  fp32 with wide heads takes 3 tiles for
-// their registers.
+// with 3 and 15: 2048 tiles 60 and 77 us, 3500 tiles 119 and 95; of 16 / 4 heads of
+// 128: 1024 tiles 29 and 50, 3500 tiles 108 and 107, 8192 in fp32 1.29 and 1.12 ms).
+// 15 tiles leave 128 registers a wave, 11 leave 168, 7 and 3 leave 256.  Forward:
+// units of 64 keys fit the first up to d_v of 128, but for 3 registers (237 us at
+// B = 8, L = 2048, 16 / 4 heads of 128, against 240 with 32 keys, 239 with 11 tiles
+// and 289 with 7); d_v of 256 takes units of 32 and 11 tiles (L = 16384, 8 / 2 heads:
+// 529 us; 7 tiles 643).  The bf16 gradient has a second sum beside that of dq and
+// takes as many tiles as hold both (B = 2, L = 4096, 16 / 4 heads of 128: 550 us with
+// 11, 580 with 7, 606 with 3; d_v of 256 at L = 16384: 1.32 ms with 7, 1.38 with 3).
+// fp32 with wide heads takes 3 tiles for their registers.
 // es: bytes of an element; dkp, dvp: padded head widths.
 constexpr TileShape tile_shape(int es, int dkp, int dvp, bool gradient, int block, bool many) {
   if (!many) return {es == 4 ? 16 : 32, 3};
   if (es == 4) return {16, dvp == 256 || (gradient && dkp == 128) ? 3 : 15};
-  return {!gradient && dvp <= 128 && block > 32 ? 64 : 32, dvp == 256 ? 11 : 15};
+  if (gradient) return {32, dkp == 128 ? (dvp == 256 ? 7 : 11) : dvp == 256 ? 11 : 15};
+  return {dvp <= 128 && block > 32 ? 64 : 32, dvp == 256 ? 11 : 15};
 }
 
 // Workgroups, for `heads` sequences and key-value heads: XCDs take equal numbers of those.

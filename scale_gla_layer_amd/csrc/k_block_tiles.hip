@@ -131,7 +131,7 @@ __global__ __launch_bounds__(64 * (WAVES + 1), WAVES == TILE_WAVES_MAX ? 4 : WAV
   constexpr int NK = DKP * ES / 64, NV = DVP * ES / 64, KEY_T = KT / 16, SLABS = KT / blk_slab<T>();
   constexpr int KB = KT * WK * 16, STAGE = KB + KT * WV * 16, NT = WAVES, THREADS = 64 * (WAVES + 1);
   constexpr int OUT = GRAD ? DKP : DVP;  // width of the accumulated rows
-  constexpr bool EXACT = GRAD && ES == 2 && WAVES == 3;  // delta put right (more tiles leave no registers for it)
+  constexpr bool EXACT = GRAD && ES == 2;  // delta put right
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const int words = (P.nb + 31) / 32, pitch = P.n + 1;
   __shared__ int slast;

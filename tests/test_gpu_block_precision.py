@@ -98,5 +98,4 @@ def test_no_bits_are_lost_in_gradients(hq, hkv, dk, dv, block, n, B, L):
     val, _ = ref.backward(h["q"], h["k"], h["v"], sel.cpu().numpy(), h["dout"], cfg, start)
     bound = _backward_bounds(keep, h["dout"], cfg, val, ref.positions(B, L, t["k"].shape[1], start) >= 0)
     for name, x in zip(("dq", "dk", "dv"), got):
-        if name == "dv" or (hq, hkv, dk, dv, block, n, B, L) in FEW:
-            _check(name, x, val[name], bound[name])
+        _check(name, x, val[name], bound[name])
