@@ -501,8 +501,8 @@ msgla_status msgla_recurrence_step(const msgla_recurrence_config* cfg, const msg
  * (1 / sqrt(d_k) as a rule).  dtype: of q, k, v, the output and their
  * gradients; bf16 inputs meet on bf16 matrix cores with fp32 sums (softmax
  * weights and their gradients enter the products with 16 bits, as two bf16
- * values each), fp32 ones on fp32 matrix cores; scores for the selection are
- * fp64 sums.
+ * values each), fp32 ones on fp32 matrix cores; a weight below 2^-126 counts as
+ * 0; scores for the selection are fp64 sums.
  */
 typedef struct {
   int32_t heads_q, heads_kv;

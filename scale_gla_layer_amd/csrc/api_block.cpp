@@ -69,10 +69,11 @@ int es_of(const msgla_block_config* c) { return c->dtype == MSGLA_BF16 ? 2 : 4; 
 
 // Tiles that share keys and values, in workgroups; or, for a few queries over long
 // sequences, a tile a wave with its blocks dealt, 32 keys at a time, to as many
-// waves (parts) as give about 4096, sixteen on a CU.  Forward of 16 / 4 heads of
-// 128, shared against dealt: 256 tiles 9.0 and 33.6 us, 64 (of 16 blocks at 8192
-// positions) 117 and 54; 8 / 2 heads of 128 and 128 in fp32: 256 tiles 30 and 57,
-// 32 (16 / 4 heads) 489 and 71.  Single queries have nothing to share.
+// waves (parts) as give about 4096, sixteen on a CU.  Calls of the forward of 16 / 4
+// heads of 128, shared against dealt: 256 tiles 17 and 32 us, 64 (of 16 blocks at
+// 8192 positions) 117 and 53, 128 118 and 90, with the gradient 176 and 152; 8 / 2
+// heads of 128 in fp32: 256 tiles 54 and 57, with the gradient 141 and 131, 32 of
+// 16 / 4 heads 469 and 70.  Single queries have nothing to share.
 bool use_tiles(const BlkParams& P) { return P.L > 1 && P.tiles >= 128 && P.nb <= BLK_TILES_MAX; }
 int parts_of(const BlkParams& P) {
   return use_tiles(P) || P.tiles >= 4096 ? 1 : std::min<int>(P.n << (P.lgT - 5), (int)(4096 / P.tiles));

@@ -5,7 +5,10 @@
 // KTW tiles of 16 keys a wave, and streams through the queries that chose the
 // block: their (query, head) rows of q and do are gathered asynchronously into
 // one of two LDS stages while the other is worked on, 32 rows for each group of
-// waves that together hold all keys.  With KTW = 2 every row that a wave reads
+// waves that together hold all keys.  The overlap is a part of the step only: the
+// threads that bring lse wait for the next stage with it, and the compiler, which
+// does not know the two stages apart, waits for all copies before the transposed
+// reads.  With KTW = 2 every row that a wave reads
 // from LDS meets 32 keys, which is what LDS and the matrix cores take equal time
 // for; two groups of waves then take different rows and add up at the end.
 //   The lists of those queries come from a bit matrix (block x query) that is

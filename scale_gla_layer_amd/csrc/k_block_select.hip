@@ -439,7 +439,7 @@ template <typename T, int DKP> void step_t(const BlkParams& P, hipStream_t st) {
 
 template <typename T, int DKP> void select_t(const BlkParams& P, hipStream_t st) {
   const dim3 grid((unsigned)((int64_t)P.B * P.Hkv * ((P.L + SEL_ROWS - 1) / SEL_ROWS))), block(64 * SEL_WAVES);
-  // the smaller score buffer lets five workgroups share a CU's LDS instead of one
+  // the smaller score buffer lets four workgroups share a CU's LDS instead of two (d_k up to 64: six and three)
   if (P.nb <= 128) hipLaunchKernelGGL((k_block_select<T, DKP, 128>), grid, block, 0, st, P);
   else hipLaunchKernelGGL((k_block_select<T, DKP, BLK_PIECE>), grid, block, 0, st, P);
 }

@@ -1,7 +1,7 @@
 // Attention over selected blocks for many queries: forward and the gradient of
 // the queries with keys and values shared by a workgroup.
 //
-// A workgroup takes 15 (or 11, or 3) neighbouring tiles of 16 (query, head) rows, one
+// A workgroup takes 15 (or 11, 7, 3) neighbouring tiles of 16 (query, head) rows, one
 // a wave, and walks the union of all its queries' blocks in ascending order, KT
 // keys a unit.  One more wave copies each unit's keys and values once,
 // asynchronously, into a ring of LDS stages; the tiles' waves work on the units
@@ -14,8 +14,9 @@
 // earlier ones as done, and the copying wave counts every unit it has issued as
 // filled before it waits for a stage, which the waves free in order.
 //
-// Bound by vector instructions, which is why a unit is as long as a block (up to
-// 64 keys) and everything that is one value a unit is kept out of the lanes:
+// Bound by vector, matrix and LDS instructions, which take turns, and by the copying
+// wave, which has one unit under way at a time.  So a unit is as long as a block (up
+// to 64 keys), and everything that is one value a unit is kept out of the lanes:
 // lists and their unions are bit maps that scalar instructions walk, the running
 // maximum follows a row's true one only when that has grown by more than 8 (in
 // units of log 2: weights stay below 2^8), and rows that have not chosen a block
@@ -93,7 +94,10 @@ __device__ __forceinline__ void ring_put(int* p, int v) {
   __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
 }
 
-// The copying wave: up to FLIGHT units under way at a time.
+// The copying wave.  Units are copied one after the other: the compiler does not know
+// that the counters are apart from the rows that the copies write, and waits for all
+// copies before it touches a counter, so the wait for all units before the last one
+// leaves none under way, and a unit is announced when the one behind it has landed.
 template <typename T, int DKP, int DVP, int KT, int WAVES>
 __device__ __forceinline__ void fill_ring(const BlkParams& P, Ring* ring, char* ring_lds, int stages, Blocks blocks,
                                           int last, const char* kbase, const char* vbase, int lane) {

@@ -23,8 +23,8 @@
 // leaves every chunk's entry state, then the chunks from the last to the first.
 // Bound by HBM and, nearly as much, by the gate's arithmetic (about 45 vector
 // instruction slots an element with NORM), which is why it is worth reading and
-// evaluating once.  B = 8, L = 2048, D = 1024 in bf16: forward 36 us (2.8 TB/s; a
-// copy of the bytes takes 20), backward 93 (33); in three passes with the maps
+// evaluating once.  B = 8, L = 2048, D = 1024 in bf16: forward 37 us (2.7 TB/s; a
+// copy of the bytes takes 20), backward 94 (33); in three passes with the maps
 // joined between them they took 77 and 286.
 #include <type_traits>
 
@@ -369,9 +369,10 @@ __global__ __launch_bounds__(64 * REC_WAVES) void k_rec_forward(const RecParams 
 // ---- backward --------------------------------------------------------------------
 
 // Chunks from the last to the first; P.entry holds their entry states.
-// fp32 with PLAIN would need 18 registers more than two workgroups a CU leave
-// (held to them, B = 8, L = 2048, D = 1024: 130 -> 110 us; bf16 fits by itself, and
-// held to them takes 260 us for 250 at B = 16, L = 4093).
+// fp32 with PLAIN and two channels a lane is held to two workgroups a CU, which costs
+// it 16 registers in memory (B = 8, L = 2048, D = 1024: 130 -> 110 us); the other fp32
+// forms fit by themselves.  So does bf16, which held to them takes 260 us for 250 at
+// B = 16, L = 4093.
 template <typename T, int VEC, int MODE>
 __global__ __launch_bounds__(64 * REC_BWAVES, sizeof(T) == 4 ? 2 : 1) void k_rec_backward(const RecParams P) {
   constexpr int NW = REC_BWAVES, NT = REC_NT;
