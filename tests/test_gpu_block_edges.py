@@ -72,3 +72,28 @@ def test_gradients_of_many_short_sequences():
     want, bound = ref.backward(h["q"], h["k"], h["v"], sel.cpu().numpy(), h["dout"], cfg)
     for name, x in zip(("dq", "dk", "dv"), got):
         _check(name, x, want[name], bound[name])
+
+
+def test_caches_beyond_32_bits():
+    """The last of five sequences whose caches hold 5 GB each, against that sequence alone."""
+    torch = _torch()
+    cfg = BlockAttentionConfig(16, 8, 64, 64, 64, 16)
+    B, S = 5, 1 << 20
+    op = _op(cfg)
+    g = torch.Generator(device="cuda").manual_seed(44)
+    k, v = (torch.empty((B, S, 8, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    for x in (*k, *v):
+        x.normal_(generator=g)
+    q, kt, vt = (torch.randn((B, n, 64), generator=g, device="cuda").bfloat16() for n in (16, 8, 8))
+    pos = _i32([5, S - 1, 77, S // 2 + 63, S - 1])
+    last, k1, v1 = slice(B - 1, B), k[B - 1:].clone(), v[B - 1:].clone()
+    means = op.means(k, pos)
+    assert torch.equal(means[last], op.means(k1, pos[last]))
+    sel = op.select(q[:, None], means, pos)
+    assert torch.equal(sel[last], op.select(q[last, None], means[last].contiguous(), pos[last]))
+    for a, b in zip(op.forward(q[:, None], k, v, sel, pos), op.forward(q[last, None], k1, v1, sel[last], pos[last])):
+        assert torch.equal(a[last], b)
+    m1 = means[last].clone()
+    out = op.step(q, kt, vt, k, v, means, pos)
+    assert torch.equal(out[last], op.step(q[last], kt[last], vt[last], k1, v1, m1, pos[last]))
+    assert torch.equal(k[last], k1) and torch.equal(v[last], v1) and torch.equal(means[last], m1)
