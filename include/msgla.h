@@ -608,6 +608,119 @@ msgla_status msgla_block_attention_step(const msgla_block_config* cfg, const msg
                                         const msgla_heads* out_t, void* workspace,
                                         size_t workspace_bytes, void* stream);
 
+/*
+ * Layer norm over the channels of every row:
+ *     y = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(mean of (x - mean)^2 + eps)
+ *   width: channels, 1 .. 16384.  eps: 1e-20 .. 1.  dtype: of x, y and their gradients; statistics and
+ *   sums are fp32, as are weight and bias.
+ */
+typedef struct {
+  int32_t width;
+  float eps;
+  int32_t dtype; /* msgla_dtype */
+} msgla_layer_norm_config;
+
+/*
+ * The norm of B * L rows (at most 2^28).
+ *   x [B][L][width] -> y [B][L][width], which may be x itself
+ *   weight, bias [width] fp32, or NULL for 1 and 0
+ *   mean, rstd: [B][L] fp32 for the backward, or NULL
+ * A NaN or infinity reaches its own row only.
+ */
+msgla_status msgla_layer_norm_forward(const msgla_layer_norm_config* cfg, const msgla_rows* x,
+                                      const float* weight, const float* bias, int64_t B, int64_t L,
+                                      const msgla_rows* y, float* mean, float* rstd, void* stream);
+
+/* Device workspace of msgla_layer_norm_backward (bytes); (size_t)-1 for an
+ * invalid configuration or size.  It may be NULL when neither dweight nor dbias
+ * is wanted. */
+size_t msgla_layer_norm_backward_workspace_bytes(const msgla_layer_norm_config* cfg, int64_t B, int64_t L);
+
+/*
+ * Its vector-Jacobian product: with xh = (x - mean) rstd and g = dy weight,
+ *     dx = rstd (g - mean of g - xh mean of (g xh))
+ *     dweight = sum of dy xh,  dbias = sum of dy  over all rows
+ * dweight and dbias [width] fp32 are overwritten and may be NULL.  x, weight and
+ * the forward's mean and rstd are given; dx may be dy itself.  The result is the
+ * same bit for bit from call to call.
+ */
+msgla_status msgla_layer_norm_backward(const msgla_layer_norm_config* cfg, const msgla_rows* x,
+                                       const msgla_rows* dy, const float* weight, const float* mean,
+                                       const float* rstd, int64_t B, int64_t L, const msgla_rows* dx,
+                                       float* dweight, float* dbias, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
+ * Linear attention with a decay for each head: the layer's recurrence on given
+ * q, k and v, with one constant gamma = exp(log_decay) a head in place of a gate,
+ *     S_t = gamma S_{t-1} + k_t^T v_t,      out_t = scale q_t S_t,
+ * the state S [d_k][d_v] a head.
+ *   heads: 1 .. 1024; d_k and d_v: multiples of 8 up to 256; scale 1e-30 .. 1e30
+ *   (1 / sqrt(d_k) as a rule).  dtype: of q, k, v, the output and their
+ *   gradients; states and sums are fp32.  bf16 inputs meet on bf16 matrix cores,
+ *   where states, decayed keys and weights enter the products with 16 bits, as two
+ *   bf16 values each; fp32 ones on fp32 matrix cores.
+ *   log_decay [heads] fp32 (device): at most 0 as a rule; minus infinity
+ *   (gamma = 0) leaves each token its own product.  It has no gradient.
+ */
+typedef struct {
+  int32_t heads;
+  int32_t d_k, d_v;
+  float scale;
+  int32_t dtype; /* msgla_dtype */
+} msgla_linear_config;
+
+/* Device workspace of msgla_linear_attention_forward / _backward for batch B and
+ * length L (bytes; may be 0, and then workspace may be NULL); (size_t)-1 for an
+ * invalid configuration or size. */
+size_t msgla_linear_attention_workspace_bytes(const msgla_linear_config* cfg, int64_t B, int64_t L);
+size_t msgla_linear_attention_backward_workspace_bytes(const msgla_linear_config* cfg, int64_t B, int64_t L);
+
+/*
+ * The attention over B sequences of L positions (B * L at most 2^28).
+ *   q, k [B][L][heads][d_k], v [B][L][heads][d_v] -> out [B][L][heads][d_v]
+ *   lens: NULL, or [B] int32 (device): tokens of each sequence, 0 .. L (values
+ *         outside are taken as the nearest).  Rows behind them are padding: what
+ *         q, k and v hold there has no influence, out is 0 and the state stays.
+ *   state_in: [B][heads][d_k][d_v] fp32 before the first token, or NULL for 0
+ *   state_out: NULL, or receives the state after the last token; may be state_in.
+ * States are 16-byte aligned.  A NaN or infinity of a token may reach every
+ * output of its sequence and head.  The result is the same bit for bit from call
+ * to call.
+ */
+msgla_status msgla_linear_attention_forward(const msgla_linear_config* cfg, const msgla_heads* q,
+                                            const msgla_heads* k, const msgla_heads* v,
+                                            const float* log_decay, const int32_t* lens,
+                                            const float* state_in, int64_t B, int64_t L,
+                                            const msgla_heads* out, float* state_out, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/*
+ * Its vector-Jacobian product: from dout [B][L][heads][d_v] and dstate_out
+ * (dLoss/dstate_out, or NULL for 0), with dS_t = gamma dS_{t+1} + scale q_t^T dout_t,
+ *     dq_t = scale dout_t S_t^T,   dk_t = v_t dS_t^T,   dv_t = k_t dS_t
+ * with 0 at padding, and dstate_in [B][heads][d_k][d_v] fp32 unless it is NULL.
+ * q, k, v, log_decay, lens and state_in are the forward's.  No output may overlap
+ * an input or another output.
+ */
+msgla_status msgla_linear_attention_backward(const msgla_linear_config* cfg, const msgla_heads* q,
+                                             const msgla_heads* k, const msgla_heads* v,
+                                             const float* log_decay, const int32_t* lens,
+                                             const float* state_in, const msgla_heads* dout,
+                                             const float* dstate_out, int64_t B, int64_t L,
+                                             const msgla_heads* dq, const msgla_heads* dk,
+                                             const msgla_heads* dv, float* dstate_in, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/* One streaming step of B sequences, in one launch without a workspace (stride_t is
+ * not read).  mask: NULL, or [B] bytes; where it is 0 the output is 0 and the state
+ * stays.  state_in and state_out are required and may be the same buffer. */
+msgla_status msgla_linear_attention_step(const msgla_linear_config* cfg, const msgla_heads* q_t,
+                                         const msgla_heads* k_t, const msgla_heads* v_t,
+                                         const float* log_decay, const uint8_t* mask,
+                                         const float* state_in, int64_t B, const msgla_heads* out_t,
+                                         float* state_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,7 +12,8 @@ import ctypes
 import os
 from typing import Optional, Sequence
 
-from .config import BF16, F32, BlockAttentionConfig, MsglaConfig, RECURRENCE_INPUTS, RecurrenceConfig
+from .config import (BF16, F32, BlockAttentionConfig, LayerNormConfig, LinearAttentionConfig, MsglaConfig, RECURRENCE_INPUTS,
+                     RecurrenceConfig)
 
 MAX_BRANCHES = 8
 N_STAGES = 6
@@ -33,6 +34,9 @@ SYMBOLS = (
     "msgla_block_means", "msgla_block_select", "msgla_block_attention_workspace_bytes",
     "msgla_block_attention_backward_workspace_bytes", "msgla_block_attention_step_workspace_bytes",
     "msgla_block_attention", "msgla_block_attention_backward", "msgla_block_attention_step",
+    "msgla_layer_norm_backward_workspace_bytes", "msgla_layer_norm_forward", "msgla_layer_norm_backward",
+    "msgla_linear_attention_workspace_bytes", "msgla_linear_attention_backward_workspace_bytes",
+    "msgla_linear_attention_forward", "msgla_linear_attention_backward", "msgla_linear_attention_step",
 )
 NOALLOC_WORKSPACE_BYTES = 192 << 20  # MSGLA_NOALLOC_WORKSPACE_BYTES
 
@@ -104,6 +108,15 @@ class CBlockConfig(ctypes.Structure):
                                               "n_recent")] + [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
+class CLayerNormConfig(ctypes.Structure):
+    _fields_ = [("width", ctypes.c_int32), ("eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
+class CLinearConfig(ctypes.Structure):
+    _fields_ = [("heads", ctypes.c_int32), ("d_k", ctypes.c_int32), ("d_v", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("dtype", ctypes.c_int32)]
+
+
 class CStageEvents(ctypes.Structure):
     _fields_ = [("start", ctypes.c_void_p * N_STAGES), ("stop", ctypes.c_void_p * N_STAGES)]
 
@@ -167,6 +180,19 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                                           i64, i64, heads, heads, heads, vp, sz, vp]),
         "msgla_block_attention_step": (ctypes.c_int, [blk, heads, heads, heads, vp, i64, i64, heads, heads, vp, heads,
                                                       vp, sz, vp]),
+    })
+    norm, lin = ctypes.POINTER(CLayerNormConfig), ctypes.POINTER(CLinearConfig)
+    sig.update({
+        "msgla_layer_norm_backward_workspace_bytes": (sz, [norm, i64, i64]),
+        "msgla_layer_norm_forward": (ctypes.c_int, [norm, rows, vp, vp, i64, i64, rows, vp, vp, vp]),
+        "msgla_layer_norm_backward": (ctypes.c_int, [norm, rows, rows, vp, vp, vp, i64, i64, rows, vp, vp, vp, sz, vp]),
+        "msgla_linear_attention_workspace_bytes": (sz, [lin, i64, i64]),
+        "msgla_linear_attention_backward_workspace_bytes": (sz, [lin, i64, i64]),
+        "msgla_linear_attention_forward": (ctypes.c_int, [lin, heads, heads, heads, vp, vp, vp, i64, i64, heads, vp, vp,
+                                                          sz, vp]),
+        "msgla_linear_attention_backward": (ctypes.c_int, [lin, heads, heads, heads, vp, vp, vp, heads, vp, i64, i64,
+                                                           heads, heads, heads, vp, vp, sz, vp]),
+        "msgla_linear_attention_step": (ctypes.c_int, [lin, heads, heads, heads, vp, vp, vp, i64, heads, vp, vp]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -619,3 +645,118 @@ def msgla_block_attention_step(cfg: BlockAttentionConfig, q_t, k_t, v_t, k, v, m
         _f32("means", means, (B, hkv, block_count(cfg, S), dk), dev), _heads_out("out_t", out_t, (B, hq, dv), dt, dev),
         *_room(workspace, dev), _raw_stream(stream))
     _check("msgla_block_attention_step", st)
+
+
+_NORM_CACHE: dict = {}
+
+
+def c_layer_norm_config(cfg: LayerNormConfig) -> CLayerNormConfig:
+    c = _NORM_CACHE.get(cfg)
+    if c is None:
+        c = _NORM_CACHE[cfg] = CLayerNormConfig(cfg.width, cfg.eps, 1 if cfg.dtype == BF16 else 0)
+    return c
+
+
+def msgla_layer_norm_backward_workspace_bytes(cfg: LayerNormConfig, B: int, L: int) -> int:
+    return load_library().msgla_layer_norm_backward_workspace_bytes(ctypes.byref(c_layer_norm_config(cfg)), B, L)
+
+
+def msgla_layer_norm_forward(cfg: LayerNormConfig, x, y, weight=None, bias=None, mean=None, rstd=None, stream=None):
+    """x, y: [B, L, width] (any strides with a dense last dimension); weight, bias [width] and mean, rstd [B, L] fp32."""
+    B, L, dt, dev = *_dims("x", x, 3).shape[:2], _storage(cfg), x.device
+    shape = (B, L, cfg.width)
+    st = load_library().msgla_layer_norm_forward(
+        c_layer_norm_config(cfg), _rows("x", x, shape, dt, dev), _f32("weight", weight, (cfg.width,), dev),
+        _f32("bias", bias, (cfg.width,), dev), B, L, _rows_out("y", y, shape, dt, dev), _f32("mean", mean, (B, L), dev),
+        _f32("rstd", rstd, (B, L), dev), _raw_stream(stream))
+    _check("msgla_layer_norm_forward", st)
+
+
+def msgla_layer_norm_backward(cfg: LayerNormConfig, x, dy, mean, rstd, dx, workspace, weight=None, dweight=None,
+                              dbias=None, stream=None):
+    """x, dy, dx: [B, L, width]; mean, rstd [B, L] and weight, dweight, dbias [width] fp32."""
+    B, L, dt, dev = *_dims("x", x, 3).shape[:2], _storage(cfg), x.device
+    shape = (B, L, cfg.width)
+    st = load_library().msgla_layer_norm_backward(
+        c_layer_norm_config(cfg), _rows("x", x, shape, dt, dev), _rows("dy", dy, shape, dt, dev),
+        _f32("weight", weight, (cfg.width,), dev), _f32("mean", mean, (B, L), dev), _f32("rstd", rstd, (B, L), dev), B, L,
+        _rows_out("dx", dx, shape, dt, dev), _f32("dweight", dweight, (cfg.width,), dev),
+        _f32("dbias", dbias, (cfg.width,), dev), *_room(workspace, dev), _raw_stream(stream))
+    _check("msgla_layer_norm_backward", st)
+
+
+_LINEAR_CACHE: dict = {}
+
+
+def c_linear_config(cfg: LinearAttentionConfig) -> CLinearConfig:
+    c = _LINEAR_CACHE.get(cfg)
+    if c is None:
+        c = _LINEAR_CACHE[cfg] = CLinearConfig(cfg.heads, cfg.d_k, cfg.d_v, cfg.scale, 1 if cfg.dtype == BF16 else 0)
+    return c
+
+
+def msgla_linear_attention_workspace_bytes(cfg: LinearAttentionConfig, B: int, L: int) -> int:
+    return load_library().msgla_linear_attention_workspace_bytes(ctypes.byref(c_linear_config(cfg)), B, L)
+
+
+def msgla_linear_attention_backward_workspace_bytes(cfg: LinearAttentionConfig, B: int, L: int) -> int:
+    return load_library().msgla_linear_attention_backward_workspace_bytes(ctypes.byref(c_linear_config(cfg)), B, L)
+
+
+def _state(name: str, t, cfg, B: int, device):
+    p = _f32(name, t, (B, cfg.heads, cfg.d_k, cfg.d_v), device)
+    if p is not None and p % 16:
+        raise ValueError(f"{name} must start at a multiple of 16 bytes")
+    return p
+
+
+def _decay(t, cfg, device):
+    if t is None:
+        raise ValueError("log_decay is missing")
+    return _f32("log_decay", t, (cfg.heads,), device)
+
+
+def _linear_inputs(cfg, q, k, v, log_decay, lens, state_in):
+    """(B, L, type, device, the C arguments of the six)"""
+    B, L, dt, dev = *_dims("q", q, 4).shape[:2], _storage(cfg), q.device
+    key, value = (B, L, cfg.heads, cfg.d_k), (B, L, cfg.heads, cfg.d_v)
+    return B, L, dt, dev, (_heads("q", q, key, dt, dev), _heads("k", k, key, dt, dev), _heads("v", v, value, dt, dev),
+                           _decay(log_decay, cfg, dev), _i32("lens", lens, (B,), dev),
+                           _state("state_in", state_in, cfg, B, dev))
+
+
+def msgla_linear_attention_forward(cfg: LinearAttentionConfig, q, k, v, log_decay, out, workspace, lens=None,
+                                   state_in=None, state_out=None, stream=None):
+    """q, k [B, L, heads, d_k], v [B, L, heads, d_v], log_decay [heads] fp32 -> out [B, L, heads, d_v]; lens [B] int32;
+    state_in, state_out [B, heads, d_k, d_v] fp32 (may be one tensor)."""
+    B, L, dt, dev, args = _linear_inputs(cfg, q, k, v, log_decay, lens, state_in)
+    st = load_library().msgla_linear_attention_forward(
+        c_linear_config(cfg), *args, B, L, _heads_out("out", out, (B, L, cfg.heads, cfg.d_v), dt, dev),
+        _state("state_out", state_out, cfg, B, dev), *_room(workspace, dev), _raw_stream(stream))
+    _check("msgla_linear_attention_forward", st)
+
+
+def msgla_linear_attention_backward(cfg: LinearAttentionConfig, q, k, v, log_decay, dout, dq, dk, dv, workspace,
+                                    lens=None, state_in=None, dstate_out=None, dstate_in=None, stream=None):
+    B, L, dt, dev, args = _linear_inputs(cfg, q, k, v, log_decay, lens, state_in)
+    key, value = (B, L, cfg.heads, cfg.d_k), (B, L, cfg.heads, cfg.d_v)
+    st = load_library().msgla_linear_attention_backward(
+        c_linear_config(cfg), *args, _heads("dout", dout, value, dt, dev), _state("dstate_out", dstate_out, cfg, B, dev),
+        B, L, _heads_out("dq", dq, key, dt, dev), _heads_out("dk", dk, key, dt, dev),
+        _heads_out("dv", dv, value, dt, dev), _state("dstate_in", dstate_in, cfg, B, dev), *_room(workspace, dev),
+        _raw_stream(stream))
+    _check("msgla_linear_attention_backward", st)
+
+
+def msgla_linear_attention_step(cfg: LinearAttentionConfig, q_t, k_t, v_t, log_decay, state_in, state_out, out_t,
+                                mask=None, stream=None):
+    """q_t, k_t [B, heads, d_k], v_t [B, heads, d_v] -> out_t [B, heads, d_v]; state_in, state_out [B, heads, d_k, d_v]
+    fp32 (may be one tensor); mask: [B] uint8."""
+    B, dt, dev = _dims("q_t", q_t, 3).shape[0], _storage(cfg), q_t.device
+    key, value = (B, cfg.heads, cfg.d_k), (B, cfg.heads, cfg.d_v)
+    st = load_library().msgla_linear_attention_step(
+        c_linear_config(cfg), _heads("q_t", q_t, key, dt, dev), _heads("k_t", k_t, key, dt, dev),
+        _heads("v_t", v_t, value, dt, dev), _decay(log_decay, cfg, dev), _dense("mask", mask, (B,), _t().uint8, dev),
+        _state("state_in", state_in, cfg, B, dev), B, _heads_out("out_t", out_t, value, dt, dev),
+        _state("state_out", state_out, cfg, B, dev), _raw_stream(stream))
+    _check("msgla_linear_attention_step", st)

@@ -42,6 +42,10 @@ SOURCES = [
     "k_block_tiles.hip",
     "k_block_grad.hip",
     "api_block.cpp",
+    "k_layer_norm.hip",
+    "api_layer_norm.cpp",
+    "k_linear.hip",
+    "api_linear.cpp",
 ]
 
 # rocBLAS: the backward's plain products (weight and input gradients)

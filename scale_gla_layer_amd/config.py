@@ -118,6 +118,45 @@ class BlockAttentionConfig:
 
 
 @dataclasses.dataclass(frozen=True)
+class LayerNormConfig:
+    """Layer norm over the last dimension: (x - mean) / sqrt(variance + eps), times a weight, plus a bias."""
+    width: int
+    eps: float = 1e-5
+    dtype: str = BF16
+
+    def __post_init__(self):
+        if not 1 <= self.width <= 16384:
+            raise ValueError("width must be 1 .. 16384")
+        if not 1e-20 <= self.eps <= 1:
+            raise ValueError("eps must be 1e-20 .. 1")
+        if self.dtype not in (F32, BF16):
+            raise ValueError(f"dtype must be {F32!r} or {BF16!r}")
+
+
+@dataclasses.dataclass(frozen=True)
+class LinearAttentionConfig:
+    """Linear attention with a decay for each head: S_t = gamma S_{t-1} + k_t^T v_t, out_t = scale q_t S_t.
+    ``scale`` None: 1 / sqrt(d_k)."""
+    heads: int
+    d_k: int
+    d_v: int
+    scale: Optional[float] = None
+    dtype: str = BF16
+
+    def __post_init__(self):
+        if not 1 <= self.heads <= 1024:
+            raise ValueError("heads must be 1 .. 1024")
+        if not 8 <= self.d_k <= 256 or self.d_k % 8 or not 8 <= self.d_v <= 256 or self.d_v % 8:
+            raise ValueError("d_k and d_v must be multiples of 8 up to 256")
+        if self.scale is None:
+            object.__setattr__(self, "scale", self.d_k ** -0.5)
+        if not 1e-30 <= self.scale <= 1e30:
+            raise ValueError("scale must be positive, 1e-30 .. 1e30")
+        if self.dtype not in (F32, BF16):
+            raise ValueError(f"dtype must be {F32!r} or {BF16!r}")
+
+
+@dataclasses.dataclass(frozen=True)
 class Workload:
     name: str
     cfg: MsglaConfig

@@ -1,0 +1,402 @@
+// Linear attention with a decay per head:
+//   S_t = gamma S_{t-1} + k_t^T v_t,   out_t = scale q_t S_t
+//
+// A chunk of 64 positions with the state S before it:
+//   out_i = scale (gamma^(i+1) q_i S + sum_{j <= i} gamma^(i-j) (q_i . k_j) v_j)
+//   S' = gamma^n S + sum_j gamma^(n-1-j) k_j^T v_j
+// so a walk over the chunks is four matrix products each.  A workgroup walks one
+// (sequence, head) for some columns of v, the state in the accumulators of its
+// four waves (each has a quarter of its rows) and, rounded, in LDS, where it is an
+// operand of the next chunk's product.  All exponents of gamma are at least 0, so
+// nothing overflows, and a decay of 0 (log_decay of minus infinity) is exact.
+//   Few sequences and heads: each sequence is cut into segments, what each adds
+// to the state is formed first (from zero, without outputs), and the walks
+// then begin with the states that these sum up to.
+//   The gradients are walks themselves: with do the output's gradient, dq is that
+// of (do, v, k), and from the last token to the first dk is that of (v, do, q) and
+// dv that of (k, q, do), whose state is the state's gradient.  Three jobs of a launch.
+//   bf16: the weighted q k^T, the state and the decayed keys enter their products
+// as two bf16 values each (16 bits); rounded once, each of them would be off by as
+// much as the output's own rounding.  Where the last state is wanted, which is fp32,
+// the decayed keys enter as three (with two it is off by 2.4e-6).  Sums are fp32.
+//   The products' layouts chain without exchanges between lanes: A^T = K Q^T holds
+// a row's weights where out^T = V^T A^T wants them, and S as the sum of K^T V has
+// four neighbouring rows a lane, which is 8 bytes of the transposed state in LDS.
+#include "block_device.hpp"
+#include "linear.hpp"
+
+namespace msgla {
+
+namespace {
+
+__device__ __forceinline__ float lin_power(int e, float lg2) { return exp2f((float)e * lg2); }
+
+// log2 of the head's decay; minus infinity as a number that no exponent makes finite again
+__device__ __forceinline__ float lin_log2(const float* log_decay, int h) {
+  const float v = log_decay[h];
+  return (v < -1e30f ? -1e30f : v) * BLK_LOG2E;
+}
+
+__device__ __forceinline__ int lin_len(const LinParams& P, int b) {
+  return P.lens ? max(0, min(P.lens[b], P.L)) : P.L;
+}
+
+// A sequence's tokens in the order of the walk; positions behind its end keep their place.
+struct LinOrder {
+  int len;
+  bool turned;
+  __device__ __forceinline__ int64_t at(int n) const { return turned && n < len ? len - 1 - n : n; }
+};
+
+// Two workgroups a CU where LDS holds them.
+template <typename T, int KWP, bool OUT>
+__global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_linear(const LinParams P) {
+  constexpr int ES = sizeof(T), VS = lin_columns(ES, KWP), C = LIN_CHUNK;
+  constexpr int NQ = KWP * ES / 64;            // slabs of a row
+  constexpr int KT = KWP / 64, VT = VS / 16;   // the wave's tiles of the state
+  constexpr int SL = C / blk_slab<T>();        // slabs of a chunk's positions
+  constexpr int KP = blk_pitch<T, KWP>(), VP = blk_pitch<T, VS>();
+  constexpr bool LO = ES == 2;
+  constexpr int NK = C * KWP * ES / 16 / 256, NV = C * VS * ES / 16 / 256;  // pieces a thread copies
+  __shared__ __attribute__((aligned(16))) char ks[C * KP];
+  __shared__ __attribute__((aligned(16))) char vs[C * VP];
+  __shared__ __attribute__((aligned(16))) char ss[OUT ? (LO ? 2 : 1) * VS * KP : 16];  // state^T [column][row], hi and lo
+  const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, a = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const LinJob& J = P.job[blockIdx.y];
+  const int nseg = OUT ? P.segments : P.segments - 1;
+  const int total = P.B * P.H * nseg * J.slices;
+  // an XCD takes neighbouring slices, which read the same q and k
+  const int w = remap_xcd(blockIdx.x, (total + N_XCD - 1) / N_XCD);
+  if (blockIdx.x / N_XCD >= (unsigned)((total + N_XCD - 1) / N_XCD) || w >= total) return;
+  const int slice = w % J.slices, seg = w / J.slices % nseg, bh = w / J.slices / nseg, b = bh / P.H, h = bh - b * P.H;
+  const int len = lin_len(P, b), v0 = slice * VS;
+  const LinOrder order{len, J.turned != 0};
+  const float lg2 = lin_log2(P.log_decay, h);
+  const int first = seg * P.seg_chunks * C, past = min(P.L, first + P.seg_chunks * C);
+  const int kw = J.kw * ES, vw = (J.vw - v0) * ES;  // bytes of a row, and of its part behind v0
+
+  f32x4 S[KT][VT];
+#pragma unroll
+  for (int i = 0; i < KT; ++i)
+#pragma unroll
+    for (int j = 0; j < VT; ++j) S[i][j] = zero4();
+  // rows 16 (KT wave + i) + 4 a + e, column v0 + 16 j + c16 of a state
+  auto each = [&](auto f) {
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int j = 0; j < VT; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * (KT * wave + i) + 4 * a + e, c = v0 + 16 * j + c16;
+          if (r < J.kw && c < J.vw) f(S[i][j], e, r, c);
+        }
+  };
+  const int64_t size = (int64_t)J.kw * J.vw;
+  if constexpr (OUT) {
+    if (J.entry) {
+      const float* p = J.entry + bh * size;
+      each([&](f32x4& s, int e, int r, int c) {
+        s[e] = p[J.flip_entry ? (int64_t)c * J.kw + r : (int64_t)r * J.vw + c] * J.entry_mul;
+      });
+    }
+    for (int m = 0; m < seg; ++m) {
+      const int begin = m * P.seg_chunks * C, n = max(0, min(len - begin, P.seg_chunks * C));
+      if (!n) break;
+      const float keep = lin_power(n - (m == 0 ? J.turned : 0), lg2);
+      const float* p = J.part + ((int64_t)bh * (P.segments - 1) + m) * size;
+      each([&](f32x4& s, int e, int r, int c) { s[e] = keep * s[e] + p[(int64_t)r * J.vw + c]; });
+    }
+  }
+
+  // decays within a chunk, for the lane's row 16 wave + c16 and its positions
+  const int mine = 16 * wave + c16;
+  float within[OUT ? C / 16 : 1][4];
+#pragma unroll
+  for (int t = 0; t < (OUT ? C / 16 : 1); ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int back = mine - (16 * t + 4 * a + e);
+      within[t][e] = back >= 0 ? lin_power(max(back, 0), lg2) : 0.f;
+    }
+  const float grow = lin_power(mine + 1, lg2), grow_first = lin_power(mine, lg2);
+  float left[SL][LO ? 8 : 4];  // until the chunk's last token, of the positions of a K^T operand
+  auto set_left = [&](int n) {
+#pragma unroll
+    for (int s = 0; s < SL; ++s)
+#pragma unroll
+      for (int e = 0; e < (LO ? 8 : 4); ++e) {
+        const int j = s * blk_slab<T>() + 4 * a + (e & 3) + 16 * (e >> 2);
+        left[s][e] = j < n ? lin_power(max(n - 1 - j, 0), lg2) : 0.f;
+      }
+  };
+  set_left(C);
+  const float keep_whole = lin_power(C, lg2);
+
+  const char *qb = J.q.p + b * J.q.sb + h * J.q.sh, *kb = J.k.p + b * J.k.sb + h * J.k.sh;
+  const char* vb = J.v.p + b * J.v.sb + h * J.v.sh + v0 * ES;
+  u32x4 kr[NK], vr[NV], qr[OUT ? NQ : 1];
+  auto fetch = [&](int n0) {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int p = tid + 256 * i, r = n0 + p / (KWP * ES / 16), at = p % (KWP * ES / 16) * 16;
+      kr[i] = r < min(len, past) ? blk_ld(kb + order.at(r) * J.k.st, at, kw) : zero16();
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = tid + 256 * i, r = n0 + p / (VS * ES / 16), at = p % (VS * ES / 16) * 16;
+      vr[i] = r < min(len, past) ? blk_ld(vb + order.at(r) * J.v.st, at, vw) : zero16();
+    }
+    if constexpr (OUT) {
+      const int r = n0 + mine;
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) qr[s] = r < min(len, past) ? blk_ld(qb + order.at(r) * J.q.st, 64 * s + 16 * a, kw) : zero16();
+    }
+  };
+  if (first < len) fetch(first);
+  int n0 = first;
+  for (; n0 < min(past, len); n0 += C) {
+    const int n = min(C, len - n0);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const int p = tid + 256 * i;
+      st16(ks + p / (KWP * ES / 16) * KP + p % (KWP * ES / 16) * 16, kr[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int p = tid + 256 * i;
+      st16(vs + p / (VS * ES / 16) * VP + p % (VS * ES / 16) * 16, vr[i]);
+    }
+    u32x4 q[OUT ? NQ : 1];
+    if constexpr (OUT) {
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) q[s] = qr[s];
+#pragma unroll
+      for (int i = 0; i < KT; ++i)
+#pragma unroll
+        for (int j = 0; j < VT; ++j) {
+          char* p = ss + (16 * j + c16) * KP + (16 * (KT * wave + i) + 4 * a) * ES;
+          const float v[4] = {S[i][j][0], S[i][j][1], S[i][j][2], S[i][j][3]};
+          if constexpr (LO) {
+            const u32x2 hi = pack8<bf16>(v);
+            const uint32_t w0 = hi[0], w1 = hi[1];
+            const float r[4] = {v[0] - u2f(w0 << 16), v[1] - u2f(w0 & 0xffff0000u), v[2] - u2f(w1 << 16), v[3] - u2f(w1 & 0xffff0000u)};
+            st8(p, hi);
+            st8(p + VS * KP, pack8<bf16>(r));
+          } else {
+            st16(p, pack16<float>(v));
+          }
+        }
+    }
+    __syncthreads();
+    if (n0 + C < min(past, len)) fetch(n0 + C);
+    if (n < C) set_left(n);
+    if constexpr (OUT) {
+      const bool lead = J.turned && n0 == 0;
+      f32x4 out[VT];
+#pragma unroll
+      for (int j = 0; j < VT; ++j) {
+        out[j] = zero4();
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) {
+          const char* p = ss + (16 * j + c16) * KP + 64 * s + 16 * a;
+          out[j] = mma_slab<T>(ld16(p), q[s], out[j]);
+          if constexpr (LO) out[j] = mma_slab<T>(ld16(p + VS * KP), q[s], out[j]);
+        }
+        out[j] *= lead ? grow_first : grow;
+      }
+      float A[C / 16][4];
+#pragma unroll
+      for (int t = 0; t < C / 16; ++t) {
+        f32x4 x = zero4();
+        if (t <= wave) {
+#pragma unroll
+          for (int s = 0; s < NQ; ++s) x = mma_slab<T>(ld16(ks + (16 * t + c16) * KP + 64 * s + 16 * a), q[s], x);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) A[t][e] = x[e] * within[t][e];
+      }
+#pragma unroll
+      for (int s = 0; s < SL; ++s) {
+        if (s * blk_slab<T>() > 16 * wave + 15) break;
+        u32x4 hi, lo;
+        blk_split<T>(A, s, hi, lo);
+#pragma unroll
+        for (int j = 0; j < VT; ++j) out[j] = blk_mma_split<T>(blk_column<T>(vs, VP, s * blk_slab<T>(), j, lane), hi, lo, out[j]);
+      }
+      if (n0 + mine < past) {
+        char* o = J.o.p + b * J.o.sb + order.at(n0 + mine) * J.o.st + h * J.o.sh + v0 * ES;
+        const float mul = mine < n ? P.scale : 0.f;
+#pragma unroll
+        for (int j = 0; j < VT; ++j) {
+          const int c = 16 * j + 4 * a;
+          const float v[4] = {out[j][0] * mul, out[j][1] * mul, out[j][2] * mul, out[j][3] * mul};
+          if (c * ES < vw) blk_st4<T>(o + c * ES, v);
+        }
+      }
+    }
+    const float keep = n == C && !(J.turned && n0 == 0) ? keep_whole : lin_power(n - (J.turned && n0 == 0 ? 1 : 0), lg2);
+#pragma unroll
+    for (int i = 0; i < KT; ++i)
+#pragma unroll
+      for (int j = 0; j < VT; ++j) S[i][j] *= keep;
+#pragma unroll
+    for (int s = 0; s < SL; ++s) {
+      u32x4 f[VT];
+#pragma unroll
+      for (int j = 0; j < VT; ++j) f[j] = blk_column<T>(vs, VP, s * blk_slab<T>(), j, lane);
+#pragma unroll
+      for (int i = 0; i < KT; ++i) {
+        const u32x4 raw = blk_column<T>(ks, KP, s * blk_slab<T>(), KT * wave + i, lane);
+        constexpr int N = LO ? 8 : 4;
+        float x[N];
+        unpack16<T>(raw, x);
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] *= left[s][e];
+        u32x4 hi, lo = zero16(), rest = zero16();
+        if constexpr (LO) {
+          split_bf16(x, hi, lo);
+          if (J.exit) {
+            float h[8], m[8];
+            unpack16<bf16>(hi, h);
+            unpack16<bf16>(lo, m);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] - h[e] - m[e];
+            rest = pack16<bf16>(x);
+          }
+        } else {
+          hi = pack16<float>(x);
+        }
+#pragma unroll
+        for (int j = 0; j < VT; ++j) {
+          S[i][j] = mma_slab<T>(hi, f[j], S[i][j]);
+          if constexpr (LO) {
+            S[i][j] = mma_slab<T>(lo, f[j], S[i][j]);
+            if (J.exit) S[i][j] = mma_slab<T>(rest, f[j], S[i][j]);
+          }
+        }
+      }
+    }
+  }
+  if constexpr (OUT) {
+    // rows behind the sequence's end
+    for (n0 = max(n0, first); n0 < past; n0 += C)
+      if (n0 + mine < past) {
+        char* o = J.o.p + b * J.o.sb + (int64_t)(n0 + mine) * J.o.st + h * J.o.sh + v0 * ES;
+        const float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < VT; ++j)
+          if ((16 * j + 4 * a) * ES < vw) blk_st4<T>(o + (16 * j + 4 * a) * ES, v);
+      }
+    if (J.exit && seg == P.segments - 1) {
+      float* p = J.last + bh * size;
+      const float mul = J.exit_mul * (J.turned && len > 0 ? lin_power(1, lg2) : 1.f);
+      each([&](f32x4& s, int e, int r, int c) { p[(int64_t)r * J.vw + c] = s[e] * mul; });
+    }
+  } else {
+    float* p = J.part + ((int64_t)bh * (P.segments - 1) + seg) * size;
+    each([&](f32x4& s, int e, int r, int c) { p[(int64_t)r * J.vw + c] = s[e]; });
+  }
+}
+
+// The last states to where they are wanted: a walk of another segment may read
+// the states before the first step from there.
+__global__ __launch_bounds__(256) void k_linear_exit(const float* from, float* to, int64_t n) {
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i < n) st16(to + i, ld16(from + i));
+}
+
+// One token: a workgroup takes LIN_STEP_COLUMNS columns of one state, four a lane.
+template <typename T> __global__ __launch_bounds__(LIN_STEP_THREADS) void k_linear_step(const LinParams P) {
+  constexpr int LANES = LIN_STEP_COLUMNS / 4, ROWS = LIN_STEP_THREADS / LANES;
+  __shared__ float side[LIN_STEP_THREADS / 64][LIN_STEP_COLUMNS];
+  const LinJob& J = P.job[0];
+  const int bh = blockIdx.x / J.slices, slice = blockIdx.x - bh * J.slices, b = bh / P.H, h = bh - b * P.H;
+  const int c = slice * LIN_STEP_COLUMNS + 4 * (threadIdx.x % LANES), r0 = threadIdx.x / LANES;
+  const bool on = !P.mask || P.mask[b];
+  const float gamma = lin_power(1, lin_log2(P.log_decay, h));
+  const T* q = reinterpret_cast<const T*>(J.q.p + b * J.q.sb + h * J.q.sh);
+  const T* k = reinterpret_cast<const T*>(J.k.p + b * J.k.sb + h * J.k.sh);
+  const T* v = reinterpret_cast<const T*>(J.v.p + b * J.v.sb + h * J.v.sh);
+  const int64_t at = (int64_t)bh * J.kw * J.vw + c;
+  f32x4 sum = zero4(), vc = zero4();
+  const bool in = c < J.vw;
+  if (in && on)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) vc[e] = to_f32(v[c + e]);
+  if (in)
+#pragma unroll 4
+    for (int r = r0; r < J.kw; r += ROWS) {
+      f32x4 s = __builtin_bit_cast(f32x4, ld16(J.entry + at + (int64_t)r * J.vw));
+      if (on) {
+        s = gamma * s + to_f32(k[r]) * vc;
+        sum += to_f32(q[r]) * s;
+      }
+      st16(J.exit + at + (int64_t)r * J.vw, __builtin_bit_cast(u32x4, s));
+    }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    float x = sum[e];
+#pragma unroll
+    for (int o = LANES; o < 64; o <<= 1) x += __shfl_xor(x, o);
+    if ((threadIdx.x & 63) < LANES) side[threadIdx.x >> 6][4 * (threadIdx.x % LANES) + e] = x;
+  }
+  __syncthreads();
+  const int col = slice * LIN_STEP_COLUMNS + threadIdx.x;
+  if (threadIdx.x < LIN_STEP_COLUMNS && col < J.vw) {
+    float x = 0.f;
+#pragma unroll
+    for (int i = 0; i < LIN_STEP_THREADS / 64; ++i) x += side[i][threadIdx.x];
+    reinterpret_cast<T*>(J.o.p + b * J.o.sb + h * J.o.sh)[col] = from_f32<T>(on ? x * P.scale : 0.f);
+  }
+}
+
+template <typename T, int KWP, bool OUT> void walk_jobs(const LinParams& P, hipStream_t st) {
+  int64_t most = 0;
+  for (int i = 0; i < P.jobs; ++i) {
+    const int64_t n = (int64_t)P.B * P.H * (OUT ? P.segments : P.segments - 1) * P.job[i].slices;
+    most = n > most ? n : most;
+  }
+  const int64_t grid = (most + N_XCD - 1) / N_XCD * N_XCD;
+  hipLaunchKernelGGL((k_linear<T, KWP, OUT>), dim3((unsigned)grid, (unsigned)P.jobs), dim3(256), 0, st, P);
+}
+
+// Jobs of one padded key width share a launch.
+template <typename T, int KWP> void walk(const LinParams& all, hipStream_t st) {
+  LinParams P = all;
+  P.jobs = 0;
+  for (int i = 0; i < all.jobs; ++i)
+    if (lin_kwp(all.job[i].kw) == KWP) P.job[P.jobs++] = all.job[i];
+  if (!P.jobs) return;
+  if (P.segments > 1) walk_jobs<T, KWP, false>(P, st);
+  walk_jobs<T, KWP, true>(P, st);
+  for (int i = 0; i < P.jobs; ++i) {
+    const LinJob& J = P.job[i];
+    const int64_t n = (int64_t)P.B * P.H * J.kw * J.vw;  // a multiple of 64
+    if (J.exit && J.last != J.exit)
+      hipLaunchKernelGGL(k_linear_exit, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, J.last, J.exit, n);
+  }
+}
+template <typename T> void walk_all(const LinParams& P, hipStream_t st) {
+  walk<T, 64>(P, st);
+  walk<T, 128>(P, st);
+  walk<T, 256>(P, st);
+}
+
+}  // namespace
+
+hipError_t launch_linear(const LinParams& P, bool bf16_path, hipStream_t st) {
+  bf16_path ? walk_all<bf16>(P, st) : walk_all<float>(P, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_step(const LinParams& P, bool bf16_path, hipStream_t st) {
+  const dim3 grid((unsigned)((int64_t)P.B * P.H * P.job[0].slices));
+  if (bf16_path) hipLaunchKernelGGL((k_linear_step<bf16>), grid, dim3(LIN_STEP_THREADS), 0, st, P);
+  else hipLaunchKernelGGL((k_linear_step<float>), grid, dim3(LIN_STEP_THREADS), 0, st, P);
+  return hipGetLastError();
+}
+
+}  // namespace msgla

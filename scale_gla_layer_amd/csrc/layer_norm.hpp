@@ -1,0 +1,45 @@
+// Launch parameters of the layer norm.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace msgla {
+
+struct LnRows {
+  char* p;
+  int64_t sb, st;  // byte strides of a sequence and of a position
+};
+
+struct LnParams {
+  LnRows x, y, dy, dx;
+  const float *weight, *bias;
+  float *mean, *rstd;               // forward: written, may be NULL
+  const float *mean_in, *rstd_in;   // backward
+  float *dweight, *dbias;
+  float* part;  // [parts][2][D] sums of dy xh and of dy over a workgroup's rows
+  int parts;
+  int64_t rows;
+  int L, D;
+  float eps;
+};
+
+constexpr int LN_MAX_WIDTH = 16384;  // 1024 lanes of four pieces, in fp32
+// Rows up to this many 16-byte pieces keep the sums for dweight and dbias in
+// registers while dx is formed; wider ones form them in a kernel of their own.
+constexpr int LN_WIDE = 1024;
+// Workgroups that the rows of a backward are dealt to, at most.
+constexpr int LN_PARTS = 1024;
+// Columns and threads of a workgroup of the kernels that sum over rows.
+constexpr int LN_COLS = 64, LN_COL_THREADS = 1024;
+
+struct LnShape {
+  int lanes, pieces, threads;  // lanes of a row, 16-byte pieces of a lane, threads of a workgroup
+};
+LnShape ln_shape(int64_t bytes_of_row);
+// workgroups of the backward, which are also the parts of its sums
+int ln_parts(int64_t rows, int64_t bytes_of_row);
+
+hipError_t launch_layer_norm(const LnParams& P, bool bf16_path, hipStream_t st);
+hipError_t launch_layer_norm_backward(const LnParams& P, bool bf16_path, hipStream_t st);
+
+}  // namespace msgla

@@ -1,0 +1,50 @@
+// Launch parameters of linear attention with a decay per head.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace msgla {
+
+struct LinHeads {
+  char* p;
+  int64_t sb, st, sh;  // byte strides of a sequence, a position, a head
+};
+
+constexpr int LIN_CHUNK = 64;     // positions of a step of a walk
+constexpr int LIN_SEGMENTS = 16;  // parts of a sequence that are walked side by side, at most
+
+// One walk: out_t = scale q_t S_t, S_t = gamma S_{t-1} + k_t^T v_t, from the first
+// token to the last or back.
+struct LinJob {
+  LinHeads q, k, v, o;
+  const float* entry;  // [B][H][kw][vw] state before the first step, or NULL
+  float* exit;         // the state after the last one, or NULL
+  float* last;         // where the walk puts it: exit, or with segments a place from which it is copied
+  float* part;         // [B][H][segments - 1][kw][vw] what each segment adds to the state
+  float entry_mul, exit_mul;
+  int kw, vw;          // widths of q and k, and of v and o
+  int turned;          // from the last token to the first; entry is then not decayed by the first step, exit is once more
+  int flip_entry;      // entry is [vw][kw]
+  int slices;          // of the columns of v
+};
+
+struct LinParams {
+  LinJob job[3];
+  int jobs;
+  const float* log_decay;
+  const int32_t* lens;
+  const uint8_t* mask;  // the step's
+  int B, L, H;
+  float scale;
+  int segments, seg_chunks;  // segments of so many chunks
+};
+
+// columns of v that a workgroup takes: the state and two roundings of it fill LDS
+constexpr int lin_columns(int es, int kwp) { return es == 4 || kwp == 256 ? 32 : 64; }
+inline int lin_kwp(int kw) { return kw <= 64 ? 64 : kw <= 128 ? 128 : 256; }
+
+hipError_t launch_linear(const LinParams& P, bool bf16_path, hipStream_t st);
+constexpr int LIN_STEP_COLUMNS = 32, LIN_STEP_THREADS = 256;
+hipError_t launch_linear_step(const LinParams& P, bool bf16_path, hipStream_t st);
+
+}  // namespace msgla

@@ -8,7 +8,7 @@ from typing import Optional
 import numpy as np
 
 from . import binding
-from .config import BF16, BlockAttentionConfig, MsglaConfig, RecurrenceConfig
+from .config import BF16, BlockAttentionConfig, LayerNormConfig, LinearAttentionConfig, MsglaConfig, RecurrenceConfig
 from .synth import LayerWeights, storage_array
 
 
@@ -356,6 +356,100 @@ class DeviceBlockAttention:
             out_t = q_t.new_empty((q_t.shape[0], self.cfg.heads_q, self.cfg.d_v))
         binding.msgla_block_attention_step(self.cfg, q_t, k_t, v_t, k, v, means, pos, out_t, ws)
         return out_t
+
+
+class DeviceLayerNorm:
+    """Layer norm on device tensors.  Every call runs on the current stream of its tensors' device,
+    allocates what it returns unless given, and may be captured in a graph."""
+
+    def __init__(self, cfg: LayerNormConfig):
+        self.cfg = cfg
+
+    def forward(self, x, weight=None, bias=None, y=None):
+        """x [B, L, width], weight and bias [width] fp32 -> (y [B, L, width], mean, rstd [B, L] fp32).  y may be x."""
+        return _on(x, self._forward, x, weight, bias, y)
+
+    def _forward(self, x, weight, bias, y):
+        torch = _torch()
+        y = x.new_empty(x.shape) if y is None else y
+        mean = x.new_empty(x.shape[:2], dtype=torch.float32)
+        rstd = torch.empty_like(mean)
+        binding.msgla_layer_norm_forward(self.cfg, x, y, weight, bias, mean, rstd)
+        return y, mean, rstd
+
+    def backward(self, x, dy, mean, rstd, weight=None, bias=None, dx=None):
+        """(dx, dweight, dbias) for the forward's inputs, mean and rstd: dweight is None without a weight, dbias
+        without a bias.  dx may be dy."""
+        return _on(x, self._backward, x, dy, mean, rstd, weight, bias, dx)
+
+    def _backward(self, x, dy, mean, rstd, weight, bias, dx):
+        torch = _torch()
+        binding._dims("x", x, 3)
+        dx = x.new_empty(x.shape) if dx is None else dx
+        dweight = None if weight is None else torch.empty_like(weight)
+        dbias = None if bias is None else torch.empty_like(bias)
+        ws = None
+        if weight is not None or bias is not None:
+            n = binding.msgla_layer_norm_backward_workspace_bytes(self.cfg, x.shape[0], x.shape[1])
+            if n == 2 ** 64 - 1:
+                raise ValueError(f"invalid batch/length B={x.shape[0]} L={x.shape[1]}")
+            ws = _workspace(n, x.device)
+        binding.msgla_layer_norm_backward(self.cfg, x, dy, mean, rstd, dx, ws, weight, dweight, dbias)
+        return dx, dweight, dbias
+
+
+class DeviceLinearAttention:
+    """Linear attention with a decay per head, on device tensors.  Every call runs on the current stream of
+    its tensors' device, allocates what it returns unless given, and may be captured in a graph."""
+
+    def __init__(self, cfg: LinearAttentionConfig):
+        self.cfg = cfg
+
+    def _room(self, q, query):
+        B, L = binding._dims("q", q, 4).shape[:2]
+        n = query(self.cfg, B, L)
+        if n == 2 ** 64 - 1:
+            raise ValueError(f"invalid batch/length B={B} L={L}")
+        return _workspace(n, q.device)
+
+    def _states(self, q):
+        return q.new_empty((q.shape[0], self.cfg.heads, self.cfg.d_k, self.cfg.d_v), dtype=_torch().float32)
+
+    def forward(self, q, k, v, log_decay, lens=None, state_in=None, out=None, state_out=None):
+        """q, k [B, L, heads, d_k], v [B, L, heads, d_v], log_decay [heads] fp32 -> (out [B, L, heads, d_v], state after
+        the last token [B, heads, d_k, d_v] fp32).  lens [B] int32: tokens of each sequence.  state_out may be state_in."""
+        return _on(q, self._forward, q, k, v, log_decay, lens, state_in, out, state_out)
+
+    def _forward(self, q, k, v, log_decay, lens, state_in, out, state_out):
+        ws = self._room(q, binding.msgla_linear_attention_workspace_bytes)
+        if out is None:
+            out = q.new_empty((*q.shape[:3], self.cfg.d_v))
+        state_out = self._states(q) if state_out is None else state_out
+        binding.msgla_linear_attention_forward(self.cfg, q, k, v, log_decay, out, ws, lens, state_in, state_out)
+        return out, state_out
+
+    def backward(self, q, k, v, log_decay, dout, lens=None, state_in=None, dstate_out=None, dq=None, dk=None, dv=None):
+        """(dq, dk, dv, dstate_in) from dout and dstate_out (or None for 0); dstate_in is None without a state_in."""
+        return _on(q, self._backward, q, k, v, log_decay, dout, lens, state_in, dstate_out, dq, dk, dv)
+
+    def _backward(self, q, k, v, log_decay, dout, lens, state_in, dstate_out, dq, dk, dv):
+        ws = self._room(q, binding.msgla_linear_attention_backward_workspace_bytes)
+        dq, dk, dv = (t.new_empty(t.shape) if d is None else d for t, d in ((q, dq), (k, dk), (v, dv)))
+        dstate_in = None if state_in is None else self._states(q)
+        binding.msgla_linear_attention_backward(self.cfg, q, k, v, log_decay, dout, dq, dk, dv, ws, lens, state_in,
+                                                dstate_out, dstate_in)
+        return dq, dk, dv, dstate_in
+
+    def step(self, q_t, k_t, v_t, log_decay, state, mask=None, out_t=None, state_out=None):
+        """One token of every sequence: q_t, k_t [B, heads, d_k], v_t [B, heads, d_v] -> (out_t [B, heads, d_v], state).
+        The state is renewed in place unless state_out is given.  mask [B] uint8: 0 for sequences that stay."""
+        return _on(q_t, self._step, q_t, k_t, v_t, log_decay, state, mask, out_t, state if state_out is None else state_out)
+
+    def _step(self, q_t, k_t, v_t, log_decay, state, mask, out_t, state_out):
+        if out_t is None:
+            out_t = v_t.new_empty(v_t.shape)
+        binding.msgla_linear_attention_step(self.cfg, q_t, k_t, v_t, log_decay, state, state_out, out_t, mask)
+        return out_t, state_out
 
 
 def read_state(cfg: MsglaConfig, state, B: int) -> dict:
