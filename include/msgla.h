@@ -721,6 +721,97 @@ msgla_status msgla_linear_attention_step(const msgla_linear_config* cfg, const m
                                          const float* state_in, int64_t B, const msgla_heads* out_t,
                                          float* state_out, void* stream);
 
+/*
+ * Attention with a sliding window and first tokens that stay visible: a query at
+ * position p attends, with softmax weights, the keys j <= p with
+ *     j > p - window   or   j < n_sink.
+ * Query head g of heads_q uses key-value head g / (heads_q / heads_kv).
+ * Requirements: heads_q a multiple of heads_kv, at most 1024; d_k a multiple of
+ * 8 up to 128, d_v one up to 256; window 1 .. 2^24 (as long as the sequence: all
+ * keys before the query); n_sink 0 .. 1024; scale 1e-30 .. 1e30 (1 / sqrt(d_k) as
+ * a rule).  dtype: of q, k, v, the output and their gradients; bf16 inputs meet
+ * on bf16 matrix cores with fp32 sums (softmax weights and their gradients enter
+ * the products with 16 bits, as two bf16 values each), fp32 ones on fp32 matrix
+ * cores; a weight below 2^-126 counts as 0.
+ */
+typedef struct {
+  int32_t heads_q, heads_kv;
+  int32_t d_k, d_v;
+  int32_t window;
+  int32_t n_sink;
+  float scale;
+  int32_t dtype; /* msgla_dtype */
+} msgla_window_config;
+
+/* Device workspace (bytes) of msgla_window_attention, its backward and its step;
+ * may be 0 for the first and the last (workspace may then be NULL); (size_t)-1
+ * for an invalid configuration or size. */
+size_t msgla_window_attention_workspace_bytes(const msgla_window_config* cfg, int64_t B, int64_t L, int64_t S);
+size_t msgla_window_attention_backward_workspace_bytes(const msgla_window_config* cfg, int64_t B, int64_t L,
+                                                       int64_t S);
+size_t msgla_window_attention_step_workspace_bytes(const msgla_window_config* cfg, int64_t B, int64_t S);
+
+/*
+ * The attention: q [B][L][heads_q][d_k], k [B][S][heads_kv][d_k],
+ * v [B][S][heads_kv][d_v] -> out [B][L][heads_q][d_v], and, unless lse is NULL,
+ * lse [B][heads_q][L] fp32, the natural logarithm of each row's sum of
+ * exp(scale q . k).  Keys stand at positions 0 .. S - 1; start and lens are as in
+ * the block attention: position of query row 0, and keys that a sequence has, each
+ * [B] int32 (device) or NULL for 0 and S.  A query row at a position below 0 or
+ * not below lens[b] is padding: its output is 0, its lse minus infinity and its
+ * gradient 0.  What k and v hold behind lens[b], or at positions that no query
+ * attends, is not used.  A NaN or infinity of k, v, q or dout at a position that is
+ * used may reach every row of its sequence and key-value head.
+ */
+msgla_status msgla_window_attention(const msgla_window_config* cfg, const msgla_heads* q,
+                                    const msgla_heads* k, const msgla_heads* v, const int32_t* start,
+                                    const int32_t* lens, int64_t B, int64_t L, int64_t S,
+                                    const msgla_heads* out, float* lse, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+
+/*
+ * Its vector-Jacobian product: from dout [B][L][heads_q][d_v], with the forward's
+ * inputs, out and lse, writes dq, and dk and dv for all S positions (0 where
+ * nothing attends).  The result is the same bit for bit from call to call.
+ */
+msgla_status msgla_window_attention_backward(const msgla_window_config* cfg, const msgla_heads* q,
+                                             const msgla_heads* k, const msgla_heads* v,
+                                             const int32_t* start, const int32_t* lens,
+                                             const msgla_heads* out, const float* lse,
+                                             const msgla_heads* dout, int64_t B, int64_t L, int64_t S,
+                                             const msgla_heads* dq, const msgla_heads* dk,
+                                             const msgla_heads* dv, void* workspace,
+                                             size_t workspace_bytes, void* stream);
+
+/*
+ * Rolling caches.  A cache k [B][S][heads_kv][d_k], v [B][S][heads_kv][d_v] keeps
+ * position p in slot p below S, and a longer sequence turns over behind the first
+ * tokens: in slot n_sink + (p - n_sink) mod (S - n_sink).  It needs
+ * S >= n_sink + window for that; in a shorter one positions from S on have no
+ * place.  pos [B] int32 (device) is the number of tokens before a call; the
+ * caller advances it.
+ */
+
+/* Puts L new keys and values k_new [B][L][heads_kv][d_k], v_new [B][L][heads_kv][d_v]
+ * (lens[b] of them, at most L; NULL: all) at positions pos[b] .. (NULL: from 0 on).
+ * Of positions that share a slot the last one stays; positions without a place,
+ * or below 0, are left out. */
+msgla_status msgla_window_attention_append(const msgla_window_config* cfg, const msgla_heads* k_new,
+                                           const msgla_heads* v_new, const int32_t* pos,
+                                           const int32_t* lens, int64_t B, int64_t L, int64_t S,
+                                           const msgla_heads* k, const msgla_heads* v, void* stream);
+
+/* One streaming step of B sequences: puts each one's new key and value (k_t
+ * [B][heads_kv][d_k], v_t [B][heads_kv][d_v]) at position pos[b] and attends the
+ * window and the first tokens with q_t [B][heads_q][d_k] -> out_t
+ * [B][heads_q][d_v].  stride_t of the four _t tensors is not read.  A position
+ * without a place, or below 0, puts nothing and gives an output row of 0. */
+msgla_status msgla_window_attention_step(const msgla_window_config* cfg, const msgla_heads* q_t,
+                                         const msgla_heads* k_t, const msgla_heads* v_t,
+                                         const int32_t* pos, int64_t B, int64_t S, const msgla_heads* k,
+                                         const msgla_heads* v, const msgla_heads* out_t, void* workspace,
+                                         size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,7 +13,7 @@ import os
 from typing import Optional, Sequence
 
 from .config import (BF16, F32, BlockAttentionConfig, LayerNormConfig, LinearAttentionConfig, MsglaConfig, RECURRENCE_INPUTS,
-                     RecurrenceConfig)
+                     RecurrenceConfig, WindowAttentionConfig)
 
 MAX_BRANCHES = 8
 N_STAGES = 6
@@ -37,6 +37,9 @@ SYMBOLS = (
     "msgla_layer_norm_backward_workspace_bytes", "msgla_layer_norm_forward", "msgla_layer_norm_backward",
     "msgla_linear_attention_workspace_bytes", "msgla_linear_attention_backward_workspace_bytes",
     "msgla_linear_attention_forward", "msgla_linear_attention_backward", "msgla_linear_attention_step",
+    "msgla_window_attention_workspace_bytes", "msgla_window_attention_backward_workspace_bytes",
+    "msgla_window_attention_step_workspace_bytes", "msgla_window_attention", "msgla_window_attention_backward",
+    "msgla_window_attention_append", "msgla_window_attention_step",
 )
 NOALLOC_WORKSPACE_BYTES = 192 << 20  # MSGLA_NOALLOC_WORKSPACE_BYTES
 
@@ -117,6 +120,11 @@ class CLinearConfig(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class CWindowConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("heads_q", "heads_kv", "d_k", "d_v", "window", "n_sink")] + \
+        [("scale", ctypes.c_float), ("dtype", ctypes.c_int32)]
+
+
 class CStageEvents(ctypes.Structure):
     _fields_ = [("start", ctypes.c_void_p * N_STAGES), ("stop", ctypes.c_void_p * N_STAGES)]
 
@@ -193,6 +201,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "msgla_linear_attention_backward": (ctypes.c_int, [lin, heads, heads, heads, vp, vp, vp, heads, vp, i64, i64,
                                                            heads, heads, heads, vp, vp, sz, vp]),
         "msgla_linear_attention_step": (ctypes.c_int, [lin, heads, heads, heads, vp, vp, vp, i64, heads, vp, vp]),
+    })
+    win = ctypes.POINTER(CWindowConfig)
+    sig.update({
+        "msgla_window_attention_workspace_bytes": (sz, [win, i64, i64, i64]),
+        "msgla_window_attention_backward_workspace_bytes": (sz, [win, i64, i64, i64]),
+        "msgla_window_attention_step_workspace_bytes": (sz, [win, i64, i64]),
+        "msgla_window_attention": (ctypes.c_int, [win, heads, heads, heads, vp, vp, i64, i64, i64, heads, vp, vp, sz, vp]),
+        "msgla_window_attention_backward": (ctypes.c_int, [win, heads, heads, heads, vp, vp, heads, vp, heads, i64, i64,
+                                                           i64, heads, heads, heads, vp, sz, vp]),
+        "msgla_window_attention_append": (ctypes.c_int, [win, heads, heads, vp, vp, i64, i64, i64, heads, heads, vp]),
+        "msgla_window_attention_step": (ctypes.c_int, [win, heads, heads, heads, vp, i64, i64, heads, heads, heads, vp,
+                                                       sz, vp]),
     })
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -760,3 +780,84 @@ def msgla_linear_attention_step(cfg: LinearAttentionConfig, q_t, k_t, v_t, log_d
         _state("state_in", state_in, cfg, B, dev), B, _heads_out("out_t", out_t, value, dt, dev),
         _state("state_out", state_out, cfg, B, dev), _raw_stream(stream))
     _check("msgla_linear_attention_step", st)
+
+
+_WINDOW_CACHE: dict = {}
+
+
+def c_window_config(cfg: WindowAttentionConfig) -> CWindowConfig:
+    c = _WINDOW_CACHE.get(cfg)
+    if c is None:
+        c = _WINDOW_CACHE[cfg] = CWindowConfig(cfg.heads_q, cfg.heads_kv, cfg.d_k, cfg.d_v, cfg.window, cfg.n_sink,
+                                               cfg.scale, 1 if cfg.dtype == BF16 else 0)
+    return c
+
+
+def msgla_window_attention_workspace_bytes(cfg: WindowAttentionConfig, B: int, L: int, S: int) -> int:
+    return load_library().msgla_window_attention_workspace_bytes(ctypes.byref(c_window_config(cfg)), B, L, S)
+
+
+def msgla_window_attention_backward_workspace_bytes(cfg: WindowAttentionConfig, B: int, L: int, S: int) -> int:
+    return load_library().msgla_window_attention_backward_workspace_bytes(ctypes.byref(c_window_config(cfg)), B, L, S)
+
+
+def msgla_window_attention_step_workspace_bytes(cfg: WindowAttentionConfig, B: int, S: int) -> int:
+    return load_library().msgla_window_attention_step_workspace_bytes(ctypes.byref(c_window_config(cfg)), B, S)
+
+
+def _window_inputs(cfg, q, k, v, start, lens):
+    """(B, L, S, type, device, the C arguments of the five)"""
+    B, L = _dims("q", q, 4).shape[:2]
+    S, dt, dev = _dims("k", k, 4).shape[1], _storage(cfg), q.device
+    return B, L, S, dt, dev, (
+        _heads("q", q, (B, L, cfg.heads_q, cfg.d_k), dt, dev), _heads("k", k, (B, S, cfg.heads_kv, cfg.d_k), dt, dev),
+        _heads("v", v, (B, S, cfg.heads_kv, cfg.d_v), dt, dev), _i32("start", start, (B,), dev),
+        _i32("lens", lens, (B,), dev))
+
+
+def msgla_window_attention(cfg: WindowAttentionConfig, q, k, v, out, lse, workspace, start=None, lens=None, stream=None):
+    """q [B, L, heads_q, d_k], k [B, S, heads_kv, d_k], v [B, S, heads_kv, d_v] -> out [B, L, heads_q, d_v] and
+    lse [B, heads_q, L] fp32 (or None); start, lens: [B] int32."""
+    B, L, S, dt, dev, args = _window_inputs(cfg, q, k, v, start, lens)
+    st = load_library().msgla_window_attention(
+        c_window_config(cfg), *args, B, L, S, _heads_out("out", out, (B, L, cfg.heads_q, cfg.d_v), dt, dev),
+        _f32("lse", lse, (B, cfg.heads_q, L), dev), *_room(workspace, dev), _raw_stream(stream))
+    _check("msgla_window_attention", st)
+
+
+def msgla_window_attention_backward(cfg: WindowAttentionConfig, q, k, v, out, lse, dout, dq, dk, dv, workspace,
+                                    start=None, lens=None, stream=None):
+    B, L, S, dt, dev, args = _window_inputs(cfg, q, k, v, start, lens)
+    shape = (B, L, cfg.heads_q, cfg.d_v)
+    st = load_library().msgla_window_attention_backward(
+        c_window_config(cfg), *args, _heads("out", out, shape, dt, dev), _f32("lse", lse, (B, cfg.heads_q, L), dev),
+        _heads("dout", dout, shape, dt, dev), B, L, S, _heads_out("dq", dq, tuple(q.shape), dt, dev),
+        _heads_out("dk", dk, tuple(k.shape), dt, dev), _heads_out("dv", dv, tuple(v.shape), dt, dev),
+        *_room(workspace, dev), _raw_stream(stream))
+    _check("msgla_window_attention_backward", st)
+
+
+def msgla_window_attention_append(cfg: WindowAttentionConfig, k_new, v_new, k, v, pos=None, lens=None, stream=None):
+    """k_new [B, L, heads_kv, d_k], v_new [B, L, heads_kv, d_v] into the caches k [B, S, heads_kv, d_k] and
+    v [B, S, heads_kv, d_v] at positions pos [B] int32 (None: 0) and on; lens [B] int32: new tokens of each sequence."""
+    B, L = _dims("k_new", k_new, 4).shape[:2]
+    S, dt, dev, H = _dims("k", k, 4).shape[1], _storage(cfg), k_new.device, cfg.heads_kv
+    st = load_library().msgla_window_attention_append(
+        c_window_config(cfg), _heads("k_new", k_new, (B, L, H, cfg.d_k), dt, dev),
+        _heads("v_new", v_new, (B, L, H, cfg.d_v), dt, dev), _i32("pos", pos, (B,), dev), _i32("lens", lens, (B,), dev),
+        B, L, S, _heads_out("k", k, (B, S, H, cfg.d_k), dt, dev), _heads_out("v", v, (B, S, H, cfg.d_v), dt, dev),
+        _raw_stream(stream))
+    _check("msgla_window_attention_append", st)
+
+
+def msgla_window_attention_step(cfg: WindowAttentionConfig, q_t, k_t, v_t, k, v, pos, out_t, workspace, stream=None):
+    """q_t [B, heads_q, d_k], k_t [B, heads_kv, d_k], v_t [B, heads_kv, d_v], caches k [B, S, heads_kv, d_k] and
+    v [B, S, heads_kv, d_v], pos [B] int32 -> out_t [B, heads_q, d_v]."""
+    B, S, dt, dev = _dims("q_t", q_t, 3).shape[0], _dims("k", k, 4).shape[1], _storage(cfg), q_t.device
+    hq, hkv, dk, dv = cfg.heads_q, cfg.heads_kv, cfg.d_k, cfg.d_v
+    st = load_library().msgla_window_attention_step(
+        c_window_config(cfg), _heads("q_t", q_t, (B, hq, dk), dt, dev), _heads("k_t", k_t, (B, hkv, dk), dt, dev),
+        _heads("v_t", v_t, (B, hkv, dv), dt, dev), _i32("pos", pos, (B,), dev), B, S,
+        _heads_out("k", k, (B, S, hkv, dk), dt, dev), _heads_out("v", v, (B, S, hkv, dv), dt, dev),
+        _heads_out("out_t", out_t, (B, hq, dv), dt, dev), *_room(workspace, dev), _raw_stream(stream))
+    _check("msgla_window_attention_step", st)

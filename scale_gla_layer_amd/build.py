@@ -46,6 +46,10 @@ SOURCES = [
     "api_layer_norm.cpp",
     "k_linear.hip",
     "api_linear.cpp",
+    "k_window.hip",
+    "k_window_few.hip",
+    "k_window_grad.hip",
+    "api_window.cpp",
 ]
 
 # rocBLAS: the backward's plain products (weight and input gradients)

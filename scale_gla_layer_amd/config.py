@@ -157,6 +157,36 @@ class LinearAttentionConfig:
 
 
 @dataclasses.dataclass(frozen=True)
+class WindowAttentionConfig:
+    """Attention with a sliding window: a query at position p attends the keys j <= p with j > p - ``window`` or
+    j < ``n_sink``, the first tokens that stay visible.  ``scale`` None: 1 / sqrt(d_k)."""
+    heads_q: int
+    heads_kv: int
+    d_k: int
+    d_v: int
+    window: int
+    n_sink: int = 0
+    scale: Optional[float] = None
+    dtype: str = BF16
+
+    def __post_init__(self):
+        if self.heads_kv < 1 or not self.heads_kv <= self.heads_q <= 1024 or self.heads_q % self.heads_kv:
+            raise ValueError("heads_q must be a multiple of heads_kv, at most 1024")
+        if not 8 <= self.d_k <= 128 or self.d_k % 8 or not 8 <= self.d_v <= 256 or self.d_v % 8:
+            raise ValueError("d_k must be a multiple of 8 up to 128, d_v one up to 256")
+        if not 1 <= self.window <= 1 << 24:
+            raise ValueError("window must be 1 .. 2^24")
+        if not 0 <= self.n_sink <= 1024:
+            raise ValueError("n_sink must be 0 .. 1024")
+        if self.scale is None:
+            object.__setattr__(self, "scale", self.d_k ** -0.5)
+        if not 1e-30 <= self.scale <= 1e30:
+            raise ValueError("scale must be positive, 1e-30 .. 1e30")
+        if self.dtype not in (F32, BF16):
+            raise ValueError(f"dtype must be {F32!r} or {BF16!r}")
+
+
+@dataclasses.dataclass(frozen=True)
 class Workload:
     name: str
     cfg: MsglaConfig

@@ -1,0 +1,151 @@
+// Device helpers of the window attention: products of 32 x 32 tiles and the LDS
+// readers of their operands.
+//
+// A "slab" is 32 bytes of each of 32 rows, 16 a lane: lane l has bytes
+// 16 (l / 32) .. of row l % 32.  For bf16 it is 16 k-values and one
+// v_mfma_f32_32x32x16_bf16, for fp32 8 and four v_mfma_f32_32x32x2_f32.  The
+// result's lane l holds, of column l % 32, rows 8 (i / 4) + 4 (l / 32) + i % 4,
+// i = 0 .. 15: in turn the B operand of a product over those rows, 8 (bf16) or 4
+// values a slab, whose A operand wants columns over the same rows.
+#pragma once
+#include "block_stage.hpp"
+#include "window.hpp"
+
+namespace msgla {
+
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
+
+__device__ __forceinline__ f32x16 zero_tile() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+template <typename T> __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
+  if constexpr (sizeof(T) == 2) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  } else {
+    const f32x4 x = __builtin_bit_cast(f32x4, a), y = __builtin_bit_cast(f32x4, b);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[e], y[e], c, 0, 0, 0);
+    return c;
+  }
+}
+
+// positions of a slab of a product over positions, and the values a lane gives to it
+template <typename T> constexpr int win_slab() { return 32 / (int)sizeof(T); }
+template <typename T> constexpr int win_vals() { return 16 / (int)sizeof(T); }
+
+// The B operand of slab s from a tile of results, as one or (bf16) two values each.
+template <typename T> __device__ __forceinline__ u32x4 win_pack(const f32x16& p, int s) {
+  constexpr int N = win_vals<T>();
+  float v[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) v[e] = p[N * s + e];
+  return pack16<T>(v);
+}
+template <typename T> __device__ __forceinline__ void win_split(const f32x16& p, int s, u32x4& hi, u32x4& lo) {
+  if constexpr (sizeof(T) == 2) {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = p[8 * s + e];
+    split_bf16(v, hi, lo);
+  } else {
+    hi = win_pack<T>(p, s);
+    lo = zero16();
+  }
+}
+
+// Tiles of rows of W 16-byte pieces, piece p of row r at p ^ tile_key(r).
+// Slab s of rows 32 t + l % 32.
+template <int W> struct Rows32 {
+  int at;
+  __device__ Rows32(int lane) {
+    const int r = lane & 31;
+    at = r * W * 16 + (((lane >> 5) ^ tile_key<W>(r)) * 16);
+  }
+  __device__ __forceinline__ u32x4 read(const char* lds, int t, int s) const { return ld16(lds + (at ^ (32 * s)) + t * 32 * W * 16); }
+};
+
+// Columns 32 t .. + 31 over slab s's positions.
+template <typename T, int W> struct Columns32;
+template <int W> struct Columns32<bf16, W> {
+  int at0, at1;
+  __device__ Columns32(int lane) {
+    const int g = lane >> 4, e = (lane >> 2) & 3, c = lane & 3, r = 4 * (g >> 1) + e, p = 2 * (g & 1) + (c >> 1);
+    at0 = r * W * 16 + ((p ^ tile_key<W>(r)) * 16) + 8 * (c & 1);
+    at1 = (r + 8) * W * 16 + ((p ^ tile_key<W>(r + 8)) * 16) + 8 * (c & 1);
+  }
+  __device__ __forceinline__ u32x4 read(const char* lds, int s, int t) const {
+    const char* base = lds + s * 16 * W * 16;
+    const blk_v4s lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((blk_lds_v4s*)(base + (at0 ^ (64 * t))));
+    const blk_v4s hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((blk_lds_v4s*)(base + (at1 ^ (64 * t))));
+    const u32x2 x = __builtin_bit_cast(u32x2, lo), y = __builtin_bit_cast(u32x2, hi);
+    return u32x4{x[0], x[1], y[0], y[1]};
+  }
+};
+template <int W> struct Columns32<float, W> {
+  static_assert(W >= 16, "swizzle of four bits");
+  int at[4];
+  __device__ Columns32(int lane) {
+    const int h = lane >> 5, c = lane & 31;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int r = 4 * h + j;
+      at[j] = r * W * 16 + (((c >> 2) ^ tile_key<W>(r)) * 16) + 4 * (c & 3);
+    }
+  }
+  __device__ __forceinline__ u32x4 read(const char* lds, int s, int t) const {
+    u32x4 v;  // row bit 3 changes bit 0 of the key
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = *reinterpret_cast<const uint32_t*>(lds + (at[j] ^ (128 * t) ^ ((s & 1) << 4)) + s * 8 * W * 16);
+    return v;
+  }
+};
+
+// 4 consecutive columns of a result tile: 32 t + 8 i + 4 (l / 32)
+__device__ __forceinline__ int win_column(int t, int i, int lane) { return 32 * t + 8 * i + 4 * (lane >> 5); }
+
+// A query's position, or -1 for padding: behind the sequence's keys, or before its start.
+__device__ __forceinline__ int win_position(const WinParams& P, int b, int i) {
+  if (i >= P.L) return -1;
+  const int64_t p = (P.start ? (int64_t)P.start[b] : 0) + i;
+  const int len = P.lens ? min(P.lens[b], P.S) : P.S;
+  return p >= 0 && p < len ? (int)p : -1;
+}
+
+// What a lane knows of its row of a tile.
+struct WinRow {
+  int i, head, p;  // query, query head, position
+  bool in;         // a row of the problem (of padding, if p < 0)
+  __device__ WinRow(const WinParams& P, int b, int h, int t, int r) {
+    const int i0 = P.GT > 1 ? t / P.GT : t * P.QT, g0 = P.GT > 1 ? (t % P.GT) * P.tile_rows : 0;
+    const int qi = P.GT > 1 ? 0 : r / P.G, g = P.GT > 1 ? g0 + r : r - qi * P.G;
+    i = i0 + qi;
+    head = h * P.G + g;
+    in = (P.GT > 1 || qi < P.QT) && g < P.G && i < P.L;
+    p = in ? win_position(P, b, i) : -1;
+  }
+};
+
+__device__ __forceinline__ const char* win_at(const WinHeads& t, int64_t b, int64_t i, int64_t h) {
+  return t.p + b * t.sb + i * t.st + h * t.sh;
+}
+__device__ __forceinline__ char* win_out(const WinHeads& t, int64_t b, int64_t i, int64_t h) {
+  return t.p + b * t.sb + i * t.st + h * t.sh;
+}
+
+__device__ __forceinline__ int wave_min(int v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v = min(v, __shfl_xor(v, o));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+__device__ __forceinline__ int wave_max(int v) {
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) v = max(v, __shfl_xor(v, o));
+  return __builtin_amdgcn_readfirstlane(v);
+}
+
+}  // namespace msgla

@@ -8,7 +8,8 @@ from typing import Optional
 import numpy as np
 
 from . import binding
-from .config import BF16, BlockAttentionConfig, LayerNormConfig, LinearAttentionConfig, MsglaConfig, RecurrenceConfig
+from .config import (BF16, BlockAttentionConfig, LayerNormConfig, LinearAttentionConfig, MsglaConfig, RecurrenceConfig,
+                     WindowAttentionConfig)
 from .synth import LayerWeights, storage_array
 
 
@@ -450,6 +451,65 @@ class DeviceLinearAttention:
             out_t = v_t.new_empty(v_t.shape)
         binding.msgla_linear_attention_step(self.cfg, q_t, k_t, v_t, log_decay, state, state_out, out_t, mask)
         return out_t, state_out
+
+
+class DeviceWindowAttention:
+    """Attention with a sliding window and first tokens that stay visible, on device tensors.  Every call runs on
+    the current stream of its tensors' device, allocates what it returns unless given, and may be captured in a graph."""
+
+    def __init__(self, cfg: WindowAttentionConfig):
+        self.cfg = cfg
+
+    def _room(self, query, device, *sizes):
+        n = query(self.cfg, *sizes)
+        if n == 2 ** 64 - 1:
+            raise ValueError(f"invalid sizes {sizes}")
+        return _workspace(n, device)
+
+    def forward(self, q, k, v, start=None, lens=None, out=None, lse=None):
+        """q [B, L, heads_q, d_k], k [B, S, heads_kv, d_k], v [B, S, heads_kv, d_v] -> (out [B, L, heads_q, d_v],
+        lse [B, heads_q, L] fp32).  start [B] int32: position of the first query; lens [B] int32: keys of a sequence."""
+        return _on(q, self._forward, q, k, v, start, lens, out, lse)
+
+    def _forward(self, q, k, v, start, lens, out, lse):
+        B, L = binding._dims("q", q, 4).shape[:2]
+        ws = self._room(binding.msgla_window_attention_workspace_bytes, q.device, B, L, binding._dims("k", k, 4).shape[1])
+        if out is None:
+            out = q.new_empty((B, L, self.cfg.heads_q, self.cfg.d_v))
+        if lse is None:
+            lse = q.new_empty((B, self.cfg.heads_q, L), dtype=_torch().float32)
+        binding.msgla_window_attention(self.cfg, q, k, v, out, lse, ws, start, lens)
+        return out, lse
+
+    def backward(self, q, k, v, out, lse, dout, start=None, lens=None, dq=None, dk=None, dv=None):
+        """(dq, dk, dv) for the forward's inputs, out and lse."""
+        return _on(q, self._backward, q, k, v, out, lse, dout, start, lens, dq, dk, dv)
+
+    def _backward(self, q, k, v, out, lse, dout, start, lens, dq, dk, dv):
+        B, L = binding._dims("q", q, 4).shape[:2]
+        ws = self._room(binding.msgla_window_attention_backward_workspace_bytes, q.device, B, L,
+                        binding._dims("k", k, 4).shape[1])
+        dq, dk, dv = (t.new_empty(t.shape) if d is None else d for t, d in ((q, dq), (k, dk), (v, dv)))
+        binding.msgla_window_attention_backward(self.cfg, q, k, v, out, lse, dout, dq, dk, dv, ws, start, lens)
+        return dq, dk, dv
+
+    def append(self, k_new, v_new, k, v, pos=None, lens=None):
+        """A prefill's keys and values k_new [B, L, heads_kv, d_k], v_new [B, L, heads_kv, d_v] into rolling caches k, v of
+        S slots, from positions pos [B] int32 (None: 0) on; lens [B] int32: new tokens of each sequence."""
+        _on(k_new, binding.msgla_window_attention_append, self.cfg, k_new, v_new, k, v, pos, lens)
+
+    def step(self, q_t, k_t, v_t, k, v, pos, out_t=None):
+        """One token of every sequence: puts k_t, v_t at position pos [B] int32 of the rolling caches and attends:
+        out_t [B, heads_q, d_v].  The caller advances pos."""
+        return _on(q_t, self._step, q_t, k_t, v_t, k, v, pos, out_t)
+
+    def _step(self, q_t, k_t, v_t, k, v, pos, out_t):
+        B = binding._dims("q_t", q_t, 3).shape[0]
+        ws = self._room(binding.msgla_window_attention_step_workspace_bytes, q_t.device, B, binding._dims("k", k, 4).shape[1])
+        if out_t is None:
+            out_t = q_t.new_empty((B, self.cfg.heads_q, self.cfg.d_v))
+        binding.msgla_window_attention_step(self.cfg, q_t, k_t, v_t, k, v, pos, out_t, ws)
+        return out_t
 
 
 def read_state(cfg: MsglaConfig, state, B: int) -> dict:

@@ -1,9 +1,10 @@
-"""CPU: the 64-bit references of layer norm and linear attention against formulas of their own and
+"""CPU: the 64-bit references of layer norm, linear attention and window attention against formulas of their own and
 differences."""
 import pytest
 import torch
 
-from tests import layer_norm_ref, linear_ref
+from scale_gla_layer_amd.config import WindowAttentionConfig
+from tests import layer_norm_ref, linear_ref, window_ref
 
 
 def _g(seed):
@@ -81,3 +82,41 @@ def test_linear_without_memory():
     (out, last), _ = linear_ref.walk(q, k, v, torch.tensor([-float("inf")], dtype=torch.float64), [3], None, 1.0, "f32")
     assert torch.allclose(out, (q * k).sum(3, keepdim=True) * v)
     assert torch.allclose(last[0, 0], torch.outer(k[0, 2, 0], v[0, 2, 0]))
+
+
+@pytest.mark.parametrize("window,n_sink,start,lens", [(3, 0, None, None), (2, 2, [0, 3], [9, 6]), (20, 0, [1, -2], None),
+                                                      (1, 1, None, [0, 5])])
+def test_window(window, n_sink, start, lens):
+    g = _g(21)
+    B, L, S, hq, hkv, dk, dv = 2, 7, 9, 4, 2, 8, 16
+    cfg = WindowAttentionConfig(hq, hkv, dk, dv, window, n_sink, dtype="f32")
+    r = lambda *n: torch.randn(n, generator=g, dtype=torch.float64)  # noqa: E731
+    q, k, v, do = r(B, L, hq, dk), r(B, S, hkv, dk), r(B, S, hkv, dv), r(B, L, hq, dv)
+    got, _, _ = window_ref.forward(q, k, v, cfg, start, lens)
+    for b in range(B):
+        for i in range(L):
+            p = i + (start[b] if start else 0)
+            n = min(lens[b], S) if lens else S
+            for h in range(hq):
+                keys = [j for j in range(S) if j <= p and (p - j < window or j < n_sink)] if 0 <= p < n else []
+                if not keys:
+                    assert (got["out"][b, i, h] == 0).all() and got["lse"][b, h, i] == -torch.inf
+                    continue
+                s = k[b, keys, h // 2] @ q[b, i, h] * cfg.scale
+                assert torch.allclose(got["lse"][b, h, i], torch.logsumexp(s, 0))
+                assert torch.allclose(got["out"][b, i, h], torch.softmax(s, 0) @ v[b, keys, h // 2])
+    loss = lambda *a: float((window_ref.forward(*a, cfg, start, lens)[0]["out"] * do).sum())  # noqa: E731
+    grads, _ = window_ref.backward(q, k, v, do, cfg, start, lens)
+    _agree(grads["dq"], _differences(lambda t: loss(t, k, v), q, 25, 22))
+    _agree(grads["dk"], _differences(lambda t: loss(q, t, v), k, 25, 23))
+    _agree(grads["dv"], _differences(lambda t: loss(q, k, t), v, 25, 24))
+
+
+def test_window_slots():
+    """A rolling cache of n_sink + window slots holds exactly what the next query attends."""
+    for S, n_sink, window in ((7, 2, 5), (8, 0, 5), (12, 3, 5)):
+        held = {}
+        for p in range(40):
+            held[window_ref.slot(p, S, n_sink)] = p
+            want = [j for j in range(p + 1) if j > p - window or j < n_sink]
+            assert set(want) <= set(held.values()) and len(held) <= S
