@@ -47,6 +47,7 @@ SOURCES = [
     "k_linear.hip",
     "api_linear.cpp",
     "k_window.hip",
+    "k_window_dq.hip",
     "k_window_few.hip",
     "k_window_grad.hip",
     "api_window.cpp",

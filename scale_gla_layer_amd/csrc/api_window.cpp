@@ -9,6 +9,7 @@ using namespace msgla::host;
 namespace {
 
 constexpr size_t BAD = (size_t)-1;
+constexpr int N_CU = 256;
 
 bool win_config_ok(const msgla_window_config* c) {
   if (!c || (c->dtype != MSGLA_F32 && c->dtype != MSGLA_BF16)) return false;
@@ -45,9 +46,8 @@ void set_tiles(WinParams& P, int rows) {
   P.tiles = (int64_t)P.B * P.Hkv * P.tiles_per_seq;
 }
 // tiles of the workgroups of k_window
-void set_many(WinParams& P, int es, bool gradient) {
-  set_tiles(P, WIN_ROWS * win_waves(es, win_dkp(P.dkw), win_dvp(P.dvw), gradient));
-}
+void set_many(WinParams& P) { set_tiles(P, WIN_ROWS * WIN_TILES); }
+int pairs_of(const WinParams& P, int es) { return win_pairs(es, win_dvp(P.dvw)); }
 
 WinParams win_params(const msgla_window_config* c, int64_t B, int64_t L, int64_t S) {
   WinParams P{};
@@ -103,45 +103,48 @@ bool few_grid_ok(const WinParams& P) {
   return launch_ok(P.tiles * P.parts, 64 * WIN_FEW_WAVES) && launch_ok(P.tiles * WIN_FEW_ROWS, 64) &&
          P.tiles <= INT32_MAX;
 }
-bool many_grid_ok(const WinParams& P) { return launch_ok(P.tiles + N_XCD, 512); }
+bool many_grid_ok(const WinParams& P) { return launch_ok(P.tiles + N_XCD, 4 * P.tile_rows); }
 
 // Whether the forward deals keys to workgroups: where the tiles of many rows leave
 // most CUs without one.
-bool use_few(WinParams P, int es) {
-  set_many(P, es, false);
-  return P.tiles < 96;
+bool use_few(WinParams P) {
+  set_many(P);
+  return P.tiles < 192;
 }
 
 struct GradWs {
-  size_t delta, part, sink_part, total;
+  size_t delta, nref, part, sink_part, total;
 };
 GradWs set_grad(WinParams& P, int es) {
-  set_many(P, es, true);
+  P.key_tile = 32 * pairs_of(P, es);
+  set_tiles(P, WIN_ROWS * pairs_of(P, es));
   const int64_t heads = (int64_t)P.B * P.Hkv;
-  P.key_tiles = cdiv(P.S, WIN_KEYS);
-  const int64_t queries = std::min<int64_t>(P.L, (int64_t)P.window + WIN_KEYS - 1);
+  P.key_tiles = cdiv(P.S, P.key_tile);
+  const int64_t queries = std::min<int64_t>(P.L, (int64_t)P.window + P.key_tile - 1);
   const int64_t sets = (queries * P.G + 31) / 32;
-  P.key_parts = (int)std::max<int64_t>(1, std::min<int64_t>((511 + heads * P.key_tiles) / (heads * P.key_tiles), sets / 16));
+  // Workgroups fill a CU each: as many as there are CUs, of four sets of 32 rows at least.
+  P.key_parts = (int)std::max<int64_t>(1, std::min<int64_t>((N_CU - 1 + heads * P.key_tiles) / (heads * P.key_tiles), sets / 4));
   const int sinks = std::min(P.n_sink, P.S);
   P.sink_tiles = P.S > P.window ? cdiv(sinks, WIN_SINK) : 0;
   if (P.sink_tiles > 0) {
     const int64_t rows = (int64_t)std::min(P.L, P.S - P.window) * P.G;
-    P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>((511 + heads * P.sink_tiles) / (heads * P.sink_tiles), rows / 512));
+    P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>((4 * N_CU - 1 + heads * P.sink_tiles) / (heads * P.sink_tiles), rows / 128));
   }
-  P.joined = P.key_parts > 1 ? P.key_tiles : P.sink_tiles > 0 ? cdiv(sinks, WIN_KEYS) : 0;
+  P.joined = P.key_parts > 1 ? P.key_tiles : P.sink_tiles > 0 ? cdiv(sinks, P.key_tile) : 0;
   const size_t width = (size_t)(win_dkp(P.dkw) + win_dvp(P.dvw)) * 4;
   GradWs w{};
   Take take;
   w.delta = take((size_t)P.B * P.Hq * P.L * 4);
-  w.part = take((size_t)heads * P.joined * P.key_parts * WIN_KEYS * width);
-  w.sink_part = take((size_t)heads * P.sink_tiles * P.sink_parts * 4 * WIN_SINK * width);
+  w.nref = take((size_t)P.B * P.Hq * P.L * 4);
+  w.part = take((size_t)heads * P.joined * P.key_parts * P.key_tile * width);
+  w.sink_part = take((size_t)heads * P.sink_tiles * P.sink_parts * WIN_SINK * width);
   w.total = take.cur;
   return w;
 }
 bool grad_grid_ok(const WinParams& P) {
   const int64_t heads = (int64_t)P.B * P.Hkv;
-  return many_grid_ok(P) && launch_ok(heads * P.key_tiles * P.key_parts + N_XCD, 256) &&
-         launch_ok(heads * P.sink_tiles * P.sink_parts + N_XCD, 256) && launch_ok(heads * P.joined * (WIN_KEYS / 4) + 1, 256);
+  return many_grid_ok(P) && launch_ok(heads * P.key_tiles * P.key_parts + N_XCD, 4 * P.key_tile) &&
+         launch_ok(heads * P.sink_tiles * P.sink_parts + N_XCD, 128) && launch_ok(heads * P.joined * P.key_tile, 256);
 }
 
 }  // namespace
@@ -151,7 +154,7 @@ extern "C" {
 size_t msgla_window_attention_workspace_bytes(const msgla_window_config* cfg, int64_t B, int64_t L, int64_t S) {
   if (!win_config_ok(cfg) || !win_sizes_ok(B, L, S)) return BAD;
   WinParams P = win_params(cfg, B, L, S);
-  return use_few(P, es_of(cfg)) ? set_few(P).total : 0;
+  return use_few(P) ? set_few(P).total : 0;
 }
 
 size_t msgla_window_attention_backward_workspace_bytes(const msgla_window_config* cfg, int64_t B, int64_t L, int64_t S) {
@@ -183,7 +186,7 @@ msgla_status msgla_window_attention(const msgla_window_config* cfg, const msgla_
   P.start = start;
   P.lens = lens;
   P.lse = lse;
-  const bool few = use_few(P, es);
+  const bool few = use_few(P);
   if (few) {
     const FewWs w = set_few(P);
     if (!few_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
@@ -193,9 +196,9 @@ msgla_status msgla_window_attention(const msgla_window_config* cfg, const msgla_
     HIP_TRY(launch_window_few(P, false, es == 2, static_cast<hipStream_t>(stream)));
     return MSGLA_OK;
   }
-  set_many(P, es, false);
+  set_many(P);
   if (!many_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
-  HIP_TRY(launch_window(P, false, es == 2, static_cast<hipStream_t>(stream)));
+  HIP_TRY(launch_window(P, es == 2, static_cast<hipStream_t>(stream)));
   return MSGLA_OK;
 }
 
@@ -211,7 +214,7 @@ msgla_status msgla_window_attention_backward(const msgla_window_config* cfg, con
       !heads_ok(dq, es) || !heads_ok(dk, es) || !heads_ok(dv, es) || !i32_ok(start) || !i32_ok(lens) || !lse || !i32_ok(lse))
     return MSGLA_ERR_INVALID_ARG;
   WinParams P = win_params(cfg, B, L, S);
-  const GradWs w = set_grad(P, es);
+  const GradWs w = set_grad(P, es_of(cfg));
   if (!grad_grid_ok(P)) return MSGLA_ERR_UNSUPPORTED;
   if (!workspace || !aligned16(workspace)) return MSGLA_ERR_INVALID_ARG;
   if (workspace_bytes < w.total) return MSGLA_ERR_WORKSPACE;
@@ -227,9 +230,10 @@ msgla_status msgla_window_attention_backward(const msgla_window_config* cfg, con
   P.lens = lens;
   P.lse_in = lse;
   P.delta = at<float>(workspace, w.delta);
+  P.nref = at<float>(workspace, w.nref);
   P.part = at<float>(workspace, w.part);
   P.sink_part = at<float>(workspace, w.sink_part);
-  HIP_TRY(launch_window(P, true, es == 2, static_cast<hipStream_t>(stream)));
+  HIP_TRY(launch_window_dq(P, es == 2, static_cast<hipStream_t>(stream)));
   HIP_TRY(launch_window_dkdv(P, es == 2, static_cast<hipStream_t>(stream)));
   return MSGLA_OK;
 }

@@ -8,6 +8,8 @@
 // i = 0 .. 15: in turn the B operand of a product over those rows, 8 (bf16) or 4
 // values a slab, whose A operand wants columns over the same rows.
 #pragma once
+#include <type_traits>
+
 #include "block_stage.hpp"
 #include "window.hpp"
 
@@ -104,6 +106,92 @@ template <int W> struct Columns32<float, W> {
     return v;
   }
 };
+
+// Copies of units of KT rows of W pieces into stage tiles, dealt to a workgroup's
+// waves: a unit's rows from one address on, or each chosen by `key`.  Pieces behind
+// the rows' width repeat the first one: they meet zeroes or columns that are not
+// stored.
+template <int W, int KT, int WAVES> struct UnitCopy {
+  static constexpr int ALL = KT * W / 64, N = (ALL + WAVES - 1) / WAVES;  // copy instructions, and a wave's
+  static_assert(KT * W % 64 == 0, "whole copy instructions");
+  const char* base;
+  int64_t st;
+  uint32_t off[N];  // from the unit's first row
+  __device__ UnitCopy(const char* b, int64_t stride, int width, int wave, int lane) : base(b), st(stride) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int pc = 64 * (wave + WAVES * i) + lane, r = pc / W, p = (pc % W) ^ tile_key<W>(r);
+      off[i] = (uint32_t)r * (uint32_t)st + (p * 16 < width ? p * 16 : 0);
+    }
+  }
+  // whether 32 bits hold the offsets
+  __device__ __forceinline__ bool near() const { return st <= 0x7fffffff / KT; }
+  __device__ __forceinline__ void whole(int64_t k0, char* lds, int wave) const {
+    const char* first = base + k0 * st;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (ALL % WAVES == 0 || wave + WAVES * i < ALL) dma16(first + off[i], lds + 1024 * (wave + WAVES * i));
+  }
+  template <class Key> __device__ __forceinline__ void chosen(int width, char* lds, int wave, int lane, Key key) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int pc = 64 * (wave + WAVES * i) + lane, r = pc / W, p = (pc % W) ^ tile_key<W>(r);
+      if (ALL % WAVES == 0 || wave + WAVES * i < ALL)
+        dma16(base + key(r) * st + (p * 16 < width ? p * 16 : 0), lds + 1024 * (wave + WAVES * i));
+    }
+  }
+};
+
+// Two values as one or (bf16) two operand words: hi + lo.
+__device__ __forceinline__ uint32_t win_pair(float a, float b) {
+  typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+  return __builtin_bit_cast(uint32_t, bf16x2{(bf16)a, (bf16)b});
+}
+
+// A tile of 32 x 32 weights as the B operands of a product over its rows.
+template <typename T> struct Weights;
+template <> struct Weights<bf16> {
+  static constexpr int SLABS = 2;
+  uint32_t hi[8], lo[8];
+  __device__ __forceinline__ void set(int i, float a, float b) {  // rows 2 i and 2 i + 1 of the lane's
+    hi[i] = win_pair(a, b);
+    lo[i] = win_pair(a - u2f(hi[i] << 16), b - u2f(hi[i] & 0xffff0000u));
+  }
+  __device__ __forceinline__ void set_hi(int i, float a, float b) { hi[i] = win_pair(a, b); }
+  // a product with the weights as they are, and with their higher halves alone
+  __device__ __forceinline__ f32x16 mma_hi(u32x4 f, int s, f32x16 c) const {
+    return mma32<bf16>(f, u32x4{hi[4 * s], hi[4 * s + 1], hi[4 * s + 2], hi[4 * s + 3]}, c);
+  }
+  __device__ __forceinline__ f32x16 mma(u32x4 f, int s, f32x16 c) const {
+    c = mma32<bf16>(f, u32x4{hi[4 * s], hi[4 * s + 1], hi[4 * s + 2], hi[4 * s + 3]}, c);
+    return mma32<bf16>(f, u32x4{lo[4 * s], lo[4 * s + 1], lo[4 * s + 2], lo[4 * s + 3]}, c);
+  }
+};
+template <> struct Weights<float> {
+  static constexpr int SLABS = 4;
+  float v[16];
+  __device__ __forceinline__ void set(int i, float a, float b) { v[2 * i] = a, v[2 * i + 1] = b; }
+  __device__ __forceinline__ f32x16 mma(u32x4 f, int s, f32x16 c) const {
+    return mma32<float>(f, u32x4{f2u(v[4 * s]), f2u(v[4 * s + 1]), f2u(v[4 * s + 2]), f2u(v[4 * s + 3])}, c);
+  }
+};
+
+// A tile of results that one wave of a pair leaves for the other, lane by lane.
+constexpr int TILE_BYTES = 64 * 64;
+__device__ __forceinline__ void tile_put(char* lds, const f32x16& t, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) st16(lds + (i * 64 + lane) * 16, u32x4{f2u(t[4 * i]), f2u(t[4 * i + 1]), f2u(t[4 * i + 2]), f2u(t[4 * i + 3])});
+}
+__device__ __forceinline__ f32x16 tile_get(const char* lds, int lane) {
+  f32x16 t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x4 v = __builtin_bit_cast(f32x4, ld16(lds + (i * 64 + lane) * 16));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) t[4 * i + e] = v[e];
+  }
+  return t;
+}
 
 // 4 consecutive columns of a result tile: 32 t + 8 i + 4 (l / 32)
 __device__ __forceinline__ int win_column(int t, int i, int lane) { return 32 * t + 8 * i + 4 * (lane >> 5); }
