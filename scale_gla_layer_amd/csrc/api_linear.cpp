@@ -70,21 +70,13 @@ LinParams lin_params(const msgla_linear_config* c, int64_t B, int64_t L, bool gr
   return P;
 }
 
-// The states of the segments, and the last one's where the call returns it; their
-// size, and with a workspace their places.
+// The states before the segments: their size, and with a workspace their places.
 size_t lin_room(LinParams& P, void* ws) {
-  if (P.segments == 1) {
-    for (int i = 0; i < P.jobs; ++i) P.job[i].last = P.job[i].exit;
-    return 0;
-  }
   size_t cur = 0;
-  for (int i = 0; i < P.jobs; ++i) {
+  for (int i = 0; i < P.jobs && P.segments > 1; ++i) {
     LinJob& J = P.job[i];
-    const size_t one = (size_t)P.B * P.H * J.kw * J.vw * 4;
     if (ws) J.part = at<float>(ws, cur);
-    cur += align256(one * (P.segments - 1));
-    if (ws) J.last = at<float>(ws, cur);
-    if (!J.flip_entry) cur += align256(one);  // only such a job has a last state to return
+    cur += align256((size_t)P.B * P.H * P.segments * J.kw * J.vw * 4);
   }
   return cur;
 }

@@ -10,8 +10,8 @@
 // operand of the next chunk's product.  All exponents of gamma are at least 0, so
 // nothing overflows, and a decay of 0 (log_decay of minus infinity) is exact.
 //   Few sequences and heads: each sequence is cut into segments, what each adds
-// to the state is formed first (from zero, without outputs), and the walks
-// then begin with the states that these sum up to.
+// to the state is formed first (from zero, without outputs), a small kernel sums up
+// the states before the segments, and the walks begin with these.
 //   The gradients are walks themselves: with do the output's gradient, dq is that
 // of (do, v, k), and from the last token to the first dk is that of (v, do, q) and
 // dv that of (k, q, do), whose state is the state's gradient.  Three jobs of a launch.
@@ -22,6 +22,8 @@
 //   The products' layouts chain without exchanges between lanes: A^T = K Q^T holds
 // a row's weights where out^T = V^T A^T wants them, and S as the sum of K^T V has
 // four neighbouring rows a lane, which is 8 bytes of the transposed state in LDS.
+#include <algorithm>
+
 #include "block_device.hpp"
 #include "linear.hpp"
 
@@ -41,11 +43,46 @@ __device__ __forceinline__ int lin_len(const LinParams& P, int b) {
   return P.lens ? max(0, min(P.lens[b], P.L)) : P.L;
 }
 
-// A sequence's tokens in the order of the walk; positions behind its end keep their place.
-struct LinOrder {
-  int len;
-  bool turned;
-  __device__ __forceinline__ int64_t at(int n) const { return turned && n < len ? len - 1 - n : n; }
+// 16-byte pieces of rows of W pieces that a thread copies to LDS a chunk: rows of
+// positions that follow one another, or (turned) that go back.  There are no
+// conditional loads, each of which would be waited for on its own: rows behind the
+// last one repeat it, and pieces behind the width the first one, which `put` makes zero.
+template <int W, int THREADS> struct LinCopy {
+  static constexpr int N = LIN_CHUNK * W / THREADS;
+  const char* base;
+  int64_t st;
+  int tid, width;
+  u32x4 r[N];
+  int32_t off[N];
+  bool near;
+  __device__ LinCopy(const char* b, int64_t stride, int w, bool turned, int t) : base(b), st(turned ? -stride : stride), tid(t), width(w) {
+    near = stride <= 0x7fffffff / (2 * LIN_CHUNK);
+#pragma unroll
+    for (int i = 0; i < N; ++i) off[i] = row(i) * (int)st + byte(i);
+  }
+  __device__ __forceinline__ int row(int i) const { return (tid + THREADS * i) / W; }
+  __device__ __forceinline__ int byte(int i) const {
+    const int at = (tid + THREADS * i) % W * 16;
+    return at < width ? at : 0;
+  }
+  // n rows from the position `first` on
+  __device__ __forceinline__ void fetch(int64_t first, int n) {
+    const char* p = base + first * (st < 0 ? -st : st);
+    if (n >= LIN_CHUNK && near) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = ld16(p + off[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = ld16(p + min(row(i), n - 1) * st + byte(i));
+    }
+  }
+  template <int PITCH> __device__ __forceinline__ void put(char* lds, bool zeroes) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = (tid + THREADS * i) % W * 16;
+      st16(lds + row(i) * PITCH + at, zeroes && at >= width ? zero16() : r[i]);
+    }
+  }
 };
 
 // Two workgroups a CU where LDS holds them.
@@ -57,7 +94,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_l
   constexpr int SL = C / blk_slab<T>();        // slabs of a chunk's positions
   constexpr int KP = blk_pitch<T, KWP>(), VP = blk_pitch<T, VS>();
   constexpr bool LO = ES == 2;
-  constexpr int NK = C * KWP * ES / 16 / 256, NV = C * VS * ES / 16 / 256;  // pieces a thread copies
   __shared__ __attribute__((aligned(16))) char ks[C * KP];
   __shared__ __attribute__((aligned(16))) char vs[C * VP];
   __shared__ __attribute__((aligned(16))) char ss[OUT ? (LO ? 2 : 1) * VS * KP : 16];  // state^T [column][row], hi and lo
@@ -71,10 +107,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_l
   if (blockIdx.x / N_XCD >= (unsigned)((total + N_XCD - 1) / N_XCD) || w >= total) return;
   const int slice = w % J.slices, seg = w / J.slices % nseg, bh = w / J.slices / nseg, b = bh / P.H, h = bh - b * P.H;
   const int len = lin_len(P, b), v0 = slice * VS;
-  const LinOrder order{len, J.turned != 0};
   const float lg2 = lin_log2(P.log_decay, h);
   const int first = seg * P.seg_chunks * C, past = min(P.L, first + P.seg_chunks * C);
-  const int kw = J.kw * ES, vw = (J.vw - v0) * ES;  // bytes of a row, and of its part behind v0
+  const int kw = J.kw * ES, vw = min(VS, J.vw - v0) * ES;  // bytes of a row, and of its part
+  const bool turned = J.turned != 0;
 
   f32x4 S[KT][VT];
 #pragma unroll
@@ -82,32 +118,30 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_l
 #pragma unroll
     for (int j = 0; j < VT; ++j) S[i][j] = zero4();
   // rows 16 (KT wave + i) + 4 a + e, column v0 + 16 j + c16 of a state
-  auto each = [&](auto f) {
+  auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
       for (int j = 0; j < VT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int r = 16 * (KT * wave + i) + 4 * a + e, c = v0 + 16 * j + c16;
-          if (r < J.kw && c < J.vw) f(S[i][j], e, r, c);
-        }
+        for (int e = 0; e < 4; ++e) f(S[i][j], e, 16 * (KT * wave + i) + 4 * a + e, v0 + 16 * j + c16);
+  };
+  auto load = [&](const float* p, bool flip, float mul) __attribute__((always_inline)) {
+    each([&](f32x4& s, int e, int r, int c) {
+      const int64_t row = min(r, J.kw - 1), column = min(c, J.vw - 1);
+      s[e] = p[flip ? column * J.kw + row : row * J.vw + column];
+    });
+    each([&](f32x4& s, int e, int r, int c) { s[e] = r < J.kw && c < J.vw ? s[e] * mul : 0.f; });
+  };
+  auto store = [&](float* p, float mul) __attribute__((always_inline)) {
+    each([&](f32x4& s, int e, int r, int c) {
+      if (r < J.kw && c < J.vw) p[(int64_t)r * J.vw + c] = s[e] * mul;
+    });
   };
   const int64_t size = (int64_t)J.kw * J.vw;
   if constexpr (OUT) {
-    if (J.entry) {
-      const float* p = J.entry + bh * size;
-      each([&](f32x4& s, int e, int r, int c) {
-        s[e] = p[J.flip_entry ? (int64_t)c * J.kw + r : (int64_t)r * J.vw + c] * J.entry_mul;
-      });
-    }
-    for (int m = 0; m < seg; ++m) {
-      const int begin = m * P.seg_chunks * C, n = max(0, min(len - begin, P.seg_chunks * C));
-      if (!n) break;
-      const float keep = lin_power(n - (m == 0 ? J.turned : 0), lg2);
-      const float* p = J.part + ((int64_t)bh * (P.segments - 1) + m) * size;
-      each([&](f32x4& s, int e, int r, int c) { s[e] = keep * s[e] + p[(int64_t)r * J.vw + c]; });
-    }
+    if (P.segments > 1) load(J.part + ((int64_t)bh * P.segments + seg) * size, false, 1.f);
+    else if (J.entry) load(J.entry + bh * size, J.flip_entry, J.entry_mul);
   }
 
   // decays within a chunk, for the lane's row 16 wave + c16 and its positions
@@ -134,41 +168,29 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_l
   set_left(C);
   const float keep_whole = lin_power(C, lg2);
 
-  const char *qb = J.q.p + b * J.q.sb + h * J.q.sh, *kb = J.k.p + b * J.k.sb + h * J.k.sh;
-  const char* vb = J.v.p + b * J.v.sb + h * J.v.sh + v0 * ES;
-  u32x4 kr[NK], vr[NV], qr[OUT ? NQ : 1];
+  const char* qb = J.q.p + b * J.q.sb + h * J.q.sh;
+  LinCopy<KWP * ES / 16, 256> kc(J.k.p + b * J.k.sb + h * J.k.sh, J.k.st, kw, turned, tid);
+  LinCopy<VS * ES / 16, 256> vc(J.v.p + b * J.v.sb + h * J.v.sh + v0 * ES, J.v.st, vw, turned, tid);
+  u32x4 qr[OUT ? NQ : 1];
+  const bool narrow = kw < KWP * ES;
+  const int end = min(past, len);
+  auto position = [&](int n) { return turned ? len - 1 - n : n; };  // of the walk's n-th token
   auto fetch = [&](int n0) {
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int p = tid + 256 * i, r = n0 + p / (KWP * ES / 16), at = p % (KWP * ES / 16) * 16;
-      kr[i] = r < min(len, past) ? blk_ld(kb + order.at(r) * J.k.st, at, kw) : zero16();
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int p = tid + 256 * i, r = n0 + p / (VS * ES / 16), at = p % (VS * ES / 16) * 16;
-      vr[i] = r < min(len, past) ? blk_ld(vb + order.at(r) * J.v.st, at, vw) : zero16();
-    }
+    kc.fetch(position(n0), end - n0);
+    vc.fetch(position(n0), end - n0);
     if constexpr (OUT) {
-      const int r = n0 + mine;
+      const char* p = qb + (int64_t)position(min(n0 + mine, end - 1)) * J.q.st;
 #pragma unroll
-      for (int s = 0; s < NQ; ++s) qr[s] = r < min(len, past) ? blk_ld(qb + order.at(r) * J.q.st, 64 * s + 16 * a, kw) : zero16();
+      for (int s = 0; s < NQ; ++s) qr[s] = ld16(p + (64 * s + 16 * a < kw ? 64 * s + 16 * a : 0));
     }
   };
-  if (first < len) fetch(first);
+  if (first < end) fetch(first);
   int n0 = first;
-  for (; n0 < min(past, len); n0 += C) {
+  for (; n0 < end; n0 += C) {
     const int n = min(C, len - n0);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const int p = tid + 256 * i;
-      st16(ks + p / (KWP * ES / 16) * KP + p % (KWP * ES / 16) * 16, kr[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int p = tid + 256 * i;
-      st16(vs + p / (VS * ES / 16) * VP + p % (VS * ES / 16) * 16, vr[i]);
-    }
+    kc.template put<KP>(ks, narrow);
+    vc.template put<VP>(vs, false);
     u32x4 q[OUT ? NQ : 1];
     if constexpr (OUT) {
 #pragma unroll
@@ -191,7 +213,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_l
         }
     }
     __syncthreads();
-    if (n0 + C < min(past, len)) fetch(n0 + C);
+    if (n0 + C < end) fetch(n0 + C);
     if (n < C) set_left(n);
     if constexpr (OUT) {
       const bool lead = J.turned && n0 == 0;
@@ -227,12 +249,14 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_l
         for (int j = 0; j < VT; ++j) out[j] = blk_mma_split<T>(blk_column<T>(vs, VP, s * blk_slab<T>(), j, lane), hi, lo, out[j]);
       }
       if (n0 + mine < past) {
-        char* o = J.o.p + b * J.o.sb + order.at(n0 + mine) * J.o.st + h * J.o.sh + v0 * ES;
-        const float mul = mine < n ? P.scale : 0.f;
+        const bool token = mine < n;
+        char* o = J.o.p + b * J.o.sb + (int64_t)(token ? position(n0 + mine) : n0 + mine) * J.o.st + h * J.o.sh + v0 * ES;
 #pragma unroll
         for (int j = 0; j < VT; ++j) {
           const int c = 16 * j + 4 * a;
-          const float v[4] = {out[j][0] * mul, out[j][1] * mul, out[j][2] * mul, out[j][3] * mul};
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = token ? out[j][e] * P.scale : 0.f;
           if (c * ES < vw) blk_st4<T>(o + c * ES, v);
         }
       }
@@ -290,22 +314,38 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_l
         for (int j = 0; j < VT; ++j)
           if ((16 * j + 4 * a) * ES < vw) blk_st4<T>(o + (16 * j + 4 * a) * ES, v);
       }
-    if (J.exit && seg == P.segments - 1) {
-      float* p = J.last + bh * size;
-      const float mul = J.exit_mul * (J.turned && len > 0 ? lin_power(1, lg2) : 1.f);
-      each([&](f32x4& s, int e, int r, int c) { p[(int64_t)r * J.vw + c] = s[e] * mul; });
-    }
+    if (J.exit && seg == P.segments - 1) store(J.exit + bh * size, J.exit_mul * (turned && len > 0 ? lin_power(1, lg2) : 1.f));
   } else {
-    float* p = J.part + ((int64_t)bh * (P.segments - 1) + seg) * size;
-    each([&](f32x4& s, int e, int r, int c) { p[(int64_t)r * J.vw + c] = s[e]; });
+    store(J.part + ((int64_t)bh * P.segments + seg + 1) * size, 1.f);
   }
 }
 
-// The last states to where they are wanted: a walk of another segment may read
-// the states before the first step from there.
-__global__ __launch_bounds__(256) void k_linear_exit(const float* from, float* to, int64_t n) {
-  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i < n) st16(to + i, ld16(from + i));
+// The states before the segments from what each segment adds: four elements a
+// thread, whose loads do not wait for one another.
+__global__ __launch_bounds__(256) void k_linear_scan(const LinParams P) {
+  const LinJob& J = P.job[blockIdx.y];
+  const int64_t size = (int64_t)J.kw * J.vw, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
+  const int bh = (int)(i / size), e = (int)(i - bh * size);  // size is a multiple of 64
+  if (bh >= P.B * P.H) return;
+  const int len = lin_len(P, bh / P.H), whole = P.seg_chunks * LIN_CHUNK;
+  const float lg2 = lin_log2(P.log_decay, bh % P.H);
+  float* p = J.part + (int64_t)bh * P.segments * size + e;
+  f32x4 s = zero4(), add[LIN_SEGMENTS - 1];
+  if (J.entry) {
+    const int r = e / J.vw, c = e - r * J.vw;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) s[x] = J.entry[bh * size + (J.flip_entry ? (int64_t)(c + x) * J.kw + r : e + x)] * J.entry_mul;
+  }
+#pragma unroll
+  for (int m = 0; m < LIN_SEGMENTS - 1; ++m) add[m] = __builtin_bit_cast(f32x4, ld16(p + min(m + 1, P.segments - 1) * size));
+  st16(p, __builtin_bit_cast(u32x4, s));
+#pragma unroll
+  for (int m = 0; m < LIN_SEGMENTS - 1; ++m) {
+    if (m + 1 >= P.segments) break;
+    const int n = max(0, min(len - m * whole, whole));
+    if (n) s = lin_power(n - (m == 0 ? J.turned : 0), lg2) * s + add[m];
+    st16(p + (m + 1) * size, __builtin_bit_cast(u32x4, s));
+  }
 }
 
 // One token: a workgroup takes LIN_STEP_COLUMNS columns of one state, four a lane.
@@ -370,14 +410,13 @@ template <typename T, int KWP> void walk(const LinParams& all, hipStream_t st) {
   for (int i = 0; i < all.jobs; ++i)
     if (lin_kwp(all.job[i].kw) == KWP) P.job[P.jobs++] = all.job[i];
   if (!P.jobs) return;
-  if (P.segments > 1) walk_jobs<T, KWP, false>(P, st);
-  walk_jobs<T, KWP, true>(P, st);
-  for (int i = 0; i < P.jobs; ++i) {
-    const LinJob& J = P.job[i];
-    const int64_t n = (int64_t)P.B * P.H * J.kw * J.vw;  // a multiple of 64
-    if (J.exit && J.last != J.exit)
-      hipLaunchKernelGGL(k_linear_exit, dim3((unsigned)((n / 4 + 255) / 256)), dim3(256), 0, st, J.last, J.exit, n);
+  if (P.segments > 1) {
+    walk_jobs<T, KWP, false>(P, st);
+    int64_t most = 0;
+    for (int i = 0; i < P.jobs; ++i) most = std::max(most, (int64_t)P.B * P.H * P.job[i].kw * P.job[i].vw);
+    hipLaunchKernelGGL(k_linear_scan, dim3((unsigned)((most / 4 + 255) / 256), (unsigned)P.jobs), dim3(256), 0, st, P);
   }
+  walk_jobs<T, KWP, true>(P, st);
 }
 template <typename T> void walk_all(const LinParams& P, hipStream_t st) {
   walk<T, 64>(P, st);

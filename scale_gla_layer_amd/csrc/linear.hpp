@@ -19,8 +19,7 @@ struct LinJob {
   LinHeads q, k, v, o;
   const float* entry;  // [B][H][kw][vw] state before the first step, or NULL
   float* exit;         // the state after the last one, or NULL
-  float* last;         // where the walk puts it: exit, or with segments a place from which it is copied
-  float* part;         // [B][H][segments - 1][kw][vw] what each segment adds to the state
+  float* part;         // [B][H][segments][kw][vw] states before the segments; first what the one before each adds
   float entry_mul, exit_mul;
   int kw, vw;          // widths of q and k, and of v and o
   int turned;          // from the last token to the first; entry is then not decayed by the first step, exit is once more
