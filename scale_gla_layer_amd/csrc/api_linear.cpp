@@ -34,8 +34,6 @@ LinHeads heads_of(const msgla_heads* t, int es) {
 }
 int es_of(const msgla_linear_config* c) { return c->dtype == MSGLA_BF16 ? 2 : 4; }
 
-int slices_of(int es, int kw, int vw) { return cdiv(vw, lin_columns(es, lin_kwp(kw))); }
-
 // Segments of a sequence: as many as give the chip about two workgroups a CU, of
 // at least four chunks each.
 void set_segments(LinParams& P, int64_t walks) {
@@ -52,13 +50,12 @@ LinParams lin_params(const msgla_linear_config* c, int64_t B, int64_t L, bool gr
   P.L = (int)L;
   P.H = c->heads;
   P.scale = c->scale;
-  const int es = es_of(c);
   P.jobs = gradient ? 3 : 1;
   for (int i = 0; i < P.jobs; ++i) {  // forward; or dq, dk, dv
     LinJob& J = P.job[i];
     J.kw = gradient && i < 2 ? c->d_v : c->d_k;
     J.vw = gradient && i < 2 ? c->d_k : c->d_v;
-    J.slices = slices_of(es, J.kw, J.vw);
+    J.slices = cdiv(J.vw, LIN_COLUMNS);
     J.turned = gradient && i > 0;
     J.flip_entry = gradient && i < 2;
     J.entry_mul = gradient && i > 0 ? 1.f / c->scale : 1.f;
@@ -84,7 +81,7 @@ size_t lin_room(LinParams& P, void* ws) {
 bool lin_grid_ok(const LinParams& P) {
   int64_t most = 0;
   for (int i = 0; i < P.jobs; ++i) most = std::max(most, (int64_t)P.B * P.H * P.segments * P.job[i].slices);
-  return launch_ok((most + N_XCD) * P.jobs, 256) && launch_ok((int64_t)P.B * P.H * 64, 256);
+  return launch_ok((most + N_XCD) * P.jobs, 512) && launch_ok((int64_t)P.B * P.H * 64, 256);
 }
 
 size_t lin_room_bytes(const msgla_linear_config* cfg, int64_t B, int64_t L, bool gradient) {

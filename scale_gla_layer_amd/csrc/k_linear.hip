@@ -5,10 +5,13 @@
 //   out_i = scale (gamma^(i+1) q_i S + sum_{j <= i} gamma^(i-j) (q_i . k_j) v_j)
 //   S' = gamma^n S + sum_j gamma^(n-1-j) k_j^T v_j
 // so a walk over the chunks is four matrix products each.  A workgroup walks one
-// (sequence, head) for some columns of v, the state in the accumulators of its
-// four waves (each has a quarter of its rows) and, rounded, in LDS, where it is an
-// operand of the next chunk's product.  All exponents of gamma are at least 0, so
-// nothing overflows, and a decay of 0 (log_decay of minus infinity) is exact.
+// (sequence, head) for 64 columns of v.  Four of its waves form the outputs, of 16
+// positions each; four others keep the state in their accumulators, a quarter of its
+// rows each, and leave it, rounded, in LDS, where it is an operand of the next chunk's
+// outputs.  Both work on a chunk at the same time, with half the registers that one
+// wave for both would need, while asynchronous copies bring the next one.  All
+// exponents of gamma are at least 0, so nothing overflows, and a decay of 0
+// (log_decay of minus infinity) is exact.
 //   Few sequences and heads: each sequence is cut into segments, what each adds
 // to the state is formed first (from zero, without outputs), a small kernel sums up
 // the states before the segments, and the walks begin with these.
@@ -24,7 +27,7 @@
 // four neighbouring rows a lane, which is 8 bytes of the transposed state in LDS.
 #include <algorithm>
 
-#include "block_device.hpp"
+#include "block_stage.hpp"
 #include "linear.hpp"
 
 namespace msgla {
@@ -43,120 +46,242 @@ __device__ __forceinline__ int lin_len(const LinParams& P, int b) {
   return P.lens ? max(0, min(P.lens[b], P.L)) : P.L;
 }
 
-// 16-byte pieces of rows of W pieces that a thread copies to LDS a chunk: rows of
-// positions that follow one another, or (turned) that go back.  There are no
-// conditional loads, each of which would be waited for on its own: rows behind the
-// last one repeat it, and pieces behind the width the first one, which `put` makes zero.
-template <int W, int THREADS> struct LinCopy {
-  static constexpr int N = LIN_CHUNK * W / THREADS;
+// Copies of chunks of 64 rows of W pieces into stage tiles, dealt to a workgroup's
+// waves: rows of positions that follow one another, or (turned) that go back.  Rows
+// behind the last one repeat it, and pieces behind the width the first one: they meet
+// zeroes or are not stored.
+template <int W, int WAVES> struct ChunkCopy {
+  static constexpr int N = W / WAVES;  // copy instructions of a wave
+  static_assert(LIN_CHUNK == 64 && W % WAVES == 0, "a row a lane and instruction");
   const char* base;
   int64_t st;
-  int tid, width;
-  u32x4 r[N];
   int32_t off[N];
+  int width;
   bool near;
-  __device__ LinCopy(const char* b, int64_t stride, int w, bool turned, int t) : base(b), st(turned ? -stride : stride), tid(t), width(w) {
+  __device__ ChunkCopy(const char* b, int64_t stride, int w, bool turned, int wave, int lane) : base(b), st(turned ? -stride : stride), width(w) {
     near = stride <= 0x7fffffff / (2 * LIN_CHUNK);
 #pragma unroll
-    for (int i = 0; i < N; ++i) off[i] = row(i) * (int)st + byte(i);
+    for (int i = 0; i < N; ++i) off[i] = row(i, wave, lane) * (int)st + byte(i, wave, lane);
   }
-  __device__ __forceinline__ int row(int i) const { return (tid + THREADS * i) / W; }
-  __device__ __forceinline__ int byte(int i) const {
-    const int at = (tid + THREADS * i) % W * 16;
+  __device__ __forceinline__ static int row(int i, int wave, int lane) { return (64 * (wave + WAVES * i) + lane) / W; }
+  __device__ __forceinline__ int byte(int i, int wave, int lane) const {
+    const int at = ((lane % W) ^ tile_key<W>(row(i, wave, lane))) * 16;
     return at < width ? at : 0;
   }
   // n rows from the position `first` on
-  __device__ __forceinline__ void fetch(int64_t first, int n) {
+  __device__ __forceinline__ void issue(int64_t first, int n, char* lds, int wave, int lane) const {
     const char* p = base + first * (st < 0 ? -st : st);
     if (n >= LIN_CHUNK && near) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = ld16(p + off[i]);
+      for (int i = 0; i < N; ++i) dma16(p + off[i], lds + 1024 * (wave + WAVES * i));
     } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) r[i] = ld16(p + min(row(i), n - 1) * st + byte(i));
-    }
-  }
-  template <int PITCH> __device__ __forceinline__ void put(char* lds, bool zeroes) const {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = (tid + THREADS * i) % W * 16;
-      st16(lds + row(i) * PITCH + at, zeroes && at >= width ? zero16() : r[i]);
+      for (int i = 0; i < N; ++i) dma16(p + min(row(i, wave, lane), n - 1) * st + byte(i, wave, lane), lds + 1024 * (wave + WAVES * i));
     }
   }
 };
 
-// Two workgroups a CU where LDS holds them.
+// Waves a SIMD: two workgroups of eight a CU where LDS holds them.
+template <typename T, int KWP, bool OUT> constexpr int lin_waves() {
+  return OUT ? (sizeof(T) == 2 && KWP <= 128 ? 4 : 2) : sizeof(T) == 2 && KWP <= 128 ? 3 : 1;
+}
+// Stages of LDS for a chunk's keys and values: two where they fit.
+template <typename T, int KWP> constexpr int lin_stages() { return sizeof(T) == 4 && KWP == 256 ? 1 : 2; }
+
+// OUT: the walk; else what a segment adds to the state (the state's waves alone).
 template <typename T, int KWP, bool OUT>
-__global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_linear(const LinParams P) {
-  constexpr int ES = sizeof(T), VS = lin_columns(ES, KWP), C = LIN_CHUNK;
+__global__ __launch_bounds__(OUT ? 512 : 256, (lin_waves<T, KWP, OUT>())) void k_linear(const LinParams P) {
+  constexpr int ES = sizeof(T), VS = LIN_COLUMNS, C = LIN_CHUNK, WAVES = OUT ? 8 : 4, STAGES = lin_stages<T, KWP>();
   constexpr int NQ = KWP * ES / 64;            // slabs of a row
-  constexpr int KT = KWP / 64, VT = VS / 16;   // the wave's tiles of the state
+  constexpr int KT = KWP / 64, VT = VS / 16;   // a state wave's tiles
   constexpr int SL = C / blk_slab<T>();        // slabs of a chunk's positions
-  constexpr int KP = blk_pitch<T, KWP>(), VP = blk_pitch<T, VS>();
+  constexpr int WK = KWP * ES / 16, WV = VS * ES / 16, KB = C * WK * 16, STAGE = KB + C * WV * 16, SB = VS * WK * 16;
   constexpr bool LO = ES == 2;
-  __shared__ __attribute__((aligned(16))) char ks[C * KP];
-  __shared__ __attribute__((aligned(16))) char vs[C * VP];
-  __shared__ __attribute__((aligned(16))) char ss[OUT ? (LO ? 2 : 1) * VS * KP : 16];  // state^T [column][row], hi and lo
+  // variables of their own, so that reads of one need not wait for copies to another
+  __shared__ __attribute__((aligned(1024))) char stage0[STAGE], stage1[STAGES == 2 ? STAGE : 16];
+  __shared__ __attribute__((aligned(16))) char ss[OUT ? (LO ? 2 : 1) * SB : 16];  // state^T [column][row], hi and lo
   const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, a = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const LinJob& J = P.job[blockIdx.y];
   const int nseg = OUT ? P.segments : P.segments - 1;
-  const int total = P.B * P.H * nseg * J.slices;
+  const int total = P.B * P.H * nseg * J.slices, per = (total + N_XCD - 1) / N_XCD;
   // an XCD takes neighbouring slices, which read the same q and k
-  const int w = remap_xcd(blockIdx.x, (total + N_XCD - 1) / N_XCD);
-  if (blockIdx.x / N_XCD >= (unsigned)((total + N_XCD - 1) / N_XCD) || w >= total) return;
+  const int w = remap_xcd(blockIdx.x, per);
+  if (blockIdx.x / N_XCD >= (unsigned)per || w >= total) return;
   const int slice = w % J.slices, seg = w / J.slices % nseg, bh = w / J.slices / nseg, b = bh / P.H, h = bh - b * P.H;
   const int len = lin_len(P, b), v0 = slice * VS;
   const float lg2 = lin_log2(P.log_decay, h);
-  const int first = seg * P.seg_chunks * C, past = min(P.L, first + P.seg_chunks * C);
+  const int first = seg * P.seg_chunks * C, past = min(P.L, first + P.seg_chunks * C), end = min(past, len);
   const int kw = J.kw * ES, vw = min(VS, J.vw - v0) * ES;  // bytes of a row, and of its part
   const bool turned = J.turned != 0;
+  auto position = [&](int n) { return turned ? len - 1 - n : n; };  // of the walk's n-th token
+  const ChunkCopy<WK, WAVES> kc(J.k.p + b * J.k.sb + h * J.k.sh, J.k.st, kw, turned, wave, lane);
+  const ChunkCopy<WV, WAVES> vc(J.v.p + b * J.v.sb + h * J.v.sh + v0 * ES, J.v.st, vw, turned, wave, lane);
+  auto fetch = [&](int n0, char* to) {
+    kc.issue(position(n0), end - n0, to, wave, lane);
+    vc.issue(position(n0), end - n0, to + KB, wave, lane);
+  };
+  if (first < end) fetch(first, stage0);
+  const Rows<WK> row(lane);
+  const Columns<T, WK> kcol(lane);
+  const Columns<T, WV> vcol(lane);
 
+  // Chunk by chunk: before(n0, stage) and after(n0, stage), with a barrier behind each; the first one
+  // finds the state before the chunk in LDS, the second one may renew it.
+  auto walk = [&](auto before, auto after) __attribute__((always_inline)) {
+    auto chunk = [&](int n0, char* stage, char* next) __attribute__((always_inline)) {
+      if (STAGES == 2 && n0 + C < end) fetch(n0 + C, next);
+      before(n0, stage);
+      if constexpr (OUT) lds_barrier();
+      after(n0, stage);
+      __syncthreads();
+      if (STAGES == 1 && n0 + C < end) {
+        fetch(n0 + C, stage);
+        __syncthreads();
+      }
+    };
+    __syncthreads();
+    for (int n0 = first; n0 < end; n0 += STAGES * C) {
+      chunk(n0, stage0, STAGES == 2 ? stage1 : stage0);
+      if (STAGES == 2 && n0 + C < end) chunk(n0 + C, stage1, stage0);
+    }
+  };
+
+  if (OUT && wave < 4) {  // the outputs
+    const int mine = 16 * wave + c16;  // the lane's row of a chunk
+    float within[C / 16][4];           // decays from the positions before it
+#pragma unroll
+    for (int t = 0; t < C / 16; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int back = mine - (16 * t + 4 * a + e);
+        within[t][e] = back >= 0 ? lin_power(max(back, 0), lg2) : 0.f;
+      }
+    const float grow = lin_power(mine + 1, lg2), grow_first = lin_power(mine, lg2);
+    const char* qb = J.q.p + b * J.q.sb + h * J.q.sh;
+    u32x4 q[NQ];
+    auto load = [&](int n0) {
+      const char* p = qb + (int64_t)position(min(n0 + mine, end - 1)) * J.q.st;
+#pragma unroll
+      for (int s = 0; s < NQ; ++s) q[s] = ld16(p + (64 * s + 16 * a < kw ? 64 * s + 16 * a : 0));
+      if (kw < KWP * ES) {
+#pragma unroll
+        for (int s = 0; s < NQ; ++s)
+          if (64 * s + 16 * a >= kw) q[s] = zero16();
+      }
+    };
+    if (first < end) load(first);
+    f32x4 out[VT];
+    float A[C / 16][4];
+    walk(
+        [&](int n0, const char* ks) {
+#pragma unroll
+          for (int t = 0; t < C / 16; ++t) {
+            f32x4 x = zero4();
+            if (t <= wave) {
+#pragma unroll
+              for (int s = 0; s < NQ; ++s) x = mma_slab<T>(row.read(ks, t, s), q[s], x);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) A[t][e] = x[e] * within[t][e];
+          }
+          const float g = turned && n0 == 0 ? grow_first : grow;
+#pragma unroll
+          for (int j = 0; j < VT; ++j) {
+            out[j] = zero4();
+#pragma unroll
+            for (int s = 0; s < NQ; ++s) {
+              out[j] = mma_slab<T>(row.read(ss, j, s), q[s], out[j]);
+              if constexpr (LO) out[j] = mma_slab<T>(row.read(ss + SB, j, s), q[s], out[j]);
+            }
+            out[j] *= g;
+          }
+        },
+        [&](int n0, const char* ks) {
+          const char* vs = ks + KB;
+          if (n0 + C < end) load(n0 + C);
+#pragma unroll
+          for (int s = 0; s < SL; ++s) {
+            if (s * blk_slab<T>() > 16 * wave + 15) break;
+            u32x4 hi, lo;
+            blk_split<T>(A, s, hi, lo);
+#pragma unroll
+            for (int j = 0; j < VT; ++j) out[j] = blk_mma_split<T>(vcol.read(vs, s, j), hi, lo, out[j]);
+          }
+          if (n0 + mine < past) {
+            const bool token = n0 + mine < len;
+            char* o = J.o.p + b * J.o.sb + (int64_t)(token ? position(n0 + mine) : n0 + mine) * J.o.st + h * J.o.sh + v0 * ES;
+#pragma unroll
+            for (int j = 0; j < VT; ++j) {
+              const int c = 16 * j + 4 * a;
+              float v[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) v[e] = token ? out[j][e] * P.scale : 0.f;
+              if (c * ES < vw) blk_st4<T>(o + c * ES, v);
+            }
+          }
+        });
+    // rows behind the sequence's end
+    for (int n0 = end > first ? first + (end - first + C - 1) / C * C : first; n0 < past; n0 += C)
+      if (n0 + mine < past) {
+        char* o = J.o.p + b * J.o.sb + (int64_t)(n0 + mine) * J.o.st + h * J.o.sh + v0 * ES;
+        const float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < VT; ++j)
+          if ((16 * j + 4 * a) * ES < vw) blk_st4<T>(o + (16 * j + 4 * a) * ES, v);
+      }
+    return;
+  }
+
+  // the state: tiles KT k0 .. of 16 rows
+  const int k0 = KT * (OUT ? wave - 4 : wave);
   f32x4 S[KT][VT];
 #pragma unroll
   for (int i = 0; i < KT; ++i)
 #pragma unroll
     for (int j = 0; j < VT; ++j) S[i][j] = zero4();
-  // rows 16 (KT wave + i) + 4 a + e, column v0 + 16 j + c16 of a state
+  // rows 16 (k0 + i) + 4 a + e, column v0 + 16 j + c16
   auto each = [&](auto f) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < KT; ++i)
 #pragma unroll
       for (int j = 0; j < VT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f(S[i][j], e, 16 * (KT * wave + i) + 4 * a + e, v0 + 16 * j + c16);
-  };
-  auto load = [&](const float* p, bool flip, float mul) __attribute__((always_inline)) {
-    each([&](f32x4& s, int e, int r, int c) {
-      const int64_t row = min(r, J.kw - 1), column = min(c, J.vw - 1);
-      s[e] = p[flip ? column * J.kw + row : row * J.vw + column];
-    });
-    each([&](f32x4& s, int e, int r, int c) { s[e] = r < J.kw && c < J.vw ? s[e] * mul : 0.f; });
-  };
-  auto store = [&](float* p, float mul) __attribute__((always_inline)) {
-    each([&](f32x4& s, int e, int r, int c) {
-      if (r < J.kw && c < J.vw) p[(int64_t)r * J.vw + c] = s[e] * mul;
-    });
+        for (int e = 0; e < 4; ++e) f(S[i][j], e, 16 * (k0 + i) + 4 * a + e, v0 + 16 * j + c16);
   };
   const int64_t size = (int64_t)J.kw * J.vw;
-  if constexpr (OUT) {
-    if (P.segments > 1) load(J.part + ((int64_t)bh * P.segments + seg) * size, false, 1.f);
-    else if (J.entry) load(J.entry + bh * size, J.flip_entry, J.entry_mul);
+  if (OUT && (P.segments > 1 || J.entry)) {
+    const bool flip = P.segments == 1 && J.flip_entry;
+    const float* p = P.segments > 1 ? J.part + ((int64_t)bh * P.segments + seg) * size : J.entry + bh * size;
+    const float mul = P.segments > 1 ? 1.f : J.entry_mul;
+    each([&](f32x4& s, int e, int r, int c) {
+      const int64_t x = min(r, J.kw - 1), y = min(c, J.vw - 1);
+      s[e] = p[flip ? y * J.kw + x : x * J.vw + y];
+    });
+    each([&](f32x4& s, int e, int r, int c) { s[e] = r < J.kw && c < J.vw ? s[e] * mul : 0.f; });
   }
-
-  // decays within a chunk, for the lane's row 16 wave + c16 and its positions
-  const int mine = 16 * wave + c16;
-  float within[OUT ? C / 16 : 1][4];
+  auto publish = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int t = 0; t < (OUT ? C / 16 : 1); ++t)
+    for (int i = 0; i < KT; ++i)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int back = mine - (16 * t + 4 * a + e);
-      within[t][e] = back >= 0 ? lin_power(max(back, 0), lg2) : 0.f;
-    }
-  const float grow = lin_power(mine + 1, lg2), grow_first = lin_power(mine, lg2);
-  float left[SL][LO ? 8 : 4];  // until the chunk's last token, of the positions of a K^T operand
-  auto set_left = [&](int n) {
+      for (int j = 0; j < VT; ++j) {
+        const int r = 16 * j + c16, piece = (16 * (k0 + i) + 4 * a) * ES / 16;
+        char* p = ss + r * WK * 16 + ((piece ^ tile_key<WK>(r)) * 16) + (LO ? 8 * (a & 1) : 0);
+        const float v[4] = {S[i][j][0], S[i][j][1], S[i][j][2], S[i][j][3]};
+        if constexpr (LO) {
+          const u32x2 hi = pack8<bf16>(v);
+          const uint32_t w0 = hi[0], w1 = hi[1];
+          const float d[4] = {v[0] - u2f(w0 << 16), v[1] - u2f(w0 & 0xffff0000u), v[2] - u2f(w1 << 16), v[3] - u2f(w1 & 0xffff0000u)};
+          st8(p, hi);
+          st8(p + SB, pack8<bf16>(d));
+        } else {
+          st16(p, pack16<float>(v));
+        }
+      }
+  };
+  if constexpr (OUT) publish();
+  float left[SL][LO ? 8 : 4];  // decays until the chunk's last token, of the positions of a K^T operand
+  auto set_left = [&](int n) __attribute__((always_inline)) {
 #pragma unroll
     for (int s = 0; s < SL; ++s)
 #pragma unroll
@@ -165,159 +290,66 @@ __global__ __launch_bounds__(256, sizeof(T) == 4 && KWP == 256 ? 1 : 2) void k_l
         left[s][e] = j < n ? lin_power(max(n - 1 - j, 0), lg2) : 0.f;
       }
   };
-  set_left(C);
-  const float keep_whole = lin_power(C, lg2);
-
-  const char* qb = J.q.p + b * J.q.sb + h * J.q.sh;
-  LinCopy<KWP * ES / 16, 256> kc(J.k.p + b * J.k.sb + h * J.k.sh, J.k.st, kw, turned, tid);
-  LinCopy<VS * ES / 16, 256> vc(J.v.p + b * J.v.sb + h * J.v.sh + v0 * ES, J.v.st, vw, turned, tid);
-  u32x4 qr[OUT ? NQ : 1];
-  const bool narrow = kw < KWP * ES;
-  const int end = min(past, len);
-  auto position = [&](int n) { return turned ? len - 1 - n : n; };  // of the walk's n-th token
-  auto fetch = [&](int n0) {
-    kc.fetch(position(n0), end - n0);
-    vc.fetch(position(n0), end - n0);
-    if constexpr (OUT) {
-      const char* p = qb + (int64_t)position(min(n0 + mine, end - 1)) * J.q.st;
+  set_left(min(C, end - first));
+  float keep = lin_power(min(C, end - first) - (turned && seg == 0 ? 1 : 0), lg2);
+  walk(
+      [&](int n0, const char* ks) {
+        const char* vs = ks + KB;
 #pragma unroll
-      for (int s = 0; s < NQ; ++s) qr[s] = ld16(p + (64 * s + 16 * a < kw ? 64 * s + 16 * a : 0));
-    }
+        for (int i = 0; i < KT; ++i)
+#pragma unroll
+          for (int j = 0; j < VT; ++j) S[i][j] *= keep;
+#pragma unroll
+        for (int s = 0; s < SL; ++s) {
+          u32x4 f[VT];
+#pragma unroll
+          for (int j = 0; j < VT; ++j) f[j] = vcol.read(vs, s, j);
+#pragma unroll
+          for (int i = 0; i < KT; ++i) {
+            constexpr int N = LO ? 8 : 4;
+            float x[N];
+            unpack16<T>(kcol.read(ks, s, k0 + i), x);
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] *= left[s][e];
+            u32x4 hi, lo = zero16(), rest = zero16();
+            if constexpr (LO) {
+              split_bf16(x, hi, lo);
+              if (J.exit) {
+                float y[8], m[8];
+                unpack16<bf16>(hi, y);
+                unpack16<bf16>(lo, m);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = x[e] - y[e] - m[e];
+                rest = pack16<bf16>(x);
+              }
+            } else {
+              hi = pack16<float>(x);
+            }
+#pragma unroll
+            for (int j = 0; j < VT; ++j) {
+              S[i][j] = mma_slab<T>(hi, f[j], S[i][j]);
+              if constexpr (LO) {
+                S[i][j] = mma_slab<T>(lo, f[j], S[i][j]);
+                if (J.exit) S[i][j] = mma_slab<T>(rest, f[j], S[i][j]);
+              }
+            }
+          }
+        }
+        // of the next chunk: another decay behind the first one, others in the last one
+        const int n = min(C, end - n0 - C);
+        if (n > 0 && n < C) set_left(n);
+        if (n > 0 && (n < C || n0 == first)) keep = lin_power(n, lg2);
+      },
+      [&](int n0, const char*) {
+        if (OUT && n0 + C < end) publish();
+      });
+  auto store = [&](float* p, float mul) __attribute__((always_inline)) {
+    each([&](f32x4& s, int e, int r, int c) {
+      if (r < J.kw && c < J.vw) p[(int64_t)r * J.vw + c] = s[e] * mul;
+    });
   };
-  if (first < end) fetch(first);
-  int n0 = first;
-  for (; n0 < end; n0 += C) {
-    const int n = min(C, len - n0);
-    __syncthreads();
-    kc.template put<KP>(ks, narrow);
-    vc.template put<VP>(vs, false);
-    u32x4 q[OUT ? NQ : 1];
-    if constexpr (OUT) {
-#pragma unroll
-      for (int s = 0; s < NQ; ++s) q[s] = qr[s];
-#pragma unroll
-      for (int i = 0; i < KT; ++i)
-#pragma unroll
-        for (int j = 0; j < VT; ++j) {
-          char* p = ss + (16 * j + c16) * KP + (16 * (KT * wave + i) + 4 * a) * ES;
-          const float v[4] = {S[i][j][0], S[i][j][1], S[i][j][2], S[i][j][3]};
-          if constexpr (LO) {
-            const u32x2 hi = pack8<bf16>(v);
-            const uint32_t w0 = hi[0], w1 = hi[1];
-            const float r[4] = {v[0] - u2f(w0 << 16), v[1] - u2f(w0 & 0xffff0000u), v[2] - u2f(w1 << 16), v[3] - u2f(w1 & 0xffff0000u)};
-            st8(p, hi);
-            st8(p + VS * KP, pack8<bf16>(r));
-          } else {
-            st16(p, pack16<float>(v));
-          }
-        }
-    }
-    __syncthreads();
-    if (n0 + C < end) fetch(n0 + C);
-    if (n < C) set_left(n);
-    if constexpr (OUT) {
-      const bool lead = J.turned && n0 == 0;
-      f32x4 out[VT];
-#pragma unroll
-      for (int j = 0; j < VT; ++j) {
-        out[j] = zero4();
-#pragma unroll
-        for (int s = 0; s < NQ; ++s) {
-          const char* p = ss + (16 * j + c16) * KP + 64 * s + 16 * a;
-          out[j] = mma_slab<T>(ld16(p), q[s], out[j]);
-          if constexpr (LO) out[j] = mma_slab<T>(ld16(p + VS * KP), q[s], out[j]);
-        }
-        out[j] *= lead ? grow_first : grow;
-      }
-      float A[C / 16][4];
-#pragma unroll
-      for (int t = 0; t < C / 16; ++t) {
-        f32x4 x = zero4();
-        if (t <= wave) {
-#pragma unroll
-          for (int s = 0; s < NQ; ++s) x = mma_slab<T>(ld16(ks + (16 * t + c16) * KP + 64 * s + 16 * a), q[s], x);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) A[t][e] = x[e] * within[t][e];
-      }
-#pragma unroll
-      for (int s = 0; s < SL; ++s) {
-        if (s * blk_slab<T>() > 16 * wave + 15) break;
-        u32x4 hi, lo;
-        blk_split<T>(A, s, hi, lo);
-#pragma unroll
-        for (int j = 0; j < VT; ++j) out[j] = blk_mma_split<T>(blk_column<T>(vs, VP, s * blk_slab<T>(), j, lane), hi, lo, out[j]);
-      }
-      if (n0 + mine < past) {
-        const bool token = mine < n;
-        char* o = J.o.p + b * J.o.sb + (int64_t)(token ? position(n0 + mine) : n0 + mine) * J.o.st + h * J.o.sh + v0 * ES;
-#pragma unroll
-        for (int j = 0; j < VT; ++j) {
-          const int c = 16 * j + 4 * a;
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = token ? out[j][e] * P.scale : 0.f;
-          if (c * ES < vw) blk_st4<T>(o + c * ES, v);
-        }
-      }
-    }
-    const float keep = n == C && !(J.turned && n0 == 0) ? keep_whole : lin_power(n - (J.turned && n0 == 0 ? 1 : 0), lg2);
-#pragma unroll
-    for (int i = 0; i < KT; ++i)
-#pragma unroll
-      for (int j = 0; j < VT; ++j) S[i][j] *= keep;
-#pragma unroll
-    for (int s = 0; s < SL; ++s) {
-      u32x4 f[VT];
-#pragma unroll
-      for (int j = 0; j < VT; ++j) f[j] = blk_column<T>(vs, VP, s * blk_slab<T>(), j, lane);
-#pragma unroll
-      for (int i = 0; i < KT; ++i) {
-        const u32x4 raw = blk_column<T>(ks, KP, s * blk_slab<T>(), KT * wave + i, lane);
-        constexpr int N = LO ? 8 : 4;
-        float x[N];
-        unpack16<T>(raw, x);
-#pragma unroll
-        for (int e = 0; e < N; ++e) x[e] *= left[s][e];
-        u32x4 hi, lo = zero16(), rest = zero16();
-        if constexpr (LO) {
-          split_bf16(x, hi, lo);
-          if (J.exit) {
-            float h[8], m[8];
-            unpack16<bf16>(hi, h);
-            unpack16<bf16>(lo, m);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] - h[e] - m[e];
-            rest = pack16<bf16>(x);
-          }
-        } else {
-          hi = pack16<float>(x);
-        }
-#pragma unroll
-        for (int j = 0; j < VT; ++j) {
-          S[i][j] = mma_slab<T>(hi, f[j], S[i][j]);
-          if constexpr (LO) {
-            S[i][j] = mma_slab<T>(lo, f[j], S[i][j]);
-            if (J.exit) S[i][j] = mma_slab<T>(rest, f[j], S[i][j]);
-          }
-        }
-      }
-    }
-  }
-  if constexpr (OUT) {
-    // rows behind the sequence's end
-    for (n0 = max(n0, first); n0 < past; n0 += C)
-      if (n0 + mine < past) {
-        char* o = J.o.p + b * J.o.sb + (int64_t)(n0 + mine) * J.o.st + h * J.o.sh + v0 * ES;
-        const float v[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < VT; ++j)
-          if ((16 * j + 4 * a) * ES < vw) blk_st4<T>(o + (16 * j + 4 * a) * ES, v);
-      }
-    if (J.exit && seg == P.segments - 1) store(J.exit + bh * size, J.exit_mul * (turned && len > 0 ? lin_power(1, lg2) : 1.f));
-  } else {
-    store(J.part + ((int64_t)bh * P.segments + seg + 1) * size, 1.f);
-  }
+  if constexpr (!OUT) store(J.part + ((int64_t)bh * P.segments + seg + 1) * size, 1.f);
+  else if (J.exit && seg == P.segments - 1) store(J.exit + bh * size, J.exit_mul * (turned && len > 0 ? lin_power(1, lg2) : 1.f));
 }
 
 // The states before the segments from what each segment adds: four elements a
@@ -400,7 +432,7 @@ template <typename T, int KWP, bool OUT> void walk_jobs(const LinParams& P, hipS
     most = n > most ? n : most;
   }
   const int64_t grid = (most + N_XCD - 1) / N_XCD * N_XCD;
-  hipLaunchKernelGGL((k_linear<T, KWP, OUT>), dim3((unsigned)grid, (unsigned)P.jobs), dim3(256), 0, st, P);
+  hipLaunchKernelGGL((k_linear<T, KWP, OUT>), dim3((unsigned)grid, (unsigned)P.jobs), dim3(OUT ? 512 : 256), 0, st, P);
 }
 
 // Jobs of one padded key width share a launch.

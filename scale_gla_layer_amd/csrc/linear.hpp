@@ -38,8 +38,7 @@ struct LinParams {
   int segments, seg_chunks;  // segments of so many chunks
 };
 
-// columns of v that a workgroup takes: the state and two roundings of it fill LDS
-constexpr int lin_columns(int es, int kwp) { return es == 4 || kwp == 256 ? 32 : 64; }
+constexpr int LIN_COLUMNS = 64;  // columns of v that a workgroup takes
 inline int lin_kwp(int kw) { return kw <= 64 ? 64 : kw <= 128 ? 128 : 256; }
 
 hipError_t launch_linear(const LinParams& P, bool bf16_path, hipStream_t st);
