@@ -9,6 +9,7 @@ using namespace msgla::host;
 namespace {
 
 constexpr size_t BAD = (size_t)-1;
+constexpr int N_CU = 256;
 
 bool lin_config_ok(const msgla_linear_config* c) {
   return c && (c->dtype == MSGLA_F32 || c->dtype == MSGLA_BF16) && c->heads >= 1 && c->heads <= 1024 && c->d_k >= 8 &&
@@ -34,14 +35,21 @@ LinHeads heads_of(const msgla_heads* t, int es) {
 }
 int es_of(const msgla_linear_config* c) { return c->dtype == MSGLA_BF16 ? 2 : 4; }
 
-// Segments of a sequence: as many as give the chip about two workgroups a CU, of
-// at least four chunks each.
-void set_segments(LinParams& P, int64_t walks) {
+// Segments of a sequence, of at least four chunks: no more than fill the CUs once with
+// the walks of jobs of this one's shape, which share a launch.
+void set_segments(LinParams& P, int es) {
+  auto columns = [es](const LinJob& J) { return lin_columns(es, lin_kwp(J.kw), J.vw); };
   const int chunks = cdiv(P.L, LIN_CHUNK);
-  const int64_t want = (512 + walks - 1) / walks;
-  const int n = (int)std::max<int64_t>(1, std::min<int64_t>({want, (int64_t)LIN_SEGMENTS, (int64_t)chunks / 4}));
-  P.seg_chunks = cdiv(chunks, n);
-  P.segments = cdiv(chunks, P.seg_chunks);
+  for (int i = 0; i < P.jobs; ++i) {
+    LinJob& J = P.job[i];
+    int64_t walks = 0;
+    for (int j = 0; j < P.jobs; ++j)
+      if (lin_kwp(P.job[j].kw) == lin_kwp(J.kw) && columns(P.job[j]) == columns(J)) walks += (int64_t)P.B * P.H * P.job[j].slices;
+    const bool share = es == 2 && lin_state_waves(es, lin_kwp(J.kw), columns(J)) == 4;
+    const int n = (int)std::max<int64_t>(1, std::min<int64_t>({(share ? 2 * N_CU : N_CU) / walks, (int64_t)LIN_SEGMENTS, (int64_t)chunks / 4}));
+    J.seg_chunks = cdiv(chunks, n);
+    J.segments = cdiv(chunks, J.seg_chunks);
+  }
 }
 
 LinParams lin_params(const msgla_linear_config* c, int64_t B, int64_t L, bool gradient) {
@@ -55,33 +63,32 @@ LinParams lin_params(const msgla_linear_config* c, int64_t B, int64_t L, bool gr
     LinJob& J = P.job[i];
     J.kw = gradient && i < 2 ? c->d_v : c->d_k;
     J.vw = gradient && i < 2 ? c->d_k : c->d_v;
-    J.slices = cdiv(J.vw, LIN_COLUMNS);
+    J.slices = cdiv(J.vw, lin_columns(es_of(c), lin_kwp(J.kw), J.vw));
     J.turned = gradient && i > 0;
     J.flip_entry = gradient && i < 2;
     J.entry_mul = gradient && i > 0 ? 1.f / c->scale : 1.f;
     J.exit_mul = gradient ? c->scale : 1.f;
   }
-  int64_t walks = 0;
-  for (int i = 0; i < P.jobs; ++i) walks += B * P.H * P.job[i].slices;
-  set_segments(P, walks);
+  set_segments(P, es_of(c));
   return P;
 }
 
 // The states before the segments: their size, and with a workspace their places.
 size_t lin_room(LinParams& P, void* ws) {
   size_t cur = 0;
-  for (int i = 0; i < P.jobs && P.segments > 1; ++i) {
+  for (int i = 0; i < P.jobs; ++i) {
     LinJob& J = P.job[i];
+    if (J.segments == 1) continue;
     if (ws) J.part = at<float>(ws, cur);
-    cur += align256((size_t)P.B * P.H * P.segments * J.kw * J.vw * 4);
+    cur += align256((size_t)P.B * P.H * J.segments * J.kw * J.vw * 4);
   }
   return cur;
 }
 
 bool lin_grid_ok(const LinParams& P) {
   int64_t most = 0;
-  for (int i = 0; i < P.jobs; ++i) most = std::max(most, (int64_t)P.B * P.H * P.segments * P.job[i].slices);
-  return launch_ok((most + N_XCD) * P.jobs, 512) && launch_ok((int64_t)P.B * P.H * 64, 256);
+  for (int i = 0; i < P.jobs; ++i) most = std::max(most, (int64_t)P.B * P.H * P.job[i].segments * P.job[i].slices);
+  return launch_ok((most + N_XCD) * P.jobs, 768) && launch_ok((int64_t)P.B * P.H * 64, 256);
 }
 
 size_t lin_room_bytes(const msgla_linear_config* cfg, int64_t B, int64_t L, bool gradient) {

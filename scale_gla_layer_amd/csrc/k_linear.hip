@@ -5,10 +5,10 @@
 //   out_i = scale (gamma^(i+1) q_i S + sum_{j <= i} gamma^(i-j) (q_i . k_j) v_j)
 //   S' = gamma^n S + sum_j gamma^(n-1-j) k_j^T v_j
 // so a walk over the chunks is four matrix products each.  A workgroup walks one
-// (sequence, head) for 64 columns of v.  Four of its waves form the outputs, of 16
-// positions each; four others keep the state in their accumulators, a quarter of its
-// rows each, and leave it, rounded, in LDS, where it is an operand of the next chunk's
-// outputs.  Both work on a chunk at the same time, with half the registers that one
+// (sequence, head) for 64 or 128 columns of v.  Four of its waves form the outputs, of
+// 16 positions each; four or eight others keep the state in their accumulators, an
+// equal share of its rows each, and leave it, rounded, in LDS, where it is an operand of
+// the next chunk's outputs.  Both work on a chunk at the same time, with half the registers that one
 // wave for both would need, while asynchronous copies bring the next one.  All
 // exponents of gamma are at least 0, so nothing overflows, and a decay of 0
 // (log_decay of minus infinity) is exact.
@@ -81,19 +81,21 @@ template <int W, int WAVES> struct ChunkCopy {
   }
 };
 
-// Waves a SIMD: two workgroups of eight a CU where LDS holds them.
-template <typename T, int KWP, bool OUT> constexpr int lin_waves() {
-  return OUT ? (sizeof(T) == 2 && KWP <= 128 ? 4 : 2) : sizeof(T) == 2 && KWP <= 128 ? 3 : 1;
+template <typename T, int KWP, int VS> constexpr int state_waves() { return lin_state_waves(sizeof(T), KWP, VS); }
+// Waves a SIMD: of one workgroup, or of the two that LDS holds.
+template <typename T, int KWP, int VS, bool OUT> constexpr int lin_waves() {
+  return sizeof(T) == 4 ? (OUT ? 2 : 1) : state_waves<T, KWP, VS>() == 8 ? (OUT ? 3 : 2) : OUT ? 4 : 3;
 }
 // Stages of LDS for a chunk's keys and values: two where they fit.
 template <typename T, int KWP> constexpr int lin_stages() { return sizeof(T) == 4 && KWP == 256 ? 1 : 2; }
 
 // OUT: the walk; else what a segment adds to the state (the state's waves alone).
-template <typename T, int KWP, bool OUT>
-__global__ __launch_bounds__(OUT ? 512 : 256, (lin_waves<T, KWP, OUT>())) void k_linear(const LinParams P) {
-  constexpr int ES = sizeof(T), VS = LIN_COLUMNS, C = LIN_CHUNK, WAVES = OUT ? 8 : 4, STAGES = lin_stages<T, KWP>();
+template <typename T, int KWP, int VS, bool OUT>
+__global__ __launch_bounds__(64 * (state_waves<T, KWP, VS>() + (OUT ? 4 : 0)), (lin_waves<T, KWP, VS, OUT>())) void k_linear(const LinParams P) {
+  constexpr int ES = sizeof(T), C = LIN_CHUNK, NSW = state_waves<T, KWP, VS>(), STAGES = lin_stages<T, KWP>();
+  constexpr int COPYING = OUT && NSW == 4 ? 8 : NSW;  // waves that copy: all, or of twelve those with the state
   constexpr int NQ = KWP * ES / 64;            // slabs of a row
-  constexpr int KT = KWP / 64, VT = VS / 16;   // a state wave's tiles
+  constexpr int KT = KWP / 16 / NSW, VT = VS / 16;   // a state wave's tiles
   constexpr int SL = C / blk_slab<T>();        // slabs of a chunk's positions
   constexpr int WK = KWP * ES / 16, WV = VS * ES / 16, KB = C * WK * 16, STAGE = KB + C * WV * 16, SB = VS * WK * 16;
   constexpr bool LO = ES == 2;
@@ -103,7 +105,7 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (lin_waves<T, KWP, OUT>())) void k
   const int tid = threadIdx.x, lane = tid & 63, c16 = lane & 15, a = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const LinJob& J = P.job[blockIdx.y];
-  const int nseg = OUT ? P.segments : P.segments - 1;
+  const int nseg = OUT ? J.segments : J.segments - 1;
   const int total = P.B * P.H * nseg * J.slices, per = (total + N_XCD - 1) / N_XCD;
   // an XCD takes neighbouring slices, which read the same q and k
   const int w = remap_xcd(blockIdx.x, per);
@@ -111,15 +113,17 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (lin_waves<T, KWP, OUT>())) void k
   const int slice = w % J.slices, seg = w / J.slices % nseg, bh = w / J.slices / nseg, b = bh / P.H, h = bh - b * P.H;
   const int len = lin_len(P, b), v0 = slice * VS;
   const float lg2 = lin_log2(P.log_decay, h);
-  const int first = seg * P.seg_chunks * C, past = min(P.L, first + P.seg_chunks * C), end = min(past, len);
+  const int first = seg * J.seg_chunks * C, past = min(P.L, first + J.seg_chunks * C), end = min(past, len);
   const int kw = J.kw * ES, vw = min(VS, J.vw - v0) * ES;  // bytes of a row, and of its part
   const bool turned = J.turned != 0;
   auto position = [&](int n) { return turned ? len - 1 - n : n; };  // of the walk's n-th token
-  const ChunkCopy<WK, WAVES> kc(J.k.p + b * J.k.sb + h * J.k.sh, J.k.st, kw, turned, wave, lane);
-  const ChunkCopy<WV, WAVES> vc(J.v.p + b * J.v.sb + h * J.v.sh + v0 * ES, J.v.st, vw, turned, wave, lane);
+  const int copier = OUT && NSW == 8 ? wave - 4 : wave;
+  const ChunkCopy<WK, COPYING> kc(J.k.p + b * J.k.sb + h * J.k.sh, J.k.st, kw, turned, copier, lane);
+  const ChunkCopy<WV, COPYING> vc(J.v.p + b * J.v.sb + h * J.v.sh + v0 * ES, J.v.st, vw, turned, copier, lane);
   auto fetch = [&](int n0, char* to) {
-    kc.issue(position(n0), end - n0, to, wave, lane);
-    vc.issue(position(n0), end - n0, to + KB, wave, lane);
+    if (copier < 0) return;
+    kc.issue(position(n0), end - n0, to, copier, lane);
+    vc.issue(position(n0), end - n0, to + KB, copier, lane);
   };
   if (first < end) fetch(first, stage0);
   const Rows<WK> row(lane);
@@ -250,10 +254,10 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (lin_waves<T, KWP, OUT>())) void k
         for (int e = 0; e < 4; ++e) f(S[i][j], e, 16 * (k0 + i) + 4 * a + e, v0 + 16 * j + c16);
   };
   const int64_t size = (int64_t)J.kw * J.vw;
-  if (OUT && (P.segments > 1 || J.entry)) {
-    const bool flip = P.segments == 1 && J.flip_entry;
-    const float* p = P.segments > 1 ? J.part + ((int64_t)bh * P.segments + seg) * size : J.entry + bh * size;
-    const float mul = P.segments > 1 ? 1.f : J.entry_mul;
+  if (OUT && (J.segments > 1 || J.entry)) {
+    const bool flip = J.segments == 1 && J.flip_entry;
+    const float* p = J.segments > 1 ? J.part + ((int64_t)bh * J.segments + seg) * size : J.entry + bh * size;
+    const float mul = J.segments > 1 ? 1.f : J.entry_mul;
     each([&](f32x4& s, int e, int r, int c) {
       const int64_t x = min(r, J.kw - 1), y = min(c, J.vw - 1);
       s[e] = p[flip ? y * J.kw + x : x * J.vw + y];
@@ -348,36 +352,40 @@ __global__ __launch_bounds__(OUT ? 512 : 256, (lin_waves<T, KWP, OUT>())) void k
       if (r < J.kw && c < J.vw) p[(int64_t)r * J.vw + c] = s[e] * mul;
     });
   };
-  if constexpr (!OUT) store(J.part + ((int64_t)bh * P.segments + seg + 1) * size, 1.f);
-  else if (J.exit && seg == P.segments - 1) store(J.exit + bh * size, J.exit_mul * (turned && len > 0 ? lin_power(1, lg2) : 1.f));
+  if constexpr (!OUT) store(J.part + ((int64_t)bh * J.segments + seg + 1) * size, 1.f);
+  else if (J.exit && seg == J.segments - 1) store(J.exit + bh * size, J.exit_mul * (turned && len > 0 ? lin_power(1, lg2) : 1.f));
 }
 
 // The states before the segments from what each segment adds: four elements a
-// thread, whose loads do not wait for one another.
+// thread, eight segments' loads under way at a time.
 __global__ __launch_bounds__(256) void k_linear_scan(const LinParams P) {
   const LinJob& J = P.job[blockIdx.y];
   const int64_t size = (int64_t)J.kw * J.vw, i = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
   const int bh = (int)(i / size), e = (int)(i - bh * size);  // size is a multiple of 64
   if (bh >= P.B * P.H) return;
-  const int len = lin_len(P, bh / P.H), whole = P.seg_chunks * LIN_CHUNK;
-  const float lg2 = lin_log2(P.log_decay, bh % P.H);
-  float* p = J.part + (int64_t)bh * P.segments * size + e;
-  f32x4 s = zero4(), add[LIN_SEGMENTS - 1];
+  const int len = lin_len(P, bh / P.H), whole = J.seg_chunks * LIN_CHUNK;
+  const float lg2 = lin_log2(P.log_decay, bh % P.H), keep = lin_power(whole, lg2);
+  float* p = J.part + (int64_t)bh * J.segments * size + e;
+  f32x4 s = zero4();
   if (J.entry) {
     const int r = e / J.vw, c = e - r * J.vw;
 #pragma unroll
     for (int x = 0; x < 4; ++x) s[x] = J.entry[bh * size + (J.flip_entry ? (int64_t)(c + x) * J.kw + r : e + x)] * J.entry_mul;
   }
+  constexpr int AHEAD = 8;
+  for (int m0 = 1; m0 < J.segments; m0 += AHEAD) {
+    f32x4 add[AHEAD];
 #pragma unroll
-  for (int m = 0; m < LIN_SEGMENTS - 1; ++m) add[m] = __builtin_bit_cast(f32x4, ld16(p + min(m + 1, P.segments - 1) * size));
-  st16(p, __builtin_bit_cast(u32x4, s));
+    for (int m = 0; m < AHEAD; ++m) add[m] = __builtin_bit_cast(f32x4, ld16(p + min(m0 + m, J.segments - 1) * size));
 #pragma unroll
-  for (int m = 0; m < LIN_SEGMENTS - 1; ++m) {
-    if (m + 1 >= P.segments) break;
-    const int n = max(0, min(len - m * whole, whole));
-    if (n) s = lin_power(n - (m == 0 ? J.turned : 0), lg2) * s + add[m];
-    st16(p + (m + 1) * size, __builtin_bit_cast(u32x4, s));
+    for (int m = 0; m < AHEAD; ++m) {
+      if (m0 + m >= J.segments) break;
+      st16(p + (m0 + m - 1) * size, __builtin_bit_cast(u32x4, s));
+      const int n = max(0, min(len - (m0 + m - 1) * whole, whole));  // tokens of the segment before
+      if (n) s = (n == whole && m0 + m > 1 ? keep : lin_power(n - (m0 + m == 1 ? J.turned : 0), lg2)) * s + add[m];
+    }
   }
+  st16(p + (J.segments - 1) * size, __builtin_bit_cast(u32x4, s));
 }
 
 // One token: a workgroup takes LIN_STEP_COLUMNS columns of one state, four a lane.
@@ -425,35 +433,40 @@ template <typename T> __global__ __launch_bounds__(LIN_STEP_THREADS) void k_line
   }
 }
 
-template <typename T, int KWP, bool OUT> void walk_jobs(const LinParams& P, hipStream_t st) {
+template <typename T, int KWP, int VS, bool OUT> void walk_jobs(const LinParams& P, hipStream_t st) {
   int64_t most = 0;
   for (int i = 0; i < P.jobs; ++i) {
-    const int64_t n = (int64_t)P.B * P.H * (OUT ? P.segments : P.segments - 1) * P.job[i].slices;
+    const int64_t n = (int64_t)P.B * P.H * (P.job[i].segments - (OUT ? 0 : 1)) * P.job[i].slices;
     most = n > most ? n : most;
   }
   const int64_t grid = (most + N_XCD - 1) / N_XCD * N_XCD;
-  hipLaunchKernelGGL((k_linear<T, KWP, OUT>), dim3((unsigned)grid, (unsigned)P.jobs), dim3(OUT ? 512 : 256), 0, st, P);
+  const int threads = 64 * (state_waves<T, KWP, VS>() + (OUT ? 4 : 0));
+  hipLaunchKernelGGL((k_linear<T, KWP, VS, OUT>), dim3((unsigned)grid, (unsigned)P.jobs), dim3(threads), 0, st, P);
 }
 
-// Jobs of one padded key width share a launch.
-template <typename T, int KWP> void walk(const LinParams& all, hipStream_t st) {
+// Jobs of one shape share a launch.
+template <typename T, int KWP, int VS> void walk(const LinParams& all, hipStream_t st) {
   LinParams P = all;
   P.jobs = 0;
   for (int i = 0; i < all.jobs; ++i)
-    if (lin_kwp(all.job[i].kw) == KWP) P.job[P.jobs++] = all.job[i];
+    if (lin_kwp(all.job[i].kw) == KWP && lin_columns(sizeof(T), KWP, all.job[i].vw) == VS) P.job[P.jobs++] = all.job[i];
   if (!P.jobs) return;
-  if (P.segments > 1) {
-    walk_jobs<T, KWP, false>(P, st);
+  if (P.job[0].segments > 1) {
+    walk_jobs<T, KWP, VS, false>(P, st);
     int64_t most = 0;
     for (int i = 0; i < P.jobs; ++i) most = std::max(most, (int64_t)P.B * P.H * P.job[i].kw * P.job[i].vw);
     hipLaunchKernelGGL(k_linear_scan, dim3((unsigned)((most / 4 + 255) / 256), (unsigned)P.jobs), dim3(256), 0, st, P);
   }
-  walk_jobs<T, KWP, true>(P, st);
+  walk_jobs<T, KWP, VS, true>(P, st);
 }
 template <typename T> void walk_all(const LinParams& P, hipStream_t st) {
-  walk<T, 64>(P, st);
-  walk<T, 128>(P, st);
-  walk<T, 256>(P, st);
+  walk<T, 64, 64>(P, st);
+  walk<T, 128, 64>(P, st);
+  walk<T, 256, 64>(P, st);
+  if constexpr (sizeof(T) == 2) {
+    walk<T, 64, 128>(P, st);
+    walk<T, 128, 128>(P, st);
+  }
 }
 
 }  // namespace

@@ -11,7 +11,7 @@ struct LinHeads {
 };
 
 constexpr int LIN_CHUNK = 64;     // positions of a step of a walk
-constexpr int LIN_SEGMENTS = 16;  // parts of a sequence that are walked side by side, at most
+constexpr int LIN_SEGMENTS = 32;  // parts of a sequence that are walked side by side, at most
 
 // One walk: out_t = scale q_t S_t, S_t = gamma S_{t-1} + k_t^T v_t, from the first
 // token to the last or back.
@@ -25,6 +25,7 @@ struct LinJob {
   int turned;          // from the last token to the first; entry is then not decayed by the first step, exit is once more
   int flip_entry;      // entry is [vw][kw]
   int slices;          // of the columns of v
+  int segments, seg_chunks;  // segments of so many chunks
 };
 
 struct LinParams {
@@ -35,10 +36,14 @@ struct LinParams {
   const uint8_t* mask;  // the step's
   int B, L, H;
   float scale;
-  int segments, seg_chunks;  // segments of so many chunks
 };
 
-constexpr int LIN_COLUMNS = 64;  // columns of v that a workgroup takes
+// Columns of v that a workgroup takes: 128 share the work on the keys where there are
+// as many and the state's two roundings leave LDS for them.  es: bytes of an element;
+// kwp: padded width of the keys.
+constexpr int lin_columns(int es, int kwp, int vw) { return es == 2 && kwp <= 128 && vw > 64 ? 128 : 64; }
+// Waves that keep the state: eight where one workgroup fills a CU, four where two share one.
+constexpr int lin_state_waves(int es, int kwp, int columns) { return es == 2 && kwp * columns >= 128 * 128 ? 8 : 4; }
 inline int lin_kwp(int kw) { return kw <= 64 ? 64 : kw <= 128 ? 128 : 256; }
 
 hipError_t launch_linear(const LinParams& P, bool bf16_path, hipStream_t st);
