@@ -28,7 +28,7 @@ int es_of(const msgla_layer_norm_config* c) { return c->dtype == MSGLA_BF16 ? 2 
 int64_t row_bytes(const msgla_layer_norm_config* c) { return (int64_t)c->width * es_of(c); }
 
 size_t ln_room(const msgla_layer_norm_config* c, int64_t B, int64_t L) {
-  return align256((size_t)ln_parts(B * L, row_bytes(c)) * 2 * c->width * 4);
+  return align256((size_t)ln_parts(B * L, row_bytes(c), es_of(c)) * 2 * c->width * 4);
 }
 
 }  // namespace
@@ -57,9 +57,6 @@ msgla_status msgla_layer_norm_forward(const msgla_layer_norm_config* cfg, const 
   P.L = (int)L;
   P.D = cfg->width;
   P.eps = cfg->eps;
-  const LnShape s = ln_shape(row_bytes(cfg));
-  const int64_t side = s.threads / s.lanes;
-  if (!launch_ok((P.rows + side - 1) / side, s.threads)) return MSGLA_ERR_UNSUPPORTED;
   HIP_TRY(launch_layer_norm(P, es == 2, static_cast<hipStream_t>(stream)));
   return MSGLA_OK;
 }
@@ -91,7 +88,7 @@ msgla_status msgla_layer_norm_backward(const msgla_layer_norm_config* cfg, const
   P.L = (int)L;
   P.D = cfg->width;
   P.eps = cfg->eps;
-  P.parts = ln_parts(P.rows, row_bytes(cfg));
+  P.parts = ln_parts(P.rows, row_bytes(cfg), es);
   HIP_TRY(launch_layer_norm_backward(P, es == 2, static_cast<hipStream_t>(stream)));
   return MSGLA_OK;
 }

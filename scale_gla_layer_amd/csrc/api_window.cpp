@@ -10,6 +10,9 @@ namespace {
 
 constexpr size_t BAD = (size_t)-1;
 constexpr int N_CU = 256;
+#ifndef FEWTILES
+#define FEWTILES 192
+#endif
 
 bool win_config_ok(const msgla_window_config* c) {
   if (!c || (c->dtype != MSGLA_F32 && c->dtype != MSGLA_BF16)) return false;
@@ -74,8 +77,9 @@ struct Take {
   }
 };
 
-// Few rows: tiles of 16, their keys dealt to as many workgroups as give about 1024,
-// each wave a unit of 32 keys at least.
+// Few rows: tiles of 16, their keys dealt to as many workgroups as there are CUs, each
+// wave a unit of 32 keys at least (a step of 16 sequences with 16 / 4 heads of 128 and
+// a window of 4096: 31 us; with twice as many workgroups 33, with four times 38).
 struct FewWs {
   size_t po, pm, total;
 };
@@ -83,7 +87,7 @@ FewWs set_few(WinParams& P) {
   set_tiles(P, WIN_FEW_ROWS);
   const int64_t keys = std::min<int64_t>(P.S, (int64_t)P.window + P.n_sink + P.QT);
   const int64_t units = (keys + WIN_FEW_KEYS - 1) / WIN_FEW_KEYS + 1;
-  P.parts = (int)std::max<int64_t>(1, std::min<int64_t>((units + WIN_FEW_WAVES - 1) / WIN_FEW_WAVES, 1024 / P.tiles));
+  P.parts = (int)std::max<int64_t>(1, std::min<int64_t>((units + WIN_FEW_WAVES - 1) / WIN_FEW_WAVES, N_CU / P.tiles));
   FewWs w{};
   Take take;
   if (P.parts > 1) {
@@ -109,7 +113,7 @@ bool many_grid_ok(const WinParams& P) { return launch_ok(P.tiles + N_XCD, 4 * P.
 // most CUs without one.
 bool use_few(WinParams P) {
   set_many(P);
-  return P.tiles < 192;
+  return P.tiles < FEWTILES;
 }
 
 struct GradWs {
