@@ -10,9 +10,6 @@ namespace {
 
 constexpr size_t BAD = (size_t)-1;
 constexpr int N_CU = 256;
-#ifndef FEWTILES
-#define FEWTILES 192
-#endif
 
 bool win_config_ok(const msgla_window_config* c) {
   if (!c || (c->dtype != MSGLA_F32 && c->dtype != MSGLA_BF16)) return false;
@@ -109,11 +106,13 @@ bool few_grid_ok(const WinParams& P) {
 }
 bool many_grid_ok(const WinParams& P) { return launch_ok(P.tiles + N_XCD, 4 * P.tile_rows); }
 
-// Whether the forward deals keys to workgroups: where the tiles of many rows leave
-// most CUs without one.
+// Whether the forward deals keys to workgroups: where the tiles of many rows give work
+// to a quarter of the CUs at most (16 / 4 heads of 128, window 512, bf16: 64 tiles take
+// 17.4 us dealt and 19.2 whole, 128 tiles 35 and 24; 8 heads of fp32: 32 tiles 26 and
+// 74, 64 tiles 50 and 75, 144 tiles of 6 / 2 heads 43 and 34).
 bool use_few(WinParams P) {
   set_many(P);
-  return P.tiles < FEWTILES;
+  return P.tiles <= N_CU / 4;
 }
 
 struct GradWs {
