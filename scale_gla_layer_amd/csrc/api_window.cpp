@@ -130,8 +130,10 @@ GradWs set_grad(WinParams& P, int es) {
   const int sinks = std::min(P.n_sink, P.S);
   P.sink_tiles = P.S > P.window ? cdiv(sinks, WIN_SINK) : 0;
   if (P.sink_tiles > 0) {
+    // two workgroups a CU, of two sets at least (2 x 16 / 4 heads of 4096 positions: 22 us, with four a CU of four
+    // sets 28; fp32, 3 x 6 / 2 heads of 999: 25 and 32)
     const int64_t rows = (int64_t)std::min(P.L, P.S - P.window) * P.G;
-    P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>((4 * N_CU - 1 + heads * P.sink_tiles) / (heads * P.sink_tiles), rows / 128));
+    P.sink_parts = (int)std::max<int64_t>(1, std::min<int64_t>((2 * N_CU - 1 + heads * P.sink_tiles) / (heads * P.sink_tiles), rows / 64));
   }
   P.joined = P.key_parts > 1 ? P.key_tiles : P.sink_tiles > 0 ? cdiv(sinks, P.key_tile) : 0;
   const size_t width = (size_t)(win_dkp(P.dkw) + win_dvp(P.dvw)) * 4;

@@ -111,11 +111,11 @@ __global__ __launch_bounds__(64 * WIN_TILES, sizeof(T) == 4 && DVP == 256 ? 1 : 
       f32x16 s = zero_tile();
 #pragma unroll
       for (int c = 0; c < NK; ++c) s = mma32<T>(krow.read(stage, x, c), q[c], s);
-      if (j0 + 31 > pmin || (j0 <= pmax - P.window && j0 + 32 > P.n_sink)) {  // an edge of some row's window
+      if (win_edge(P, j0, 32, pmin, pmax)) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = j0 + 8 * (i >> 2) + 4 * h2 + (i & 3);
-          if (j > row.p || (j <= rlow && j >= P.n_sink)) s[i] = -__builtin_inff();
+          s[i] = win_out_of(P, j, row.p, rlow) ? -__builtin_inff() : s[i];
         }
       }
       float mx = s[0];

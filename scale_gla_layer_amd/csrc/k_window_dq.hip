@@ -104,6 +104,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dq(c
       unit(u + 1, stage1, stage0, stage2);
       unit(u + 2, stage2, stage1, stage0);
     }
+    products_done();
   };
 
   if (wave < PAIRS) {  // the weights
@@ -115,11 +116,11 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dq(c
       f32x16 s = zero_tile();
 #pragma unroll
       for (int c = 0; c < NK; ++c) s = mma32<T>(krow.read(ks, 0, c), q[c], s);
-      if (j0 + 31 > pmin || (j0 <= pmax - P.window && j0 + 32 > P.n_sink)) {  // an edge of some row's window
+      if (win_edge(P, j0, 32, pmin, pmax)) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = j0 + 8 * (i >> 2) + 4 * h2 + (i & 3);
-          if (j > row.p || (j <= rlow && j >= P.n_sink)) s[i] = -__builtin_inff();
+          s[i] = win_out_of(P, j, row.p, rlow) ? -__builtin_inff() : s[i];
         }
       }
 #pragma unroll

@@ -196,7 +196,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dkdv
         for (int i = 0; i < 16; ++i) {
           const int r = 8 * (i >> 2) + 4 * h2 + (i & 3);
           const int64_t p = x.pa + walk.div(x.rem + r);
-          if (!is_key || set * 32 + r >= rows || p < near || p >= far) s[i] = 0.f;
+          s[i] = (!is_key | (set * 32 + r >= rows) | (p < near) | (p >= far)) ? 0.f : s[i];
         }
       }
       tile_put(weights[set & 1][pair], s, lane);

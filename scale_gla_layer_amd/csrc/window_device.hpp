@@ -225,6 +225,27 @@ __device__ __forceinline__ char* win_out(const WinHeads& t, int64_t b, int64_t i
   return t.p + b * t.sb + i * t.st + h * t.sh;
 }
 
+// Wait states for the result of the last matrix product (16 passes at most), where a
+// loop's end and a barrier are all that lies between it and its first reader: hipcc
+// 7.2 leaves out some on the loop's shortest way.
+__device__ __forceinline__ void products_done() {
+  __builtin_amdgcn_sched_barrier(0);
+  asm volatile("s_nop 15\n\ts_nop 3");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// Whether a row at a position from pmin to pmax does not attend all of the n keys from
+// j0 on.  Operators that take both sides make one branch of it: where a branch in two
+// steps follows a matrix product, hipcc 7.2 counts the wait states that the product's
+// result needs along the longer way alone.
+__device__ __forceinline__ bool win_edge(const WinParams& P, int j0, int n, int pmin, int pmax) {
+  return (j0 + n - 1 > pmin) | ((j0 <= pmax - P.window) & (j0 + n > P.n_sink));
+}
+// Whether a row at position p, whose window begins behind `low`, does not attend key j.
+__device__ __forceinline__ bool win_out_of(const WinParams& P, int j, int p, int low) {
+  return (j > p) | ((j <= low) & (j >= P.n_sink));
+}
+
 __device__ __forceinline__ int wave_min(int v) {
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) v = min(v, __shfl_xor(v, o));
