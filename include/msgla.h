@@ -684,8 +684,8 @@ size_t msgla_linear_attention_backward_workspace_bytes(const msgla_linear_config
  *         q, k and v hold there has no influence, out is 0 and the state stays.
  *   state_in: [B][heads][d_k][d_v] fp32 before the first token, or NULL for 0
  *   state_out: NULL, or receives the state after the last token; may be state_in.
- * States are 16-byte aligned.  A NaN or infinity of a token may reach every
- * output of its sequence and head.  The result is the same bit for bit from call
+ * States are 16-byte aligned.  out may not overlap an input or a state.  A NaN or
+ * infinity of a token may reach every output of its sequence and head.  The result is the same bit for bit from call
  * to call.
  */
 msgla_status msgla_linear_attention_forward(const msgla_linear_config* cfg, const msgla_heads* q,
@@ -761,7 +761,8 @@ size_t msgla_window_attention_step_workspace_bytes(const msgla_window_config* cf
  * not below lens[b] is padding: its output is 0, its lse minus infinity and its
  * gradient 0.  What k and v hold behind lens[b], or at positions that no query
  * attends, is not used.  A NaN or infinity of k, v, q or dout at a position that is
- * used may reach every row of its sequence and key-value head.
+ * used may reach every row of its sequence and key-value head.  out may not overlap
+ * an input.
  */
 msgla_status msgla_window_attention(const msgla_window_config* cfg, const msgla_heads* q,
                                     const msgla_heads* k, const msgla_heads* v, const int32_t* start,
@@ -772,7 +773,8 @@ msgla_status msgla_window_attention(const msgla_window_config* cfg, const msgla_
 /*
  * Its vector-Jacobian product: from dout [B][L][heads_q][d_v], with the forward's
  * inputs, out and lse, writes dq, and dk and dv for all S positions (0 where
- * nothing attends).  The result is the same bit for bit from call to call.
+ * nothing attends).  No output may overlap an input or another output.  The
+ * result is the same bit for bit from call to call.
  */
 msgla_status msgla_window_attention_backward(const msgla_window_config* cfg, const msgla_heads* q,
                                              const msgla_heads* k, const msgla_heads* v,
@@ -804,8 +806,9 @@ msgla_status msgla_window_attention_append(const msgla_window_config* cfg, const
 /* One streaming step of B sequences: puts each one's new key and value (k_t
  * [B][heads_kv][d_k], v_t [B][heads_kv][d_v]) at position pos[b] and attends the
  * window and the first tokens with q_t [B][heads_q][d_k] -> out_t
- * [B][heads_q][d_v].  stride_t of the four _t tensors is not read.  A position
- * without a place, or below 0, puts nothing and gives an output row of 0. */
+ * [B][heads_q][d_v].  stride_t of the four _t tensors is not read, and none of them
+ * lies in the cache.  A position without a place, or below 0, puts nothing and gives
+ * an output row of 0. */
 msgla_status msgla_window_attention_step(const msgla_window_config* cfg, const msgla_heads* q_t,
                                          const msgla_heads* k_t, const msgla_heads* v_t,
                                          const int32_t* pos, int64_t B, int64_t S, const msgla_heads* k,

@@ -437,10 +437,10 @@ def _dense(name: str, t, shape, dtype, device):
     """The address of a contiguous t, or None for None."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
     _tensor(name, t, shape, dtype, device)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _f32(name: str, t, shape, device):

@@ -125,7 +125,8 @@ GradWs set_grad(WinParams& P, int es) {
   P.key_tiles = cdiv(P.S, P.key_tile);
   const int64_t queries = std::min<int64_t>(P.L, (int64_t)P.window + P.key_tile - 1);
   const int64_t sets = (queries * P.G + 31) / 32;
-  // Workgroups fill a CU each: as many as there are CUs, of four sets of 32 rows at least.
+  // Workgroups fill a CU each: as many as there are CUs, of four sets of 32 rows at least (fp32, 3 x 6 / 2 heads of
+  // 999: 47 us, with two sets 66, with eight 84).
   P.key_parts = (int)std::max<int64_t>(1, std::min<int64_t>((N_CU - 1 + heads * P.key_tiles) / (heads * P.key_tiles), sets / 4));
   const int sinks = std::min(P.n_sink, P.S);
   P.sink_tiles = P.S > P.window ? cdiv(sinks, WIN_SINK) : 0;

@@ -13,6 +13,8 @@
 //   The backward's workgroups keep their channels' sums of dy xh and dy in
 // registers over all their rows, and a second kernel adds the workgroups' sums in
 // order: the result does not vary from call to call.
+//   HBM-bound: B = 8, L = 2048, D = 1024 in bf16 takes 16.3 us forward (67 MB, 4.1 TB/s)
+// and 21 + 4 for the gradient (101 MB); a copy reaches 5.1 TB/s.
 #include <algorithm>
 
 #include "device_common.hpp"

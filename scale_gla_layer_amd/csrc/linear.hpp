@@ -39,10 +39,12 @@ struct LinParams {
 };
 
 // Columns of v that a workgroup takes: 128 share the work on the keys where there are
-// as many and the state's two roundings leave LDS for them.  es: bytes of an element;
+// as many and the state's two roundings leave LDS for them (B = 8, L = 2048, 4 heads of
+// 128 and 256: 66 us, with 64 columns 72; a single sequence of 512 34 and 30).  es: bytes of an element;
 // kwp: padded width of the keys.
 constexpr int lin_columns(int es, int kwp, int vw) { return es == 2 && kwp <= 128 && vw > 64 ? 128 : 64; }
-// Waves that keep the state: eight where one workgroup fills a CU, four where two share one.
+// Waves that keep the state: eight where one workgroup fills a CU (66 us at the size
+// above, with four 98), four where two share one.
 constexpr int lin_state_waves(int es, int kwp, int columns) { return es == 2 && kwp * columns >= 128 * 128 ? 8 : 4; }
 inline int lin_kwp(int kw) { return kw <= 64 ? 64 : kw <= 128 ? 128 : 256; }
 

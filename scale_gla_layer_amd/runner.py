@@ -372,7 +372,8 @@ class DeviceLayerNorm:
 
     def _forward(self, x, weight, bias, y):
         torch = _torch()
-        y = x.new_empty(x.shape) if y is None else y
+        if y is None:
+            y = torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
         mean = x.new_empty(x.shape[:2], dtype=torch.float32)
         rstd = torch.empty_like(mean)
         binding.msgla_layer_norm_forward(self.cfg, x, y, weight, bias, mean, rstd)
