@@ -59,13 +59,13 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dq(c
   const UnitCopy<WV, KT, WAVES> vc(P.v.p + b * P.v.sb + h * P.v.sh, P.v.st, vw, wave, lane);
   auto unit_key = [&](int u) { return (u < sinks ? u : from + u - sinks) * KT; };
   // the unit's rows; those that no row of the workgroup attends are replaced by one that is
-  auto fetch = [&](int u, char* stage) {
+  auto fetch = [&](int u, char* stage) __attribute__((always_inline)) {
     const int k0 = unit_key(u);
     if (k0 + KT - 1 <= last && (k0 >= low || k0 + KT <= P.n_sink) && kc.near() && vc.near()) {
       kc.whole(k0, stage, wave);
       vc.whole(k0, stage + KB, wave);
     } else {
-      auto key = [&](int r) {
+      auto key = [&](int r) __attribute__((always_inline)) {
         const int j = k0 + r;
         return (int64_t)(j <= last && (j >= low || j < P.n_sink) ? j : last);
       };
@@ -87,12 +87,15 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dq(c
 #pragma unroll
   for (int d = 0; d < NO; ++d) acc[d] = zero_tile();
   // work(u, stage) for each unit, `lag` units behind the copies, that some of the tile's rows attend
-  auto walk = [&](auto lag, auto work) {
-    auto one = [&](int u, const char* stage) {
+  auto walk = [&](auto lag, auto work) __attribute__((always_inline)) {
+    auto one = [&](int u, const char* stage) __attribute__((always_inline)) {
       const int j0 = unit_key(u);
-      if (j0 <= pmax && (j0 + 31 >= wlow || j0 < P.n_sink)) work(u, j0, stage);
+      if (j0 <= pmax && (j0 + 31 >= wlow || j0 < P.n_sink)) {
+        work(u, j0, stage);
+        if constexpr (PAIRS == 1) products_done();
+      }
     };
-    auto unit = [&](int u, const char* stage, const char* before, char* next) {
+    auto unit = [&](int u, const char* stage, const char* before, char* next) __attribute__((always_inline)) {
       if (u > units) return;
       if (u + 1 < units) fetch(u + 1, next);
       if constexpr (lag() == 0) {
@@ -108,7 +111,6 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dq(c
       unit(u + 1, stage1, stage0, stage2);
       unit(u + 2, stage2, stage1, stage0);
     }
-    products_done();
   };
 
   if (wave < PAIRS) {  // the weights
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dq(c
     const char* qr = win_at(P.q, b, li, hd);
 #pragma unroll
     for (int s = 0; s < NK; ++s) q[s] = live ? blk_ld(qr, 32 * s + 16 * h2, kw) : zero16();
-    walk(std::integral_constant<int, 0>(), [&](int u, int j0, const char* ks) {
+    walk(std::integral_constant<int, 0>(), [&](int u, int j0, const char* ks) __attribute__((always_inline)) {
       f32x16 s = zero_tile();
 #pragma unroll
       for (int c = 0; c < NK; ++c) s = mma32<T>(krow.read(ks, 0, c), q[c], s);
@@ -162,7 +164,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dq(c
     for (int s = 0; s < NV; ++s) delta += blk_dot<T>(g[s], live ? blk_ld(orow, 32 * s + 16 * h2, vw) : zero16());
     delta += __shfl_xor(delta, 32);
   }
-  walk(std::integral_constant<int, 1>(), [&](int u, int, const char* ks) {
+  walk(std::integral_constant<int, 1>(), [&](int u, int, const char* ks) __attribute__((always_inline)) {
     f32x16 dp = zero_tile();
 #pragma unroll
     for (int c = 0; c < NV; ++c) dp = mma32<T>(vrow.read(ks + KB, 0, c), g[c], dp);

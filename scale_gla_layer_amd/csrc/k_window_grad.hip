@@ -99,7 +99,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dkdv
   const SetCopy<WK, WAVES> qc(win_at(P.q, b, at0, h * P.G), P.q, P.G, kw, wave, lane);
   const SetCopy<WV, WAVES> gc(win_at(P.dout, b, at0, h * P.G), P.dout, P.G, vw, wave, lane);
   const float* stats = (lane < 32 ? P.nref : P.delta) + ((int64_t)b * P.Hq + h * P.G) * P.L + at0;
-  auto fetch = [&](int64_t set, char* to) {
+  auto fetch = [&](int64_t set, char* to) __attribute__((always_inline)) {
     const int64_t q0 = set * 32 / P.G;
     const int rem = (int)(set * 32 - q0 * P.G);
     qc.issue(walk, set, q0, rem, rows, kw, to, wave, lane);
@@ -127,8 +127,8 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dkdv
     int rem;
   };
   // work(set, place, stage) for each set, `lag` sets behind the copies, of which any row holds any of the pair's keys
-  auto stream = [&](auto lag, auto work) {
-    auto one = [&](int64_t set, const char* stage) {
+  auto stream = [&](auto lag, auto work) __attribute__((always_inline)) {
+    auto one = [&](int64_t set, const char* stage) __attribute__((always_inline)) {
       const int64_t q0 = set * 32 / P.G;
       Set x;
       x.rem = (int)(set * 32 - q0 * P.G);
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dkdv
       x.pb = x.pa + walk.div(x.rem + 31);
       if (SINK || (x.pb >= k0 && x.pa <= (int64_t)k0 + 30 + P.window)) work(set, x, stage);
     };
-    auto unit = [&](int64_t set, const char* stage, const char* before, char* next) {
+    auto unit = [&](int64_t set, const char* stage, const char* before, char* next) __attribute__((always_inline)) {
       if (set > end) return;
       if (set + 1 < end) fetch(set + 1, next);
       if constexpr (lag() == 0) {
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dkdv
     f32x16 dv[DVP / 32];
 #pragma unroll
     for (int d = 0; d < DVP / 32; ++d) dv[d] = zero_tile();
-    stream(std::integral_constant<int, 0>(), [&](int64_t set, const Set& x, const char* qs) {
+    stream(std::integral_constant<int, 0>(), [&](int64_t set, const Set& x, const char* qs) __attribute__((always_inline)) {
       const float* nref = reinterpret_cast<const float*>(qs + QB + GB) + 4 * h2;
       f32x16 s = zero_tile();
 #pragma unroll
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(128 * PAIRS, PAIRS == 4 ? 2 : 1) void k_window_dkdv
   f32x16 dk[DKP / 32];
 #pragma unroll
   for (int d = 0; d < DKP / 32; ++d) dk[d] = zero_tile();
-  stream(std::integral_constant<int, 1>(), [&](int64_t set, const Set&, const char* qs) {
+  stream(std::integral_constant<int, 1>(), [&](int64_t set, const Set&, const char* qs) __attribute__((always_inline)) {
     const float* delta = reinterpret_cast<const float*>(qs + QB + GB) + 32 + 4 * h2;
     f32x16 dp = zero_tile();
 #pragma unroll

@@ -225,9 +225,9 @@ __device__ __forceinline__ char* win_out(const WinHeads& t, int64_t b, int64_t i
   return t.p + b * t.sb + i * t.st + h * t.sh;
 }
 
-// Wait states for the result of the last matrix product (16 passes at most), where a
-// loop's end and a barrier are all that lies between it and its first reader: hipcc
-// 7.2 leaves out some on the loop's shortest way.
+// Wait states for the result of the last matrix product (16 passes at most), where
+// results that do not fit in vector registers are moved about behind a branch: hipcc
+// 7.2 leaves out some on the shortest way there.
 __device__ __forceinline__ void products_done() {
   __builtin_amdgcn_sched_barrier(0);
   asm volatile("s_nop 15\n\ts_nop 3");
