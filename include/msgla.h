@@ -761,8 +761,8 @@ size_t msgla_window_attention_step_workspace_bytes(const msgla_window_config* cf
  * not below lens[b] is padding: its output is 0, its lse minus infinity and its
  * gradient 0.  What k and v hold behind lens[b], or at positions that no query
  * attends, is not used.  A NaN or infinity of k, v, q or dout at a position that is
- * used may reach every row of its sequence and key-value head.  out may not overlap
- * an input.
+ * used may reach every row of its sequence and key-value head but padding, and
+ * every key's gradient there.  out may not overlap an input.
  */
 msgla_status msgla_window_attention(const msgla_window_config* cfg, const msgla_heads* q,
                                     const msgla_heads* k, const msgla_heads* v, const int32_t* start,

@@ -181,9 +181,11 @@ __global__ __launch_bounds__(64 * WIN_FEW_WAVES, sizeof(T) == 2 && DVP <= 128 ? 
       st16(P.po + pr * DVP + c, __builtin_bit_cast(u32x4, o));
     } else {
       const WinRow to(P, b, h, t, r);
-      const float inv = sum > 0.f ? 1.f / sum : sum == 0.f ? 0.f : sum;  // no key: 0; a NaN stays
+      const float inv = sum > 0.f ? 1.f / sum : sum;  // a NaN stays
       if (to.in && c < P.dvw) {
-        const float v[4] = {o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+        float v[4];  // no key: 0, whatever the tile's other rows attend
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = sum == 0.f ? 0.f : o[e] * inv;
         blk_st4<T>(win_out(P.o, b, to.i, to.head) + c * ES, v);
       }
       if (to.in && c == 0 && P.lse)
@@ -214,11 +216,11 @@ template <typename T, int DVP> __global__ __launch_bounds__(64) void k_window_jo
 #pragma unroll
     for (int d = 0; d < DVP / 64; ++d) o[d] += w * P.po[at * DVP + 64 * d + lane];
   }
-  const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+  const float inv = l > 0.f ? 1.f / l : l;  // a NaN stays
   T* out = reinterpret_cast<T*>(win_out(P.o, b, row.i, row.head));
 #pragma unroll
   for (int d = 0; d < DVP / 64; ++d)
-    if (64 * d + lane < P.dvw) out[64 * d + lane] = from_f32<T>(o[d] * inv);
+    if (64 * d + lane < P.dvw) out[64 * d + lane] = from_f32<T>(l == 0.f ? 0.f : o[d] * inv);  // no key: 0
   if (P.lse && lane == 0)
     P.lse[((int64_t)b * P.Hq + row.head) * P.L + row.i] = l == 0.f ? -__builtin_inff() : m * BLK_LN2 + logf(l);
 }
