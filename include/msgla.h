@@ -700,6 +700,8 @@ msgla_status msgla_linear_attention_forward(const msgla_linear_config* cfg, cons
  * (dLoss/dstate_out, or NULL for 0), with dS_t = gamma dS_{t+1} + scale q_t^T dout_t,
  *     dq_t = scale dout_t S_t^T,   dk_t = v_t dS_t^T,   dv_t = k_t dS_t
  * with 0 at padding, and dstate_in [B][heads][d_k][d_v] fp32 unless it is NULL.
+ * The state's gradient is kept divided by scale: dstate_out / scale has to be within
+ * fp32.
  * q, k, v, log_decay, lens and state_in are the forward's.  No output may overlap
  * an input or another output.
  */
