@@ -793,13 +793,15 @@ msgla_status msgla_window_attention_backward(const msgla_window_config* cfg, con
  * tokens: in slot n_sink + (p - n_sink) mod (S - n_sink).  It needs
  * S >= n_sink + window for that; in a shorter one positions from S on have no
  * place.  pos [B] int32 (device) is the number of tokens before a call; the
- * caller advances it.
+ * caller advances it.  A sequence whose pos is below 0 sits out: a call leaves its
+ * cache as it is, whatever number of tokens it brings.
  */
 
 /* Puts L new keys and values k_new [B][L][heads_kv][d_k], v_new [B][L][heads_kv][d_v]
  * (lens[b] of them, at most L; NULL: all) at positions pos[b] .. (NULL: from 0 on).
- * Of positions that share a slot the last one stays; positions without a place,
- * or below 0, are left out. */
+ * Of positions that share a slot the last one stays; positions without a place are
+ * left out.  Nothing is put for a sequence whose pos[b] is below 0, or whose number
+ * of tokens pos[b] + lens[b] would pass 2^31 - 1, which no later pos could give. */
 msgla_status msgla_window_attention_append(const msgla_window_config* cfg, const msgla_heads* k_new,
                                            const msgla_heads* v_new, const int32_t* pos,
                                            const int32_t* lens, int64_t B, int64_t L, int64_t S,
@@ -809,8 +811,8 @@ msgla_status msgla_window_attention_append(const msgla_window_config* cfg, const
  * [B][heads_kv][d_k], v_t [B][heads_kv][d_v]) at position pos[b] and attends the
  * window and the first tokens with q_t [B][heads_q][d_k] -> out_t
  * [B][heads_q][d_v].  stride_t of the four _t tensors is not read, and none of them
- * lies in the cache.  A position without a place, or below 0, puts nothing and gives
- * an output row of 0. */
+ * lies in the cache.  A position without a place, or below 0 (a sequence that sits
+ * out), puts nothing and gives an output row of 0. */
 msgla_status msgla_window_attention_step(const msgla_window_config* cfg, const msgla_heads* q_t,
                                          const msgla_heads* k_t, const msgla_heads* v_t,
                                          const int32_t* pos, int64_t B, int64_t S, const msgla_heads* k,

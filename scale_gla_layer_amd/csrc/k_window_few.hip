@@ -226,7 +226,9 @@ template <typename T, int DVP> __global__ __launch_bounds__(64) void k_window_jo
 }
 
 // A prefill's keys and values into their slots: one wave a position and head.  Of
-// the positions that share a slot the last one stays.
+// the positions that share a slot the last one stays.  A sequence with fewer than 0
+// tokens before sits out, as in the step, and so does one whose number of tokens a
+// later call could not be told.
 __global__ __launch_bounds__(256) void k_window_append(const WinParams P, int es) {
   const int lane = threadIdx.x & 63, h = blockIdx.y;
   const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);

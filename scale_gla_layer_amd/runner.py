@@ -496,7 +496,8 @@ class DeviceWindowAttention:
 
     def append(self, k_new, v_new, k, v, pos=None, lens=None):
         """A prefill's keys and values k_new [B, L, heads_kv, d_k], v_new [B, L, heads_kv, d_v] into rolling caches k, v of
-        S slots, from positions pos [B] int32 (None: 0) on; lens [B] int32: new tokens of each sequence."""
+        S slots, from positions pos [B] int32 (None: 0) on; lens [B] int32: new tokens of each sequence.  A sequence whose
+        pos is below 0 sits out, here and in the step: nothing of it is put into the caches."""
         _on(k_new, binding.msgla_window_attention_append, self.cfg, k_new, v_new, k, v, pos, lens)
 
     def step(self, q_t, k_t, v_t, k, v, pos, out_t=None):

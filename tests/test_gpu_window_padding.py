@@ -52,3 +52,18 @@ def test_step_without_a_place_beside_a_nan(dtype):
     pos = _i32([500, -1, 5000])
     out = h.step(qt, kt, vt, k, v, pos)
     assert (out[1] == 0).all() and torch.isfinite(out[::2].float()).all() and k[1].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_sequence_that_sits_out(dtype):
+    """pos below 0: append and step leave the sequence's cache as it is, also where tokens would reach positions from 0 on."""
+    cfg = WindowAttentionConfig(4, 2, 64, 64, 20, 3, None, dtype)
+    h, (_, k, v, _), (q, kn, vn, _) = _handle(cfg), _inputs(4, 1, 30, cfg, 6), _inputs(4, 50, 50, cfg, 7)
+    pos = _i32([0, -1, -7, 12])
+    want_k, want_v = k.clone(), v.clone()
+    h.append(kn, vn, k, v, pos=pos)
+    out = h.step(q[:, 0], kn[:, 3], vn[:, 3], k, v, pos)
+    for b in (1, 2):
+        assert torch.equal(k[b], want_k[b]) and torch.equal(v[b], want_v[b]) and (out[b] == 0).all()
+    for b in (0, 3):
+        assert not torch.equal(k[b], want_k[b]) and (out[b] != 0).any()
