@@ -38,14 +38,13 @@ int es_of(const msgla_linear_config* c) { return c->dtype == MSGLA_BF16 ? 2 : 4;
 // Segments of a sequence, of at least four chunks: no more than fill the CUs once with
 // the walks of jobs of this one's shape, which share a launch.
 void set_segments(LinParams& P, int es) {
-  auto columns = [es](const LinJob& J) { return lin_columns(es, lin_kwp(J.kw), J.vw); };
   const int chunks = cdiv(P.L, LIN_CHUNK);
   for (int i = 0; i < P.jobs; ++i) {
     LinJob& J = P.job[i];
     int64_t walks = 0;
     for (int j = 0; j < P.jobs; ++j)
-      if (lin_kwp(P.job[j].kw) == lin_kwp(J.kw) && columns(P.job[j]) == columns(J)) walks += (int64_t)P.B * P.H * P.job[j].slices;
-    const bool share = es == 2 && lin_state_waves(es, lin_kwp(J.kw), columns(J)) == 4;
+      if (lin_kwp(P.job[j].kw) == lin_kwp(J.kw) && P.job[j].columns == J.columns) walks += (int64_t)P.B * P.H * P.job[j].slices;
+    const bool share = es == 2 && lin_state_waves(es, lin_kwp(J.kw), J.columns) == 4;
     const int n = (int)std::max<int64_t>(1, std::min<int64_t>({(share ? 2 * N_CU : N_CU) / walks, (int64_t)LIN_SEGMENTS, (int64_t)chunks / 4}));
     J.seg_chunks = cdiv(chunks, n);
     J.segments = cdiv(chunks, J.seg_chunks);
@@ -63,11 +62,18 @@ LinParams lin_params(const msgla_linear_config* c, int64_t B, int64_t L, bool gr
     LinJob& J = P.job[i];
     J.kw = gradient && i < 2 ? c->d_v : c->d_k;
     J.vw = gradient && i < 2 ? c->d_k : c->d_v;
-    J.slices = cdiv(J.vw, lin_columns(es_of(c), lin_kwp(J.kw), J.vw));
     J.turned = gradient && i > 0;
     J.flip_entry = gradient && i < 2;
     J.entry_mul = gradient && i > 0 ? 1.f / c->scale : 1.f;
     J.exit_mul = gradient ? c->scale : 1.f;
+  }
+  for (int i = 0; i < P.jobs; ++i) {
+    LinJob& J = P.job[i];
+    int64_t walks = 0;  // of 128 columns, in a launch of their own
+    for (int j = 0; j < P.jobs; ++j)
+      if (lin_kwp(P.job[j].kw) == lin_kwp(J.kw) && P.job[j].vw > 64) walks += B * c->heads * cdiv(P.job[j].vw, 128);
+    J.columns = lin_columns(es_of(c), lin_kwp(J.kw), J.vw, walks, walks * cdiv(P.L, LIN_CHUNK));
+    J.slices = cdiv(J.vw, J.columns);
   }
   set_segments(P, es_of(c));
   return P;

@@ -454,7 +454,7 @@ template <typename T, int KWP, int VS> void walk(const LinParams& all, hipStream
   LinParams P = all;
   P.jobs = 0;
   for (int i = 0; i < all.jobs; ++i)
-    if (lin_kwp(all.job[i].kw) == KWP && lin_columns(sizeof(T), KWP, all.job[i].vw) == VS) P.job[P.jobs++] = all.job[i];
+    if (lin_kwp(all.job[i].kw) == KWP && all.job[i].columns == VS) P.job[P.jobs++] = all.job[i];
   if (!P.jobs) return;
   if (P.job[0].segments > 1) {
     walk_jobs<T, KWP, VS, false>(P, st);
@@ -468,10 +468,7 @@ template <typename T> void walk_all(const LinParams& P, hipStream_t st) {
   walk<T, 64, 64>(P, st);
   walk<T, 128, 64>(P, st);
   walk<T, 256, 64>(P, st);
-  if constexpr (sizeof(T) == 2) {
-    walk<T, 64, 128>(P, st);
-    walk<T, 128, 128>(P, st);
-  }
+  if constexpr (sizeof(T) == 2) walk<T, 128, 128>(P, st);
 }
 
 }  // namespace

@@ -24,7 +24,7 @@ struct LinJob {
   int kw, vw;          // widths of q and k, and of v and o
   int turned;          // from the last token to the first; entry is then not decayed by the first step, exit is once more
   int flip_entry;      // entry is [vw][kw]
-  int slices;          // of the columns of v
+  int columns, slices; // of v: a workgroup's, and the workgroups they make
   int segments, seg_chunks;  // segments of so many chunks
 };
 
@@ -38,11 +38,17 @@ struct LinParams {
   float scale;
 };
 
-// Columns of v that a workgroup takes: 128 share the work on the keys where there are
-// as many and the state's two roundings leave LDS for them (B = 8, L = 2048, 4 heads of
-// 128 and 256: 66 us, with 64 columns 72; a single sequence of 512 34 and 30).  es: bytes of an element;
-// kwp: padded width of the keys.
-constexpr int lin_columns(int es, int kwp, int vw) { return es == 2 && kwp <= 128 && vw > 64 ? 128 : 64; }
+// Columns of v that a workgroup takes.  128 share the work on the keys, where the state's
+// two roundings leave LDS for them, at the price of half as many workgroups: they pay for
+// keys of more than 64 (padded: kwp) once a launch has as many such walks as CUs, or more
+// than two chunks of them a CU.  4 heads of 128 and 256, bf16, us with 128 and with 64
+// columns: B = 8, L = 2048 (2048 chunks) 64 and 70, B = 6, L = 1024 (768) 41 and 45, B = 8, L = 512
+// (512) 39 and 36, one sequence of 512 34 and 30; B = 32, L = 128 (256 walks) 16.6 and 18.0.  Keys
+// of 64 (8 heads of 64 and 128): B = 1, L = 512 31 and 22, B = 4, L = 2048 40 and 35, 16 heads,
+// B = 8, L = 2048 83 and 76.  es: bytes of an element.
+inline int lin_columns(int es, int kwp, int vw, int64_t walks, int64_t chunks) {
+  return es == 2 && kwp == 128 && vw > 64 && (walks >= 256 || chunks > 2 * 256) ? 128 : 64;
+}
 // Waves that keep the state: eight where one workgroup fills a CU (66 us at the size
 // above, with four 98), four where two share one.
 constexpr int lin_state_waves(int es, int kwp, int columns) { return es == 2 && kwp * columns >= 128 * 128 ? 8 : 4; }
