@@ -18,10 +18,11 @@
 // with those three at L = 16384, 8 / 2 heads of 128 and 256, window 4096 (a large
 // library product takes 1.2), 0.8 at B = 8, L = 2048, 16 / 4 heads of 128, window 512.
 //   Four waves, two workgroups a CU that take turns at the vector and the matrix
-// instructions (at the latter size 128 us; eight waves with a barrier in common 140,
-// units of 32 keys 137, three such workgroups a CU 125 and at 4096 keys of window 445
-// to 411; of 128 keys 240).  A wave that forms a tile's weights between the products of
-// the one before it takes 149: it waits for every LDS read of its own.
+// instructions.  At the latter size, and for two sequences of 4096 with 32 / 8 heads of
+// 128 and a window of 4096, that takes 122 and 416 us; with units of 32 keys 126 and 454, with
+// three such workgroups a CU 119 and 448.  When the former took 128: eight waves with a barrier
+// in common 140, units of 128 keys 240, and a wave that forms a tile's weights between the
+// products of the one before it 149: it waits for every LDS read of its own.
 #include "window_device.hpp"
 
 namespace msgla {
@@ -172,7 +173,8 @@ __global__ __launch_bounds__(64 * WIN_TILES, sizeof(T) == 4 && DVP == 256 ? 1 : 
     P.lse[((int64_t)b * P.Hq + row.head) * P.L + row.i] = live ? logf(l) - nref * BLK_LN2 : -__builtin_inff();
 }
 
-// Keys of a unit: as many as three stages of LDS leave room for.
+// Keys of a unit: 64 for bf16 values of up to 128, whose two stages leave LDS for two
+// workgroups a CU, and 32 elsewhere.
 template <typename T, int DKP, int DVP> void launch_t(const WinParams& P, hipStream_t st) {
   constexpr int KT = sizeof(T) == 2 && DVP <= 128 ? 64 : 32;
   const int64_t total = (int64_t)P.B * P.Hkv * P.tiles_per_seq;

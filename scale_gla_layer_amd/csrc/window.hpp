@@ -38,7 +38,7 @@ struct WinParams {
   float* sink_part;
 };
 
-constexpr int WIN_TILES = 4;   // tiles of a workgroup of the forward (one a wave) and of dq (one a pair of waves)
+constexpr int WIN_TILES = 4;   // tiles of a workgroup of the forward, one a wave
 // Pairs of waves of a workgroup of the gradients, each with a tile of 32 rows (dq) or
 // keys (dk and dv): four, or one where three stages of LDS leave no more room and a
 // wave needs more than 256 registers.  es: bytes of an element; dvp: padded width.

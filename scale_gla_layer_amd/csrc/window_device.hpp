@@ -35,30 +35,6 @@ template <typename T> __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, 
   }
 }
 
-// positions of a slab of a product over positions, and the values a lane gives to it
-template <typename T> constexpr int win_slab() { return 32 / (int)sizeof(T); }
-template <typename T> constexpr int win_vals() { return 16 / (int)sizeof(T); }
-
-// The B operand of slab s from a tile of results, as one or (bf16) two values each.
-template <typename T> __device__ __forceinline__ u32x4 win_pack(const f32x16& p, int s) {
-  constexpr int N = win_vals<T>();
-  float v[N];
-#pragma unroll
-  for (int e = 0; e < N; ++e) v[e] = p[N * s + e];
-  return pack16<T>(v);
-}
-template <typename T> __device__ __forceinline__ void win_split(const f32x16& p, int s, u32x4& hi, u32x4& lo) {
-  if constexpr (sizeof(T) == 2) {
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = p[8 * s + e];
-    split_bf16(v, hi, lo);
-  } else {
-    hi = win_pack<T>(p, s);
-    lo = zero16();
-  }
-}
-
 // Tiles of rows of W 16-byte pieces, piece p of row r at p ^ tile_key(r).
 // Slab s of rows 32 t + l % 32.
 template <int W> struct Rows32 {
