@@ -612,7 +612,7 @@ msgla_status msgla_block_attention_step(const msgla_block_config* cfg, const msg
  * Layer norm over the channels of every row:
  *     y = (x - mean) rstd weight + bias,   rstd = 1 / sqrt(mean of (x - mean)^2 + eps)
  *   width: channels, 1 .. 16384.  eps: 1e-20 .. 1.  dtype: of x, y and their gradients; statistics and
- *   sums are fp32, as are weight and bias.
+ *   the sums within a row are fp32, the sums over rows are formed in 64 bits; weight and bias are fp32.
  */
 typedef struct {
   int32_t width;

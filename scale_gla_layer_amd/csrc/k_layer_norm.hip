@@ -16,8 +16,8 @@
 // 64 bits and rounded to 32 where a lane's and a workgroup's are left for others: in 32
 // bits, equal gradients in each row put dbias off by 1.2e-6 at 32768 rows and by 1.7e-5
 // at 2^20 (fp32, D = 2048), now by at most 1.8e-7 at any number.
-//   HBM-bound: B = 8, L = 2048, D = 1024 in bf16 takes 16.3 us forward (67 MB, 4.1 TB/s)
-// and 21 + 4 for the gradient (101 MB); a copy reaches 5.1 TB/s.
+//   HBM-bound: B = 8, L = 2048, D = 1024 in bf16 takes 16.5 us forward (67 MB, 4.1 TB/s)
+// and 21.4 + 4.0 for the gradient (101 MB); a copy reaches 5.1 TB/s.
 #include <algorithm>
 
 #include "device_common.hpp"

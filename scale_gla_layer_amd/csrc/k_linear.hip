@@ -23,10 +23,12 @@
 // much as the output's own rounding.  Where the last state is wanted, which is fp32,
 // the decayed keys enter as three (with two it is off by 2.4e-6).  Sums are fp32.
 //   Bound by latency, between barriers, and vector instructions: B = 8, L = 2048, 4 heads
-// of 128 and 256, bf16 takes 21 us for the segments, 7 for their states and 43 for the
+// of 128 and 256, bf16 takes 19.0 us for the segments, 6.5 for their states and 37.8 for the
 // walk, whose workgroups' eight chunks have matrix instructions for 8 and LDS reads for
-// 15 (counted).  64 to 67 us a call; 89 with 32 x 32 tiles for both, which read half as
-// much from LDS and leave two waves a SIMD.  The gradient 154.
+// 15 (counted): 63.3 a call in a long run of calls (77 in the first of them; 89 for 66 with
+// 32 x 32 tiles for both, which read half as much from LDS and leave two waves a SIMD).  Its
+// gradient takes 153.  fp32 195 and 575: at a large product's rate the walk's matrix
+// instructions take 82 of its 138.
 //   The products' layouts chain without exchanges between lanes: A^T = K Q^T holds
 // a row's weights where out^T = V^T A^T wants them, and S as the sum of K^T V has
 // four neighbouring rows a lane, which is 8 bytes of the transposed state in LDS.

@@ -14,9 +14,10 @@
 // when that has grown by more than 8 in units of log 2 (weights stay below 2^8).
 //   bf16 weights enter their product as two bf16 values each (16 bits; rounded once
 // they put outputs 1.3 times as far off as the output's own rounding does), which
-// makes three products of the formula's two.  Bound by the matrix cores: 1.0 PFLOP/s
+// makes three products of the formula's two.  Bound by the matrix cores: 0.95 PFLOP/s
 // with those three at L = 16384, 8 / 2 heads of 128 and 256, window 4096 (a large
-// library product takes 1.2), 0.8 at B = 8, L = 2048, 16 / 4 heads of 128, window 512.
+// library product takes 1.2), 0.74 at B = 8, L = 2048, 16 / 4 heads of 128, window 512.
+// fp32: 0.10 of 0.154 at B = 4 of the latter (301 us).
 //   Four waves, two workgroups a CU that take turns at the vector and the matrix
 // instructions.  At the latter size, and for two sequences of 4096 with 32 / 8 heads of
 // 128 and a window of 4096, that takes 122 and 416 us; with units of 32 keys 126 and 454, with

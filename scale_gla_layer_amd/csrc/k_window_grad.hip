@@ -13,8 +13,10 @@
 //   Scores are formed as S = Q K^T, whose result is the operand of dV^T = dO^T P
 // and dK^T = Q^T dS.  bf16 weights and their gradients enter these as two bf16 values
 // each, as in the other kernels: six products.  2 x 16 / 4 heads of 128, 4096
-// positions, window 1024: 245 us in a long run of calls, 283 in a short one (a wave
-// that does it all 470, workgroups of one pair 393), first tokens 21, joining 5.
+// positions, window 1024: 235 us in a long run of calls, 283 in a short one (a wave
+// that does it all 470, workgroups of one pair 393), first tokens 21, joining 5.  fp32,
+// 2 x 2048, window 512: 343, 51 and 16; its instances of 128 values keep 4 or 5 registers
+// in scratch memory.
 #include "window_device.hpp"
 
 namespace msgla {
